@@ -1,4 +1,4 @@
-"""ctypes view of the C ABI in include/mimo_bwd_fwd.h.
+"""ctypes view of the C ABI in include/mimo_bwd_fwd.h and include/mamba_layer.h.
 
 Only argument marshalling lives here. The shared library is the in-tree
 build (``mamba_mimo_chunked_amd/_build/libmimo_bwd_fwd.so``); when it is
@@ -113,6 +113,123 @@ class MimoBwdBwdArgs(ctypes.Structure):
     ]
 
 
+class MambaRows(ctypes.Structure):
+    """Mirror of ``mamba_rows``."""
+
+    _fields_ = [
+        ("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+    ]
+
+
+class MambaConvFwdArgs(ctypes.Structure):
+    """Mirror of ``mamba_conv_fwd_args``."""
+
+    _fields_ = [
+        ("n", ctypes.c_int64), ("S", ctypes.c_int64), ("D", ctypes.c_int64), ("W", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("silu", ctypes.c_int32), ("zero_tail", ctypes.c_int32),
+        ("cu_seqlens", ctypes.c_void_p), ("x", MambaRows), ("weight", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p), ("initial_state", ctypes.c_void_p), ("out", ctypes.c_void_p),
+        ("state", ctypes.c_void_p),
+    ]
+
+
+class MambaConvBwdArgs(ctypes.Structure):
+    """Mirror of ``mamba_conv_bwd_args``."""
+
+    _fields_ = [
+        ("n", ctypes.c_int64), ("S", ctypes.c_int64), ("D", ctypes.c_int64), ("W", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("silu", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("cu_seqlens", ctypes.c_void_p), ("dout", MambaRows), ("x", MambaRows), ("weight", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p), ("initial_state", ctypes.c_void_p), ("dstate", ctypes.c_void_p),
+        ("dx", ctypes.c_void_p), ("dweight", ctypes.c_void_p), ("dbias", ctypes.c_void_p),
+        ("dinitial_state", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class MambaConvStepArgs(ctypes.Structure):
+    """Mirror of ``mamba_conv_step_args``."""
+
+    _fields_ = [
+        ("n", ctypes.c_int64), ("D", ctypes.c_int64), ("slots", ctypes.c_int64),
+        ("slot_stride", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("W", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("silu", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("x", ctypes.c_void_p), ("state", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p), ("indices", ctypes.c_void_p), ("out", ctypes.c_void_p),
+    ]
+
+
+class MambaScanFwdArgs(ctypes.Structure):
+    """Mirror of ``mamba_scan_fwd_args``."""
+
+    _fields_ = [
+        ("n", ctypes.c_int64), ("S", ctypes.c_int64), ("D", ctypes.c_int64), ("G", ctypes.c_int64),
+        ("N", ctypes.c_int64), ("dtype", ctypes.c_int32), ("dt_softplus", ctypes.c_int32),
+        ("zero_tail", ctypes.c_int32), ("reserved", ctypes.c_int32), ("cu_seqlens", ctypes.c_void_p),
+        ("u", MambaRows), ("dt", MambaRows), ("b", MambaRows), ("c", MambaRows), ("z", MambaRows),
+        ("a", ctypes.c_void_p), ("d", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p),
+        ("initial_state", ctypes.c_void_p), ("out", ctypes.c_void_p), ("state", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class MambaScanBwdArgs(ctypes.Structure):
+    """Mirror of ``mamba_scan_bwd_args``."""
+
+    _fields_ = [
+        ("n", ctypes.c_int64), ("S", ctypes.c_int64), ("D", ctypes.c_int64), ("G", ctypes.c_int64),
+        ("N", ctypes.c_int64), ("dtype", ctypes.c_int32), ("dt_softplus", ctypes.c_int32),
+        ("reserved0", ctypes.c_int32), ("reserved1", ctypes.c_int32), ("cu_seqlens", ctypes.c_void_p),
+        ("dout", MambaRows), ("u", MambaRows), ("dt", MambaRows), ("b", MambaRows), ("c", MambaRows),
+        ("z", MambaRows), ("a", ctypes.c_void_p), ("d", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p),
+        ("initial_state", ctypes.c_void_p), ("dstate", ctypes.c_void_p), ("du", ctypes.c_void_p),
+        ("ddt", ctypes.c_void_p), ("db", ctypes.c_void_p), ("dc", ctypes.c_void_p), ("dz", ctypes.c_void_p),
+        ("da", ctypes.c_void_p), ("dd", ctypes.c_void_p), ("ddt_bias", ctypes.c_void_p),
+        ("dinitial_state", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class MambaScanStepArgs(ctypes.Structure):
+    """Mirror of ``mamba_scan_step_args``."""
+
+    _fields_ = [
+        ("n", ctypes.c_int64), ("D", ctypes.c_int64), ("G", ctypes.c_int64), ("N", ctypes.c_int64),
+        ("slots", ctypes.c_int64), ("slot_stride", ctypes.c_int64), ("dtype", ctypes.c_int32),
+        ("dt_softplus", ctypes.c_int32), ("u", MambaRows), ("dt", MambaRows), ("b", MambaRows),
+        ("c", MambaRows), ("z", MambaRows), ("a", ctypes.c_void_p), ("d", ctypes.c_void_p),
+        ("dt_bias", ctypes.c_void_p), ("state", ctypes.c_void_p), ("indices", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+    ]
+
+
+class MambaNormFwdArgs(ctypes.Structure):
+    """Mirror of ``mamba_norm_fwd_args``."""
+
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("D", ctypes.c_int64), ("G", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+        ("z_stride", ctypes.c_int64), ("dtype", ctypes.c_int32), ("center", ctypes.c_int32),
+        ("gate_after", ctypes.c_int32), ("silu", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("reserved", ctypes.c_int32), ("x", ctypes.c_void_p), ("z", ctypes.c_void_p),
+        ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("out", ctypes.c_void_p),
+    ]
+
+
+class MambaNormBwdArgs(ctypes.Structure):
+    """Mirror of ``mamba_norm_bwd_args``."""
+
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("D", ctypes.c_int64), ("G", ctypes.c_int64),
+        ("dout_stride", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("center", ctypes.c_int32), ("gate_after", ctypes.c_int32),
+        ("silu", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32),
+        ("dout", ctypes.c_void_p), ("x", ctypes.c_void_p), ("z", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("dz", ctypes.c_void_p),
+        ("dweight", ctypes.c_void_p), ("dbias", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 DTYPE_BF16, DTYPE_FP16, DTYPE_FP32 = 0, 1, 2
 
 EXPORTED = ("mimo_bwd_fwd", "mimo_bwd_fwd_timed", "mimo_bwd_fwd_workspace_size", "mimo_fwd",
@@ -121,6 +238,13 @@ EXPORTED = ("mimo_bwd_fwd", "mimo_bwd_fwd_timed", "mimo_bwd_fwd_workspace_size",
             "mimo_siso_fwd", "mimo_siso_fwd_timed", "mimo_siso_fwd_workspace_size", "mimo_bwd_bwd",
             "mimo_bwd_bwd_timed", "mimo_bwd_bwd_workspace_size", "mimo_last_error", "mimo_abi_version",
             "mimo_bwd_fwd_noalloc")
+# the layer operators (include/mamba_layer.h): argument struct, and whether a workspace goes with it
+LAYER_CALLS = {
+    "mamba_conv_fwd": (MambaConvFwdArgs, False), "mamba_conv_bwd": (MambaConvBwdArgs, True),
+    "mamba_conv_step": (MambaConvStepArgs, False), "mamba_scan_fwd": (MambaScanFwdArgs, True),
+    "mamba_scan_bwd": (MambaScanBwdArgs, True), "mamba_scan_step": (MambaScanStepArgs, False),
+    "mamba_norm_fwd": (MambaNormFwdArgs, False), "mamba_norm_bwd": (MambaNormBwdArgs, True),
+}
 NOALLOC_SCRATCH_BYTES = 64 << 20
 TIMED_EVENTS = 5
 
@@ -175,6 +299,12 @@ def lib():
         L.mimo_bwd_bwd_timed.restype = ctypes.c_int
         L.mimo_bwd_bwd_workspace_size.argtypes = [bargp, szp]
         L.mimo_bwd_bwd_workspace_size.restype = ctypes.c_int
+        for name, (args, workspace) in LAYER_CALLS.items():
+            getattr(L, name).argtypes = [ctypes.POINTER(args), ctypes.c_void_p]
+            getattr(L, name).restype = ctypes.c_int
+            if workspace:
+                getattr(L, name + "_workspace_size").argtypes = [ctypes.POINTER(args), szp]
+                getattr(L, name + "_workspace_size").restype = ctypes.c_int
         L.mimo_last_error.argtypes = []
         L.mimo_last_error.restype = ctypes.c_char_p
         L.mimo_abi_version.argtypes = []

@@ -1,0 +1,488 @@
+// Short causal convolution over channels-last sequences: forward, backward, one token.
+//
+//   pre[t] = bias + sum_k w[k] e[t + k],  out = silu(pre) or pre,  e = (W - 1 rows of state, x)
+//   dpre = dout * silu'(pre);  dx[t] = sum_k w[k] dpre[t + W-1 - k];  dw[k] = sum_t dpre[t] e[t + k]
+//
+// A thread owns VEC neighbouring channels (16 bytes of a row) over one chunk of CH tokens and
+// slides the window through registers, so a token of x is read once and W - 1 rows more at each
+// chunk's start. The passes are bound by memory.
+#include "layer.hpp"
+
+namespace mimo {
+namespace layer {
+namespace {
+
+constexpr int UNROLL = 8;   // rows of loads in flight in a thread (forward)
+constexpr int UNROLL_B = 4; // backward: two streams, and the windows of both in registers
+
+struct ConvParams {
+    Seqs q;
+    int D, nvec, silu, zero_tail;
+    long items;                     // threads with work (forward), slots (backward)
+    Rows x, dout;
+    const float *w, *bias;
+    const void *init, *dstate;
+    void *out, *state, *dinit;      // out: also dx
+    float* part;                    // backward: [groups][W + 1][D]
+    float *dw, *db;
+    int groups;
+};
+
+template <int VEC, int W> struct Filter {
+    float w[W][VEC], bias[VEC];
+    __device__ __forceinline__ Filter(const float* pw, const float* pb, int d) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            bias[v] = pb ? pb[d + v] : 0.f;
+#pragma unroll
+            for (int k = 0; k < W; ++k) w[k][v] = pw[(long)(d + v) * W + k];
+        }
+    }
+};
+
+// row t of x, or of the state in front of it where t < 0
+template <int DT, int VEC, int W>
+__device__ __forceinline__ void row_before(const raw_t<DT>* x, long ts, const raw_t<DT>* init, long D, int t, float (&e)[VEC]) {
+    if (t >= 0) unpack<DT, VEC>(load<DT, VEC>(x + t * ts), e);
+    else if (init != nullptr) unpack<DT, VEC>(load<DT, VEC>(init + (t + W - 1) * D), e);
+    else {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) e[v] = 0.f;
+    }
+}
+
+template <int DT, int VEC, int W> __global__ __launch_bounds__(256) void k_conv_fwd(ConvParams p) {
+    typedef raw_t<DT> raw;
+    const long g = (long)blockIdx.x * 256 + threadIdx.x;
+    if (g >= p.items) return;
+    const int slot = (int)(g / p.nvec), d = (int)(g - (long)slot * p.nvec) * VEC;
+    const Place pl = place(p.q, slot);
+    if (!pl.ok) return;
+    const int t0 = pl.j * p.q.CH, t1 = min(t0 + p.q.CH, pl.len);
+    const long D = p.D;
+    raw* out = static_cast<raw*>(p.out) + ((long)(p.q.cu ? pl.row0 : pl.i * (long)p.q.S)) * D + d;
+    if (pl.i == p.q.n) {            // behind the last sequence
+        const float zero[VEC] = {};
+        if (p.zero_tail)
+            for (int t = t0; t < t1; ++t) store<DT, VEC>(out + t * D, zero);
+        return;
+    }
+    const raw* x = at<DT>(p.x, pl) + d;
+    const long ts = p.x.ts;
+    const raw* init = p.init ? static_cast<const raw*>(p.init) + (long)pl.i * (W - 1) * D + d : nullptr;
+    const Filter<VEC, W> f(p.w, p.bias, d);
+    float e[W - 1 + UNROLL][VEC];
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) row_before<DT, VEC, W>(x, ts, init, D, t0 - (W - 1) + k, e[k]);
+    for (int t = t0; t < t1; t += UNROLL) {
+        Pack<DT, VEC> r[UNROLL];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) r[u] = load<DT, VEC>(x + (long)min(t + u, t1 - 1) * ts);
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) unpack<DT, VEC>(r[u], e[W - 1 + u]);
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            float y[VEC];
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                float s = f.bias[v];
+#pragma unroll
+                for (int k = 0; k < W; ++k) s = __builtin_fmaf(f.w[k][v], e[u + k][v], s);
+                y[v] = p.silu ? s * sigmoid(s) : s;
+            }
+            if (t + u < t1) store<DT, VEC>(out + (long)(t + u) * D, y);
+        }
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) e[k][v] = e[UNROLL + k][v];
+    }
+    if (p.state != nullptr && t1 == pl.len) {
+        raw* state = static_cast<raw*>(p.state) + (long)pl.i * (W - 1) * D + d;
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) {
+            float s[VEC];
+            row_before<DT, VEC, W>(x, ts, init, D, pl.len - (W - 1) + k, s);
+            store<DT, VEC>(state + k * D, s);
+        }
+    }
+}
+
+// Backward. A block takes TY slots by TX channel vectors. A thread walks s over its chunk and W - 1
+// tokens more: dpre[s] from the window of x, then dx[s - (W-1)] from the window of dpre. In a
+// sequence's first chunk the rows in front of token 0 are those of the state. The sums for dw and
+// db stay in registers, are joined over the TY slots in LDS and leave one partial row for each block,
+// which k_conv_sums adds up in order (no atomics).
+template <int DT, int VEC, int W, int TX> __global__ __launch_bounds__(256) void k_conv_bwd(ConvParams p) {
+    typedef raw_t<DT> raw;
+    constexpr int TY = 256 / TX;
+    __shared__ float s_sum[TY][TX * VEC];
+    const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
+    const int vec = blockIdx.y * TX + tx, d = vec * VEC;
+    const long slot = (long)blockIdx.x * TY + ty, D = p.D;
+    float acc[W + 1][VEC] = {};
+    Place pl = {};
+    if (slot < p.items && vec < p.nvec) pl = place(p.q, (int)slot);
+    if (pl.ok) {
+        const int t0 = pl.j * p.q.CH, t1 = min(t0 + p.q.CH, pl.len);
+        raw* dx = static_cast<raw*>(p.out) + ((long)(p.q.cu ? pl.row0 : pl.i * (long)p.q.S)) * D + d;
+        if (pl.i == p.q.n) {
+            const float zero[VEC] = {};
+            for (int t = t0; t < t1; ++t) store<DT, VEC>(dx + t * D, zero);
+        } else {
+            const raw* x = at<DT>(p.x, pl) + d;
+            const raw* dout = at<DT>(p.dout, pl) + d;
+            const long xs = p.x.ts, gs = p.dout.ts, sd = (long)pl.i * (W - 1) * D + d;
+            const raw* init = p.init ? static_cast<const raw*>(p.init) + sd : nullptr;
+            const raw* dstate = p.dstate ? static_cast<const raw*>(p.dstate) + sd : nullptr;
+            raw* dinit = p.dinit ? static_cast<raw*>(p.dinit) + sd : nullptr;
+            const Filter<VEC, W> f(p.w, p.bias, d);
+            float e[W - 1 + UNROLL_B][VEC], g[W - 1 + UNROLL_B][VEC];
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) {
+                row_before<DT, VEC, W>(x, xs, init, D, t0 - (W - 1) + k, e[k]);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) g[k][v] = 0.f;
+            }
+            const int s1 = t1 + W - 1;   // dx up to t1 - 1
+            for (int s = t0; s < s1; s += UNROLL_B) {
+                Pack<DT, VEC> rx[UNROLL_B], rg[UNROLL_B];
+#pragma unroll
+                for (int u = 0; u < UNROLL_B; ++u) {
+                    const long t = max(min(min(s + u, s1 - 1), pl.len - 1), 0);
+                    if (pl.len > 0) {
+                        rx[u] = load<DT, VEC>(x + t * xs);
+                        rg[u] = load<DT, VEC>(dout + t * gs);
+                    } else {
+                        rx[u] = Pack<DT, VEC>{};
+                        rg[u] = Pack<DT, VEC>{};
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < UNROLL_B; ++u) {
+                    unpack<DT, VEC>(rx[u], e[W - 1 + u]);
+                    float dy[VEC];
+                    unpack<DT, VEC>(rg[u], dy);
+                    const bool in = s + u < pl.len, mine = s + u < t1;
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) {
+                        float dp = dy[v];
+                        if (p.silu) {
+                            float pre = f.bias[v];
+#pragma unroll
+                            for (int k = 0; k < W; ++k) pre = __builtin_fmaf(f.w[k][v], e[u + k][v], pre);
+                            dp *= silu_slope(pre, sigmoid(pre));
+                        }
+                        dp = in ? dp : 0.f;
+                        g[W - 1 + u][v] = dp;
+                        if (mine) {
+#pragma unroll
+                            for (int k = 0; k < W; ++k) acc[k][v] = __builtin_fmaf(dp, e[u + k][v], acc[k][v]);
+                            acc[W][v] += dp;
+                        }
+                    }
+                    const int t = s + u - (W - 1);
+                    if (s + u < s1 && (t >= t0 || pl.j == 0)) {
+                        float r[VEC];
+#pragma unroll
+                        for (int v = 0; v < VEC; ++v) {
+                            r[v] = 0.f;
+#pragma unroll
+                            for (int k = 0; k < W; ++k) r[v] = __builtin_fmaf(f.w[k][v], g[u + W - 1 - k][v], r[v]);
+                        }
+                        const int k = t - (pl.len - (W - 1));   // this row's place in the last state
+                        if (dstate != nullptr && k >= 0) {
+                            float a[VEC];
+                            unpack<DT, VEC>(load<DT, VEC>(dstate + k * D), a);
+#pragma unroll
+                            for (int v = 0; v < VEC; ++v) r[v] += a[v];
+                        }
+                        if (t >= 0) store<DT, VEC>(dx + t * D, r);
+                        else if (dinit != nullptr) store<DT, VEC>(dinit + (t + W - 1) * D, r);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) {
+                        e[k][v] = e[UNROLL_B + k][v];
+                        g[k][v] = g[UNROLL_B + k][v];
+                    }
+            }
+        }
+    }
+    float* part = p.part + (long)blockIdx.x * (W + 1) * D;
+#pragma unroll
+    for (int k = 0; k <= W; ++k) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) s_sum[ty][tx * VEC + v] = acc[k][v];
+        __syncthreads();
+        for (int c = threadIdx.x; c < TX * VEC; c += 256) {
+            float s = 0.f;
+#pragma unroll
+            for (int y = 0; y < TY; ++y) s += s_sum[y][c];
+            const long col = (long)blockIdx.y * TX * VEC + c;
+            if (col < D) part[k * D + col] = s;
+        }
+        __syncthreads();
+    }
+}
+
+template <int W> __global__ __launch_bounds__(256) void k_conv_sums(ConvParams p) {
+    const long D = p.D;
+    column_sums(p.part, (W + 1) * D, p.groups, (long)blockIdx.x * 64, (W + 1) * D, [&](long col, float s) {
+        const int k = (int)(col / D);
+        const long d = col - k * D;
+        if (k < W) p.dw[d * W + k] = s;
+        else if (p.db != nullptr) p.db[d] = s;
+    });
+}
+
+struct StepParams {
+    int n, D, slots, silu;
+    long slot_stride, x_stride;
+    const void* x;
+    void *state, *out;
+    const float *w, *bias;
+    const int* idx;
+};
+
+// One token: a thread takes VEC channels of a row (blockIdx.y), reads its state row and x, writes
+// both back shifted. Rows of one slot are taken by the first of them, in order.
+template <int DT, int VEC, int W> __global__ __launch_bounds__(256) void k_conv_step(StepParams p) {
+    typedef raw_t<DT> raw;
+    int row = blockIdx.y;
+    const int vec = blockIdx.x * 256 + threadIdx.x, d = vec * VEC;
+    const bool act = d < p.D;
+    const long D = p.D;
+    const int slot = p.idx ? p.idx[row] : row;
+    raw* out = static_cast<raw*>(p.out) + d;
+    if (slot < 0 || slot >= p.slots) {
+        const float zero[VEC] = {};
+        if (act) store<DT, VEC>(out + row * D, zero);
+        return;
+    }
+    raw* state = static_cast<raw*>(p.state) + slot * p.slot_stride + d;
+    float e[W][VEC] = {};
+    const Filter<VEC, W> f(p.w, p.bias, act ? d : 0);
+    if (act) {
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) unpack<DT, VEC>(load<DT, VEC>(state + k * D), e[k]);
+    }
+    if (p.idx && !first_of(p.idx, row, slot)) return;
+    for (;;) {
+        if (act) {
+            unpack<DT, VEC>(load<DT, VEC>(static_cast<const raw*>(p.x) + row * p.x_stride + d), e[W - 1]);
+            float y[VEC];
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                float s = f.bias[v];
+#pragma unroll
+                for (int k = 0; k < W; ++k) s = __builtin_fmaf(f.w[k][v], e[k][v], s);
+                y[v] = p.silu ? s * sigmoid(s) : s;
+            }
+            store<DT, VEC>(out + row * D, y);
+        }
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) e[k][v] = e[k + 1][v];
+        row = p.idx ? next_of(p.idx, row, p.n, slot) : p.n;
+        if (row >= p.n) break;
+    }
+    if (act) {
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) store<DT, VEC>(state + k * D, e[k]);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+// tokens of a chunk: as few threads as still fill the GPU (about 512 a CU in each pass), 16 to 64 tokens
+int chunk_tokens(int64_t n, int64_t S, bool packed, int64_t nvec) {
+    const int64_t T = packed ? S : n * S;
+    int64_t c = T * nvec / (256 * 512);
+    c = c < 16 ? 16 : c > 64 ? 64 : c / 8 * 8;
+    return (int)c;
+}
+
+Seqs make_seqs(int64_t n, int64_t S, const int32_t* cu, int CH) {
+    return Seqs{cu, (int)n, (int)S, CH, (int)((S + CH - 1) / CH)};
+}
+
+mimo_status check_filter(int32_t W, const float* w) {
+    if (W < MAMBA_CONV_MIN_TAPS || W > MAMBA_CONV_MAX_TAPS) return unsupported("the filter must have 2 to 8 taps");
+    if (w == nullptr) return bad("weight must not be NULL");
+    return MIMO_OK;
+}
+
+// channels of a thread: 16 bytes of a row where every row allows it (filters beyond four taps: 8
+// bytes of 16-bit types, for the registers of their windows), else one
+int vec_of(int dtype, int W, int64_t D, bool even) {
+    const int v = dtype == F32 ? 4 : W <= 4 ? 8 : 4;
+    return even && D % v == 0 ? v : 1;
+}
+
+template <int DT, int W, class F> mimo_status with_vec(int vec, F f) {
+    constexpr int V = DT == F32 ? 4 : W <= 4 ? 8 : 4;
+    if (vec == V) return f.template operator()<DT, V, W>();
+    return f.template operator()<DT, 1, W>();
+}
+template <int DT, class F> mimo_status with_taps(int W, int vec, F f) {
+    switch (W) {
+        case 2: return with_vec<DT, 2>(vec, f);
+        case 3: return with_vec<DT, 3>(vec, f);
+        case 4: return with_vec<DT, 4>(vec, f);
+        case 5: return with_vec<DT, 5>(vec, f);
+        case 6: return with_vec<DT, 6>(vec, f);
+        case 7: return with_vec<DT, 7>(vec, f);
+        default: return with_vec<DT, 8>(vec, f);
+    }
+}
+template <class F> mimo_status dispatch(int dtype, int W, int vec, F f) {
+    if (dtype == BF16) return with_taps<BF16>(W, vec, f);
+    if (dtype == F16) return with_taps<F16>(W, vec, f);
+    return with_taps<F32>(W, vec, f);
+}
+
+struct FwdRun {
+    ConvParams p;
+    hipStream_t st;
+    template <int DT, int VEC, int W> mimo_status operator()() {
+        return launch(&k_conv_fwd<DT, VEC, W>, dim3((unsigned)((p.items + 255) / 256)), 256, 0, st, p);
+    }
+};
+struct BwdRun {
+    ConvParams p;
+    hipStream_t st;
+    template <int DT, int VEC, int W> mimo_status operator()() {
+        constexpr int TX = VEC == 1 ? 64 : 32;
+        mimo_status s = launch(&k_conv_bwd<DT, VEC, W, TX>, dim3(p.groups, (p.nvec + TX - 1) / TX), 256, 0, st, p);
+        if (s != MIMO_OK) return s;
+        return launch(&k_conv_sums<W>, dim3((unsigned)(((W + 1) * (long)p.D + 63) / 64)), 256, 0, st, p);
+    }
+};
+struct StepRun {
+    StepParams p;
+    hipStream_t st;
+    template <int DT, int VEC, int W> mimo_status operator()() {
+        const int nvec = p.D / VEC;
+        return launch(&k_conv_step<DT, VEC, W>, dim3((nvec + 255) / 256, p.n), 256, 0, st, p);
+    }
+};
+
+struct BwdPlan {
+    int vec, CH, groups;
+    size_t bytes;
+};
+mimo_status plan_bwd(const mamba_conv_bwd_args* a, BwdPlan* pl) {
+    if (a == nullptr) return bad("args must not be NULL");
+    mimo_status s = check_sequences(a->n, a->S, a->D, a->dtype);
+    if (s != MIMO_OK) return s;
+    if (a->W < MAMBA_CONV_MIN_TAPS || a->W > MAMBA_CONV_MAX_TAPS) return unsupported("the filter must have 2 to 8 taps");
+    const int esz = a->dtype == F32 ? 4 : 2;
+    bool even = aligned(a->x.data, a->x.batch_stride, a->x.token_stride, 16, esz) &&
+                aligned(a->dout.data, a->dout.batch_stride, a->dout.token_stride, 16, esz);
+    for (const void* x : {a->initial_state, a->dstate, (const void*)a->dx, (const void*)a->dinitial_state}) even = even && aligned(x, 0, 0, 16, 1);
+    pl->vec = vec_of(a->dtype, a->W, a->D, even);
+    const bool packed = a->cu_seqlens != nullptr;
+    pl->CH = chunk_tokens(a->n, a->S, packed, a->D / pl->vec);
+    const Seqs q = make_seqs(a->n, a->S, a->cu_seqlens, pl->CH);
+    const int TY = pl->vec == 1 ? 4 : 8;
+    const long groups = (slots_of(q) + TY - 1) / TY;
+    if (slots_of(q) > (long)1 << 30) return unsupported("too many tokens");
+    pl->groups = (int)groups;
+    pl->bytes = up256((size_t)groups * (a->W + 1) * a->D * sizeof(float));
+    return MIMO_OK;
+}
+
+}  // namespace
+}  // namespace layer
+}  // namespace mimo
+
+using namespace mimo;
+using namespace mimo::layer;
+
+extern "C" {
+
+mimo_status mamba_conv_fwd(const mamba_conv_fwd_args* a, void* stream) {
+    if (a == nullptr) return bad("args must not be NULL");
+    mimo_status s = check_sequences(a->n, a->S, a->D, a->dtype);
+    if (s != MIMO_OK || (s = check_filter(a->W, a->weight)) != MIMO_OK) return s;
+    if (!a->x.data || !a->out) return bad("x and out must not be NULL");
+    const int esz = a->dtype == F32 ? 4 : 2;
+    bool even = aligned(a->x.data, a->x.batch_stride, a->x.token_stride, 16, esz);
+    for (const void* x : {a->initial_state, (const void*)a->out, (const void*)a->state}) even = even && aligned(x, 0, 0, 16, 1);
+    const int vec = vec_of(a->dtype, a->W, a->D, even);
+    const bool packed = a->cu_seqlens != nullptr;
+    ConvParams p{};
+    p.D = (int)a->D;
+    p.nvec = p.D / vec;
+    p.q = make_seqs(a->n, a->S, a->cu_seqlens, chunk_tokens(a->n, a->S, packed, p.nvec));
+    p.items = slots_of(p.q) * p.nvec;
+    if (slots_of(p.q) > (long)1 << 30 || p.items > (long)1 << 38) return unsupported("too many tokens");
+    p.silu = a->silu;
+    p.zero_tail = a->zero_tail;
+    p.x = rows_of(a->x, packed);
+    p.w = a->weight;
+    p.bias = a->bias;
+    p.init = a->initial_state;
+    p.out = a->out;
+    p.state = a->state;
+    if ((s = require_gfx950()) != MIMO_OK) return s;
+    return dispatch(a->dtype, a->W, vec, FwdRun{p, static_cast<hipStream_t>(stream)});
+}
+
+mimo_status mamba_conv_bwd_workspace_size(const mamba_conv_bwd_args* a, size_t* bytes) {
+    BwdPlan pl;
+    const mimo_status s = plan_bwd(a, &pl);
+    if (s != MIMO_OK) return s;
+    if (bytes == nullptr) return bad("bytes must not be NULL");
+    *bytes = pl.bytes;
+    return MIMO_OK;
+}
+
+mimo_status mamba_conv_bwd(const mamba_conv_bwd_args* a, void* stream) {
+    BwdPlan pl;
+    mimo_status s = plan_bwd(a, &pl);
+    if (s != MIMO_OK || (s = check_filter(a->W, a->weight)) != MIMO_OK) return s;
+    if (!a->x.data || !a->dout.data || !a->dx || !a->dweight) return bad("dout, x, dx and dweight must not be NULL");
+    if ((s = check_workspace(a->workspace, a->workspace_bytes, pl.bytes)) != MIMO_OK) return s;
+    const bool packed = a->cu_seqlens != nullptr;
+    ConvParams p{};
+    p.D = (int)a->D;
+    p.nvec = p.D / pl.vec;
+    p.q = make_seqs(a->n, a->S, a->cu_seqlens, pl.CH);
+    p.items = slots_of(p.q);
+    p.groups = pl.groups;
+    p.silu = a->silu;
+    p.x = rows_of(a->x, packed);
+    p.dout = rows_of(a->dout, packed);
+    p.w = a->weight;
+    p.bias = a->bias;
+    p.init = a->initial_state;
+    p.dstate = a->dstate;
+    p.out = a->dx;
+    p.dinit = a->dinitial_state;
+    p.part = static_cast<float*>(a->workspace);
+    p.dw = a->dweight;
+    p.db = a->dbias;
+    if ((s = require_gfx950()) != MIMO_OK) return s;
+    return dispatch(a->dtype, a->W, pl.vec, BwdRun{p, static_cast<hipStream_t>(stream)});
+}
+
+mimo_status mamba_conv_step(const mamba_conv_step_args* a, void* stream) {
+    if (a == nullptr) return bad("args must not be NULL");
+    mimo_status s = check_sequences(a->n, 1, a->D, a->dtype);
+    if (s != MIMO_OK || (s = check_filter(a->W, a->weight)) != MIMO_OK) return s;
+    if (!a->x || !a->out || !a->state) return bad("x, state and out must not be NULL");
+    if (a->slots < 1 || a->slots > (int64_t)1 << 30) return bad("slots must be in [1, 2^30]");
+    if (!a->indices && a->slots < a->n) return bad("without indices the state needs a slot for each row");
+    const int esz = a->dtype == F32 ? 4 : 2;
+    const bool even = aligned(a->x, a->x_stride, 0, 16, esz) && aligned(a->state, a->slot_stride, 0, 16, esz) && aligned(a->out, 0, 0, 16, 1);
+    const StepParams p{(int)a->n, (int)a->D, (int)a->slots, a->silu, (long)a->slot_stride, (long)a->x_stride, a->x, a->state, a->out,
+                       a->weight, a->bias, a->indices};
+    if ((s = require_gfx950()) != MIMO_OK) return s;
+    return dispatch(a->dtype, a->W, vec_of(a->dtype, a->W, a->D, even), StepRun{p, static_cast<hipStream_t>(stream)});
+}
+
+}  // extern "C"

@@ -162,6 +162,11 @@ __global__ __launch_bounds__(256) void k_finish(Params p) {
 
 }  // namespace mimo
 
+namespace mimo {
+mimo_status set_error(mimo_status s, const char* msg);
+mimo_status require_gfx950();
+}  // namespace mimo
+
 namespace {
 
 using namespace mimo;
@@ -1023,6 +1028,10 @@ mimo_status scratch_on_current_device(void** ptr) {
 }
 
 }  // namespace
+
+// for the layer operators (layer_*.hip)
+mimo_status mimo::set_error(mimo_status s, const char* msg) { return fail(s, "%s", msg); }
+mimo_status mimo::require_gfx950() { return check_device(); }
 
 extern "C" {
 

@@ -1,0 +1,458 @@
+"""The layer operators around the scan: the short causal convolution ``mamba_conv_*``, the selective
+scan ``mamba_scan_*`` with a decay for each channel and state, and the gated group norm
+``mamba_norm_*``, each as a forward call, a backward call that returns the gradients, and (where there
+is a state) a step of one token.
+
+Data tensors share one dtype: bfloat16, float16 or float32. Parameters, the scan's state and their
+gradients are float32; so is all arithmetic, rounded once when stored. Sequences are a dense batch
+[B, S, ...] or packed along one token axis [T, ...] with ``cu_seqlens`` [n + 1] (int32, on the device:
+0, then each sequence's end, not decreasing, at most T; its values are not checked, and sequences may
+be empty). Token and batch strides are free as long as the inner axes are dense; other layouts are
+copied. Calls are asynchronous on the current HIP stream of the tensors' device. Sums run in a fixed
+order: equal inputs give equal bits.
+"""
+
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import _lib
+from .api import _BWD2_DTYPES as _DTYPES
+from .api import _aligned, _check_output, _check_tensor, _is_gfx950, _raise, _workspace
+
+__all__ = ["MambaConvOutputs", "MambaConvGrads", "MambaScanOutputs", "MambaScanGrads", "MambaNormGrads", "mamba_conv_fwd",
+           "mamba_conv_bwd", "mamba_conv_step", "mamba_scan_fwd", "mamba_scan_bwd", "mamba_scan_step", "mamba_norm_fwd",
+           "mamba_norm_bwd"]
+
+Tensor = torch.Tensor
+_F32 = torch.float32
+
+
+class MambaConvOutputs(NamedTuple):
+    out: Tensor
+    state: Optional[Tensor]
+
+
+class MambaConvGrads(NamedTuple):
+    dx: Tensor
+    dweight: Tensor
+    dbias: Optional[Tensor]
+    dinitial_state: Optional[Tensor]
+
+
+class MambaScanOutputs(NamedTuple):
+    out: Tensor
+    state: Optional[Tensor]
+
+
+class MambaScanGrads(NamedTuple):
+    du: Tensor
+    ddt: Tensor
+    da: Tensor
+    db: Tensor
+    dc: Tensor
+    dd: Optional[Tensor]
+    dz: Optional[Tensor]
+    ddt_bias: Optional[Tensor]
+    dinitial_state: Optional[Tensor]
+
+
+class MambaNormGrads(NamedTuple):
+    dx: Tensor
+    dweight: Tensor
+    dbias: Optional[Tensor]
+    dz: Optional[Tensor]
+
+
+# ---------------------------------------------------------------- checks
+def _data_dtype(name, x):
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"{name} must use torch.bfloat16, torch.float16 or torch.float32, got {x.dtype}")
+    return _DTYPES[x.dtype]
+
+
+def _device(what, name, x):
+    """The device of the first tensor; every other one has to be there too."""
+    if x.device.type != "cuda":
+        raise ValueError(f"{what} requires GPU (HIP) tensors, got {name} on {x.device}")
+    if not _is_gfx950(x.device.index if x.device.index is not None else torch.cuda.current_device()):
+        raise NotImplementedError(f"{what} supports gfx950 (MI355X) devices only")
+    return x.device
+
+
+def _sequences(name, x, cu_seqlens, inner):
+    """(n, S, leading shape): a dense batch [B, S, ...] or, with cu_seqlens, tokens [T, ...]."""
+    if cu_seqlens is None:
+        if x.dim() != 2 + inner:
+            raise ValueError(f"{name} must have {2 + inner} axes (batch, tokens, ...), got shape {list(x.shape)}")
+        n, S = int(x.shape[0]), int(x.shape[1])
+        lead = (n, S)
+    else:
+        if x.dim() != 1 + inner:
+            raise ValueError(f"{name} must have {1 + inner} axes (tokens, ...) with cu_seqlens, got shape {list(x.shape)}")
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+            raise ValueError("cu_seqlens must have shape [n + 1] with at least one sequence")
+        n, S = int(cu_seqlens.shape[0]) - 1, int(x.shape[0])
+        lead = (S,)
+    if min(n, S) < 1 or x.numel() == 0:
+        raise ValueError(f"{name} must not be empty, got shape {list(x.shape)}")
+    return n, S, lead
+
+
+def _cu(cu_seqlens, device):
+    if cu_seqlens is None:
+        return None
+    _check_tensor("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, device)
+    return cu_seqlens.contiguous()
+
+
+def _check(table, dtype, device):
+    """(name, tensor or None, shape, dtype or None for the data dtype) of every tensor."""
+    for name, x, shape, dt in table:
+        if x is not None:
+            _check_tensor(name, x, shape, dt or dtype, device)
+
+
+def _dense_inner(x, inner):
+    """x as it is if its last ``inner`` axes are dense, else a contiguous copy."""
+    step = 1
+    for k in range(1, inner + 1):
+        if x.shape[-k] != 1 and x.stride(-k) != step:
+            return x.contiguous()
+        step *= x.shape[-k]
+    return x
+
+
+def _rows(x, packed):
+    """The mamba_rows view of a tensor whose inner axes are dense (None: no tensor)."""
+    if x is None:
+        return _lib.MambaRows(None, 0, 0)
+    return _lib.MambaRows(x.data_ptr(), 0 if packed else x.stride(0), x.stride(0 if packed else 1))
+
+
+def _ptr(x):
+    return None if x is None else x.data_ptr()
+
+
+def _span(x):
+    """First and last byte (exclusive) that a tensor's elements lie in."""
+    last = sum((s - 1) * st for s, st in zip(x.shape, x.stride()))
+    return x.data_ptr(), x.data_ptr() + (last + 1) * x.element_size()
+
+
+def _apart(name, x, others):
+    """A caller's output must not lie over an input."""
+    lo, hi = _span(x)
+    for other, y in others:
+        if y is not None and y.numel() and y.device == x.device:
+            a, b = _span(y)
+            if lo < b and a < hi:
+                raise ValueError(f"{name} must not overlap {other}")
+
+
+def _out(out, shape, dtype, device, inputs):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check_output("out", out, shape, dtype, device)
+    _apart("out", out, inputs)
+    return out
+
+
+def _call(fn, args, device, workspace=None):
+    """Queue one library call on the device's current stream, with its workspace where it has one."""
+    L = _lib.lib()
+    if _lib.LAYER_CALLS[fn][1]:
+        need = ctypes.c_size_t(0)
+        st = getattr(L, fn + "_workspace_size")(ctypes.byref(args), ctypes.byref(need))
+        if st != _lib.MIMO_OK:
+            _raise(st)
+        workspace = _workspace(workspace, need.value, device)
+        if workspace is not None:
+            args.workspace, args.workspace_bytes = workspace.data_ptr(), workspace.numel()
+    with torch.cuda.device(device):
+        st = getattr(L, fn)(ctypes.byref(args), torch.cuda.current_stream(device).cuda_stream)
+    if st != _lib.MIMO_OK:
+        _raise(st)
+
+
+# ---------------------------------------------------------------- short causal convolution
+def _activation(activation):
+    if activation not in (None, "silu"):
+        raise ValueError("activation must be None or 'silu'")
+    return int(activation == "silu")
+
+
+def _check_filter(weight, bias, D, device):
+    if weight.dim() != 2 or weight.shape[0] != D:
+        raise ValueError(f"weight must have shape [{D}, taps], got {list(weight.shape)}")
+    _check([("weight", weight, weight.shape, _F32), ("bias", bias, (D,), _F32)], None, device)
+    W = int(weight.shape[1])
+    if not 2 <= W <= 8:
+        raise NotImplementedError(f"mamba_conv supports 2 to 8 taps, got {W}")
+    return W
+
+
+def mamba_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, *, activation: Optional[str] = None,
+                   return_state: bool = False, out: Optional[Tensor] = None) -> MambaConvOutputs:
+    """Short causal convolution, one filter of W = 2..8 taps per channel: with e the sequence behind its
+    W - 1 rows of state (zeros without ``initial_state``), ``out[t] = act(bias + sum_k weight[:, k] e[t + k])``,
+    act the identity or SiLU.
+
+    x, out [B, S, D] or packed [T, D]; weight [D, W] and bias [D] float32; initial_state and the returned
+    ``state`` (with ``return_state``; the last W - 1 rows of e) [n, W - 1, D] in x's dtype, newest last, as
+    ``mamba_conv_step`` takes them. Tokens behind the last sequence: rows of ``out`` are left as they
+    were when the caller gives it, else zero."""
+    dev = _device("mamba_conv_fwd", "x", x)
+    code = _data_dtype("x", x)
+    silu = _activation(activation)
+    n, S, lead = _sequences("x", x, cu_seqlens, 1)
+    D = int(x.shape[-1])
+    W = _check_filter(weight, bias, D, dev)
+    _check([("initial_state", initial_state, (n, W - 1, D), None)], x.dtype, dev)
+    cu, x = _cu(cu_seqlens, dev), _dense_inner(x, 1)
+    weight, bias, initial_state = _aligned(weight), _aligned(bias), _aligned(initial_state)
+    res = _out(out, (*lead, D), x.dtype, dev, (("x", x), ("initial_state", initial_state)))
+    state = torch.empty((n, W - 1, D), dtype=x.dtype, device=dev) if return_state else None
+    a = _lib.MambaConvFwdArgs(n, S, D, W, code, silu, int(out is None), _ptr(cu), _rows(x, cu is not None), _ptr(weight),
+                              _ptr(bias), _ptr(initial_state), _ptr(res), _ptr(state))
+    _call("mamba_conv_fwd", a, dev)
+    return MambaConvOutputs(res, state)
+
+
+def mamba_conv_bwd(dout, x, weight, bias=None, initial_state=None, dstate=None, cu_seqlens=None, *,
+                   activation: Optional[str] = None, workspace: Optional[Tensor] = None) -> MambaConvGrads:
+    """Gradients of ``sum(out * dout) + sum(state * dstate)`` for the arguments of ``mamba_conv_fwd``: dx and
+    dinitial_state in x's dtype, dweight and dbias float32; dbias and dinitial_state are None without the
+    input. dout like x, dstate like initial_state. dx is zero behind the last sequence."""
+    dev = _device("mamba_conv_bwd", "x", x)
+    code = _data_dtype("x", x)
+    silu = _activation(activation)
+    n, S, lead = _sequences("x", x, cu_seqlens, 1)
+    D = int(x.shape[-1])
+    W = _check_filter(weight, bias, D, dev)
+    _check([("dout", dout, x.shape, None), ("initial_state", initial_state, (n, W - 1, D), None),
+            ("dstate", dstate, (n, W - 1, D), None)], x.dtype, dev)
+    cu, x, dout = _cu(cu_seqlens, dev), _dense_inner(x, 1), _dense_inner(dout, 1)
+    weight, bias, initial_state, dstate = (_aligned(t) for t in (weight, bias, initial_state, dstate))
+    dx = torch.empty((*lead, D), dtype=x.dtype, device=dev)
+    dweight = torch.empty((D, W), dtype=_F32, device=dev)
+    dbias = None if bias is None else torch.empty((D,), dtype=_F32, device=dev)
+    dinit = None if initial_state is None else torch.empty((n, W - 1, D), dtype=x.dtype, device=dev)
+    packed = cu is not None
+    a = _lib.MambaConvBwdArgs(n, S, D, W, code, silu, 0, _ptr(cu), _rows(dout, packed), _rows(x, packed), _ptr(weight), _ptr(bias),
+                              _ptr(initial_state), _ptr(dstate), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(dinit))
+    _call("mamba_conv_bwd", a, dev, workspace)
+    return MambaConvGrads(dx, dweight, dbias, dinit)
+
+
+def _check_pool(state, inner, dtype, indices, n, device):
+    """A pool of states [slots, ...]: dense inside a slot, slots that do not overlap, updated in place."""
+    if state.dim() != 1 + len(inner) or tuple(state.shape[1:]) != tuple(inner):
+        raise ValueError(f"state must have shape [slots, {', '.join(map(str, inner))}], got {list(state.shape)}")
+    _check_tensor("state", state, state.shape, dtype, device)
+    size = 1
+    for k in (-1, -2):
+        if state.shape[k] != 1 and state.stride(k) != size:
+            raise ValueError("state must be dense inside a slot: it is updated in place")
+        size *= int(state.shape[k])
+    slots = int(state.shape[0])
+    if slots < 1:
+        raise ValueError("state must have at least one slot")
+    if slots > 1 and state.stride(0) < size:
+        raise ValueError("the slots of state must not overlap")
+    if indices is None:
+        if slots < n:
+            raise ValueError(f"state has {slots} slots for {n} rows: without state_indices each row needs its own")
+    else:
+        _check_tensor("state_indices", indices, (n,), torch.int32, device)
+        indices = indices.contiguous()
+    return slots, state.stride(0) if slots > 1 else size, indices
+
+
+def mamba_conv_step(x, state, weight, bias=None, state_indices=None, *, activation: Optional[str] = None,
+                    out: Optional[Tensor] = None) -> Tensor:
+    """One token of ``mamba_conv_fwd`` for each of n rows: x, out [n, D]; ``state`` [slots, W - 1, D] in x's
+    dtype is updated in place. Row i uses slot ``state_indices[i]`` (int32; i without it). A row whose index
+    is outside [0, slots) is skipped and its output is zero; rows with the same index are taken in row
+    order, as consecutive tokens of one sequence."""
+    dev = _device("mamba_conv_step", "x", x)
+    code = _data_dtype("x", x)
+    silu = _activation(activation)
+    if x.dim() != 2 or x.numel() == 0:
+        raise ValueError(f"x must have shape [n, D] and not be empty, got {list(x.shape)}")
+    n, D = (int(s) for s in x.shape)
+    W = _check_filter(weight, bias, D, dev)
+    slots, stride, idx = _check_pool(state, (W - 1, D), x.dtype, state_indices, n, dev)
+    x, weight, bias = _dense_inner(x, 1), _aligned(weight), _aligned(bias)
+    _apart("state", state, (("x", x), ("weight", weight), ("bias", bias), ("state_indices", idx)))
+    res = _out(out, (n, D), x.dtype, dev, (("x", x), ("state", state)))
+    a = _lib.MambaConvStepArgs(n, D, slots, stride, x.stride(0), W, code, silu, 0, _ptr(x), _ptr(state), _ptr(weight), _ptr(bias),
+                               _ptr(idx), _ptr(res))
+    _call("mamba_conv_step", a, dev)
+    return res
+
+
+# ---------------------------------------------------------------- selective scan
+def _check_scan(u, dt, a, b, c, d, z, dt_bias, lead, dev):
+    """Sizes and the tensors with dense inner axes, parameters contiguous."""
+    D = int(u.shape[-1])
+    if a.dim() != 2 or a.shape[0] != D:
+        raise ValueError(f"a must have shape [{D}, N], got {list(a.shape)}")
+    N = int(a.shape[1])
+    if b.dim() != len(lead) + 2 or tuple(b.shape[:-2]) != lead or b.shape[-1] != N:
+        raise ValueError(f"b must have shape {[*lead, 'G', N]}, got {list(b.shape)}")
+    G = int(b.shape[-2])
+    if G < 1 or N < 1 or D % G:
+        raise ValueError(f"the {D} channels must be divisible by the {G} groups of b and c, and a must have states")
+    if N > 128:
+        raise NotImplementedError(f"mamba_scan supports at most 128 states, got {N}")
+    _check([("dt", dt, u.shape, None), ("a", a, (D, N), _F32), ("b", b, (*lead, G, N), None), ("c", c, (*lead, G, N), None),
+            ("d", d, (D,), _F32), ("z", z, u.shape, None), ("dt_bias", dt_bias, (D,), _F32)], u.dtype, dev)
+    data = tuple(None if t is None else _dense_inner(t, k) for t, k in ((u, 1), (dt, 1), (b, 2), (c, 2), (z, 1)))
+    return D, G, N, data, tuple(_aligned(t) for t in (a, d, dt_bias))
+
+
+def mamba_scan_fwd(u, dt, a, b, c, d=None, z=None, dt_bias=None, initial_state=None, cu_seqlens=None, *, dt_softplus: bool = False,
+                   return_state: bool = False, out: Optional[Tensor] = None, workspace: Optional[Tensor] = None) -> MambaScanOutputs:
+    """Selective scan. For channel d of group g = d // (D / G) and state n, with dt' = dt + dt_bias (through
+    softplus with ``dt_softplus``):
+
+        h[t] = exp(dt'[t] a[d, n]) h[t-1] + dt'[t] u[t] b[t, g, n]
+        out[t] = (sum_n c[t, g, n] h[t] + d[d] u[t]) * silu(z[t])
+
+    from ``initial_state`` (zeros without it); the skip, gate and bias are left out where d, z, dt_bias are None.
+
+    u, dt, z, out [B, S, D] or packed [T, D]; b, c [..., G, N]; a [D, N], d, dt_bias [D] float32; initial_state
+    and the returned ``state`` (with ``return_state``; the last h) [n, D, N] float32, as ``mamba_scan_step``
+    takes them. N at most 128. Tokens behind the last sequence: rows of ``out`` are left as they were when
+    the caller gives it, else zero."""
+    dev = _device("mamba_scan_fwd", "u", u)
+    code = _data_dtype("u", u)
+    n, S, lead = _sequences("u", u, cu_seqlens, 1)
+    D, G, N, (u, dt, b, c, z), (a, d, dt_bias) = _check_scan(u, dt, a, b, c, d, z, dt_bias, lead, dev)
+    _check([("initial_state", initial_state, (n, D, N), _F32)], None, dev)
+    cu, initial_state = _cu(cu_seqlens, dev), _aligned(initial_state)
+    res = _out(out, (*lead, D), u.dtype, dev, (("u", u), ("dt", dt), ("b", b), ("c", c), ("z", z), ("initial_state", initial_state)))
+    state = torch.empty((n, D, N), dtype=_F32, device=dev) if return_state else None
+    packed = cu is not None
+    args = _lib.MambaScanFwdArgs(n, S, D, G, N, code, int(bool(dt_softplus)), int(out is None), 0, _ptr(cu),
+                                 *(_rows(t, packed) for t in (u, dt, b, c, z)), _ptr(a), _ptr(d), _ptr(dt_bias),
+                                 _ptr(initial_state), _ptr(res), _ptr(state))
+    _call("mamba_scan_fwd", args, dev, workspace)
+    return MambaScanOutputs(res, state)
+
+
+def mamba_scan_bwd(dout, u, dt, a, b, c, d=None, z=None, dt_bias=None, initial_state=None, dstate=None, cu_seqlens=None, *,
+                   dt_softplus: bool = False, workspace: Optional[Tensor] = None) -> MambaScanGrads:
+    """Gradients of ``sum(out * dout) + sum(state * dstate)`` for the arguments of ``mamba_scan_fwd``: du, ddt,
+    db, dc, dz in the data dtype, da, dd, ddt_bias, dinitial_state float32; those of absent inputs are None.
+    dout like u, dstate like initial_state. The states are recomputed, so nothing is kept from the forward
+    call. Token gradients are zero behind the last sequence."""
+    dev = _device("mamba_scan_bwd", "u", u)
+    code = _data_dtype("u", u)
+    n, S, lead = _sequences("u", u, cu_seqlens, 1)
+    D, G, N, (u, dt, b, c, z), (a, d, dt_bias) = _check_scan(u, dt, a, b, c, d, z, dt_bias, lead, dev)
+    _check([("dout", dout, u.shape, None), ("initial_state", initial_state, (n, D, N), _F32), ("dstate", dstate, (n, D, N), _F32)],
+           u.dtype, dev)
+    cu, dout, initial_state, dstate = _cu(cu_seqlens, dev), _dense_inner(dout, 1), _aligned(initial_state), _aligned(dstate)
+    packed = cu is not None
+
+    def new(*shape, dtype=_F32, like=True):
+        return None if like is None else torch.empty(shape, dtype=dtype, device=dev)
+
+    g = MambaScanGrads(du=new(*lead, D, dtype=u.dtype), ddt=new(*lead, D, dtype=u.dtype), da=new(D, N), db=new(*lead, G, N, dtype=u.dtype),
+                       dc=new(*lead, G, N, dtype=u.dtype), dd=new(D, like=d), dz=new(*lead, D, dtype=u.dtype, like=z),
+                       ddt_bias=new(D, like=dt_bias), dinitial_state=new(n, D, N, like=initial_state))
+    args = _lib.MambaScanBwdArgs(n, S, D, G, N, code, int(bool(dt_softplus)), 0, 0, _ptr(cu),
+                                 *(_rows(t, packed) for t in (dout, u, dt, b, c, z)), _ptr(a), _ptr(d), _ptr(dt_bias),
+                                 _ptr(initial_state), _ptr(dstate), *(_ptr(t) for t in (g.du, g.ddt, g.db, g.dc, g.dz)),
+                                 *(_ptr(t) for t in (g.da, g.dd, g.ddt_bias, g.dinitial_state)))
+    _call("mamba_scan_bwd", args, dev, workspace)
+    return g
+
+
+def mamba_scan_step(u, dt, state, a, b, c, d=None, z=None, dt_bias=None, state_indices=None, *, dt_softplus: bool = False,
+                    out: Optional[Tensor] = None) -> Tensor:
+    """One token of ``mamba_scan_fwd`` for each of n rows: u, dt, z, out [n, D]; b, c [n, G, N]; ``state`` [slots,
+    D, N] float32 is updated in place. Slots and ``state_indices`` as for ``mamba_conv_step``."""
+    dev = _device("mamba_scan_step", "u", u)
+    code = _data_dtype("u", u)
+    if u.dim() != 2 or u.numel() == 0:
+        raise ValueError(f"u must have shape [n, D] and not be empty, got {list(u.shape)}")
+    n = int(u.shape[0])
+    D, G, N, (u, dt, b, c, z), (a, d, dt_bias) = _check_scan(u, dt, a, b, c, d, z, dt_bias, (n,), dev)
+    slots, stride, idx = _check_pool(state, (D, N), _F32, state_indices, n, dev)
+    inputs = (("u", u), ("dt", dt), ("b", b), ("c", c), ("z", z))
+    _apart("state", state, (*inputs, ("a", a), ("d", d), ("dt_bias", dt_bias), ("state_indices", idx)))
+    res = _out(out, (n, D), u.dtype, dev, (*inputs, ("state", state)))
+    rows = (_lib.MambaRows(None, 0, 0) if t is None else _lib.MambaRows(t.data_ptr(), t.stride(0), 0) for t in (u, dt, b, c, z))
+    args = _lib.MambaScanStepArgs(n, D, G, N, slots, stride, code, int(bool(dt_softplus)), *rows, _ptr(a), _ptr(d), _ptr(dt_bias),
+                                  _ptr(state), _ptr(idx), _ptr(res))
+    _call("mamba_scan_step", args, dev)
+    return res
+
+
+# ---------------------------------------------------------------- gated group norm
+def _row_view(x, D):
+    """x [..., D] as rows with one stride: a view where the leading axes allow it, else a copy."""
+    x = _dense_inner(x, 1)
+    return x.reshape(-1, D) if x.dim() != 2 else x
+
+
+def _check_norm(what, x, weight, bias, z, groups, eps, gate, activation):
+    dev = _device(what, "x", x)
+    code = _data_dtype("x", x)
+    silu = _activation(activation)
+    if gate not in ("before", "after"):
+        raise ValueError("gate must be 'before' or 'after'")
+    if silu and z is not None:
+        raise ValueError("activation and a gate z exclude each other")
+    if x.dim() < 1 or x.numel() == 0:
+        raise ValueError(f"x must have shape [..., D] and not be empty, got {list(x.shape)}")
+    D = int(x.shape[-1])
+    if isinstance(groups, bool) or not isinstance(groups, int) or groups < 1 or D % groups:
+        raise ValueError(f"groups must be a positive int that divides the {D} channels, got {groups!r}")
+    if not eps >= 0:
+        raise ValueError(f"eps must not be negative, got {eps}")
+    if D // groups > 8192:
+        raise NotImplementedError(f"mamba_norm supports at most 8192 channels in a group, got {D // groups}")
+    _check([("weight", weight, (D,), _F32), ("bias", bias, (D,), _F32), ("z", z, x.shape, None)], x.dtype, dev)
+    return dev, code, silu, D, _row_view(x, D), None if z is None else _row_view(z, D), _aligned(weight), _aligned(bias)
+
+
+def mamba_norm_fwd(x, weight, bias=None, z=None, *, groups: int = 1, eps: float = 1e-5, center: bool = False, gate: str = "before",
+                   activation: Optional[str] = None, out: Optional[Tensor] = None) -> Tensor:
+    """Gated group norm over the last axis, in ``groups`` groups of neighbouring channels (at most 8192 each). With
+    v = x * silu(z) (z given, gate "before") or x, and m = mean(v) over the group with ``center``, else 0:
+
+        p = (v - m) / sqrt(mean((v - m)^2) + eps) * weight + bias
+
+    and out = p * silu(z) (z given, gate "after"), silu(p) (activation "silu", without z), or p. x, z, out
+    [..., D]; weight, bias [D] float32."""
+    dev, code, silu, D, rows, zr, weight, bias = _check_norm("mamba_norm_fwd", x, weight, bias, z, groups, eps, gate, activation)
+    res = _out(out, x.shape, x.dtype, dev, (("x", rows), ("z", zr)))
+    a = _lib.MambaNormFwdArgs(rows.shape[0], D, groups, rows.stride(0), 0 if zr is None else zr.stride(0), code, int(bool(center)),
+                              int(gate == "after"), silu, eps, 0, _ptr(rows), _ptr(zr), _ptr(weight), _ptr(bias), _ptr(res))
+    _call("mamba_norm_fwd", a, dev)
+    return res
+
+
+def mamba_norm_bwd(dout, x, weight, bias=None, z=None, *, groups: int = 1, eps: float = 1e-5, center: bool = False,
+                   gate: str = "before", activation: Optional[str] = None, workspace: Optional[Tensor] = None) -> MambaNormGrads:
+    """Gradients of ``sum(out * dout)`` for the arguments of ``mamba_norm_fwd``: dx and dz in x's dtype, dweight and
+    dbias float32; dbias and dz are None without the input. The statistics are recomputed from x and z."""
+    dev, code, silu, D, rows, zr, weight, bias = _check_norm("mamba_norm_bwd", x, weight, bias, z, groups, eps, gate, activation)
+    _check([("dout", dout, x.shape, None)], x.dtype, dev)
+    dr = _row_view(dout, D)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dz = None if z is None else torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dweight = torch.empty((D,), dtype=_F32, device=dev)
+    dbias = None if bias is None else torch.empty((D,), dtype=_F32, device=dev)
+    a = _lib.MambaNormBwdArgs(rows.shape[0], D, groups, dr.stride(0), rows.stride(0), 0 if zr is None else zr.stride(0), code,
+                              int(bool(center)), int(gate == "after"), silu, eps, 0, _ptr(dr), _ptr(rows), _ptr(zr), _ptr(weight),
+                              _ptr(bias), _ptr(dx), _ptr(dz), _ptr(dweight), _ptr(dbias))
+    _call("mamba_norm_bwd", a, dev, workspace)
+    return MambaNormGrads(dx, dweight, dbias, dz)
