@@ -8,6 +8,7 @@ missing the import of this module's ``lib()`` raises, there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import struct
 from pathlib import Path
 
 LIB_PATH = Path(__file__).resolve().parent / "_build" / "libmimo_bwd_fwd.so"
@@ -299,11 +300,11 @@ def lib():
         L.mimo_bwd_bwd_timed.restype = ctypes.c_int
         L.mimo_bwd_bwd_workspace_size.argtypes = [bargp, szp]
         L.mimo_bwd_bwd_workspace_size.restype = ctypes.c_int
-        for name, (args, workspace) in LAYER_CALLS.items():
-            getattr(L, name).argtypes = [ctypes.POINTER(args), ctypes.c_void_p]
+        for name, (_, workspace) in LAYER_CALLS.items():
+            getattr(L, name).argtypes = [ctypes.c_void_p, ctypes.c_void_p]   # the struct, or its bytes
             getattr(L, name).restype = ctypes.c_int
             if workspace:
-                getattr(L, name + "_workspace_size").argtypes = [ctypes.POINTER(args), szp]
+                getattr(L, name + "_workspace_size").argtypes = [ctypes.c_void_p, szp]
                 getattr(L, name + "_workspace_size").restype = ctypes.c_int
         L.mimo_last_error.argtypes = []
         L.mimo_last_error.restype = ctypes.c_char_p
@@ -313,6 +314,17 @@ def lib():
             raise ImportError(f"{LIB_PATH}: ABI version {L.mimo_abi_version()} != {ABI_VERSION}")
         _lib = L
     return _lib
+
+
+def packer(cls):
+    """A function that packs the fields of a ctypes struct (nested ones flattened, pointers as integers) into its bytes."""
+    codes = {ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f", ctypes.c_size_t: "Q", ctypes.c_void_p: "Q"}
+
+    def flat(c):
+        return "".join(codes[t] if t in codes else flat(t) for _, t in c._fields_)
+    form = struct.Struct("@" + flat(cls))
+    assert form.size == ctypes.sizeof(cls), cls
+    return form.pack
 
 
 def last_error() -> str:

@@ -194,25 +194,33 @@ __device__ __forceinline__ int next_of(const int* idx, int row, int n, int slot)
 }
 
 // ---------------------------------------------------------------- sums over partial rows
-// out(col) = sum over R rows of part[r * ld + col], for the 64 columns of a block of 256 threads: four
-// threads a column, each over every fourth row with four sums in flight, joined in LDS in order.
+// put(col, sum over R rows of part[r * ld + col]) for SUM_COLS columns from col0, by a block of 256 threads: sixteen
+// threads a column, each over every sixteenth row with four sums in flight, joined in LDS in order.
+// Few columns a block, so that the usual few thousand columns make enough blocks to fill the GPU.
+constexpr int SUM_COLS = 16;
 template <class F> __device__ __forceinline__ void column_sums(const float* part, long ld, long R, long col0, long cols, F put) {
-    __shared__ float s[4][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const long col = col0 + lane;
+    constexpr int TR = 256 / SUM_COLS;
+    __shared__ float s[TR][SUM_COLS];
+    const int c = threadIdx.x % SUM_COLS, w = threadIdx.x / SUM_COLS;
+    const long col = col0 + c;
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     if (col < cols) {
         const float* p = part + col;
         long r = w;
-        for (; r + 12 < R; r += 16) {
+        for (; r + 3 * TR < R; r += 4 * TR) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) acc[k] += p[(r + 4 * k) * ld];
+            for (int k = 0; k < 4; ++k) acc[k] += p[(r + k * TR) * ld];
         }
-        for (int k = 0; r < R; r += 4, ++k) acc[k] += p[r * ld];
+        for (int k = 0; r < R; r += TR, ++k) acc[k] += p[r * ld];
     }
-    s[w][lane] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+    s[w][c] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
     __syncthreads();
-    if (w == 0 && col < cols) put(col, (s[0][lane] + s[1][lane]) + (s[2][lane] + s[3][lane]));
+    if (w == 0 && col < cols) {
+        float x = 0.f;
+#pragma unroll
+        for (int k = 0; k < TR; ++k) x += s[k][c];
+        put(col, x);
+    }
 }
 
 // ---------------------------------------------------------------- host side

@@ -3,9 +3,11 @@
 //   pre[t] = bias + sum_k w[k] e[t + k],  out = silu(pre) or pre,  e = (W - 1 rows of state, x)
 //   dpre = dout * silu'(pre);  dx[t] = sum_k w[k] dpre[t + W-1 - k];  dw[k] = sum_t dpre[t] e[t + k]
 //
-// A thread owns VEC neighbouring channels (16 bytes of a row) over one chunk of CH tokens and
-// slides the window through registers, so a token of x is read once and W - 1 rows more at each
-// chunk's start. The passes are bound by memory.
+// A thread owns two neighbouring channels over one chunk of CH tokens and slides the window through
+// registers, so a token of x is read once and W - 1 rows more at each chunk's start. Memory binds.
+// Two channels a thread and many threads beat wider accesses, whose windows cost the registers that
+// keep waves, and so loads, in flight: [8192, 2048] bf16 forward 18.5 us with eight channels, 17.1 with
+// four, 16.1 with two; [4, 4100, 2048] bf16 backward 156, 60 and 57 us.
 #include "layer.hpp"
 
 namespace mimo {
@@ -230,7 +232,7 @@ template <int DT, int VEC, int W, int TX> __global__ __launch_bounds__(256) void
 
 template <int W> __global__ __launch_bounds__(256) void k_conv_sums(ConvParams p) {
     const long D = p.D;
-    column_sums(p.part, (W + 1) * D, p.groups, (long)blockIdx.x * 64, (W + 1) * D, [&](long col, float s) {
+    column_sums(p.part, (W + 1) * D, p.groups, (long)blockIdx.x * SUM_COLS, (W + 1) * D, [&](long col, float s) {
         const int k = (int)(col / D);
         const long d = col - k * D;
         if (k < W) p.dw[d * W + k] = s;
@@ -297,13 +299,15 @@ template <int DT, int VEC, int W> __global__ __launch_bounds__(256) void k_conv_
 }
 
 // ---------------------------------------------------------------- host side
-// tokens of a chunk: as few threads as still fill the GPU (about 512 a CU in each pass), 16 to 64 tokens
-int chunk_tokens(int64_t n, int64_t S, bool packed, int64_t nvec) {
+// Tokens of a chunk: about 1024 threads a CU, 16 tokens at least. Longer chunks read fewer rows twice, and the
+// backward pass leaves fewer partial sums; 32 suffice forward (8 x 8192 x 2048 bf16: 107 us at 32, 115 at 128), where the
+// backward pass gains up to 128 (243 us at 64, 208 at 128).
+int chunk_tokens(int64_t n, int64_t S, bool packed, int64_t nvec, int most) {
     const int64_t T = packed ? S : n * S;
-    int64_t c = T * nvec / (256 * 512);
-    c = c < 16 ? 16 : c > 64 ? 64 : c / 8 * 8;
-    return (int)c;
+    const int64_t c = T * nvec / (256 * 1024) / 8 * 8;
+    return (int)(c < 16 ? 16 : c > most ? most : c);
 }
+constexpr int MOST_FWD = 32, MOST_BWD = 128;
 
 Seqs make_seqs(int64_t n, int64_t S, const int32_t* cu, int CH) {
     return Seqs{cu, (int)n, (int)S, CH, (int)((S + CH - 1) / CH)};
@@ -315,17 +319,11 @@ mimo_status check_filter(int32_t W, const float* w) {
     return MIMO_OK;
 }
 
-// channels of a thread: 16 bytes of a row where every row allows it (filters beyond four taps: 8
-// bytes of 16-bit types, for the registers of their windows), else one
-int vec_of(int dtype, int W, int64_t D, bool even) {
-    const int v = dtype == F32 ? 4 : W <= 4 ? 8 : 4;
-    return even && D % v == 0 ? v : 1;
-}
+// channels of a thread: two where every row starts at a multiple of both, else one
+int vec_of(int64_t D, bool even) { return even && D % 2 == 0 ? 2 : 1; }
 
 template <int DT, int W, class F> mimo_status with_vec(int vec, F f) {
-    constexpr int V = DT == F32 ? 4 : W <= 4 ? 8 : 4;
-    if (vec == V) return f.template operator()<DT, V, W>();
-    return f.template operator()<DT, 1, W>();
+    return vec == 2 ? f.template operator()<DT, 2, W>() : f.template operator()<DT, 1, W>();
 }
 template <int DT, class F> mimo_status with_taps(int W, int vec, F f) {
     switch (W) {
@@ -355,10 +353,10 @@ struct BwdRun {
     ConvParams p;
     hipStream_t st;
     template <int DT, int VEC, int W> mimo_status operator()() {
-        constexpr int TX = VEC == 1 ? 64 : 32;
+        constexpr int TX = 32 * (3 - VEC);
         mimo_status s = launch(&k_conv_bwd<DT, VEC, W, TX>, dim3(p.groups, (p.nvec + TX - 1) / TX), 256, 0, st, p);
         if (s != MIMO_OK) return s;
-        return launch(&k_conv_sums<W>, dim3((unsigned)(((W + 1) * (long)p.D + 63) / 64)), 256, 0, st, p);
+        return launch(&k_conv_sums<W>, dim3((unsigned)(((W + 1) * (long)p.D + SUM_COLS - 1) / SUM_COLS)), 256, 0, st, p);
     }
 };
 struct StepRun {
@@ -380,14 +378,14 @@ mimo_status plan_bwd(const mamba_conv_bwd_args* a, BwdPlan* pl) {
     if (s != MIMO_OK) return s;
     if (a->W < MAMBA_CONV_MIN_TAPS || a->W > MAMBA_CONV_MAX_TAPS) return unsupported("the filter must have 2 to 8 taps");
     const int esz = a->dtype == F32 ? 4 : 2;
-    bool even = aligned(a->x.data, a->x.batch_stride, a->x.token_stride, 16, esz) &&
-                aligned(a->dout.data, a->dout.batch_stride, a->dout.token_stride, 16, esz);
-    for (const void* x : {a->initial_state, a->dstate, (const void*)a->dx, (const void*)a->dinitial_state}) even = even && aligned(x, 0, 0, 16, 1);
-    pl->vec = vec_of(a->dtype, a->W, a->D, even);
+    bool even = aligned(a->x.data, a->x.batch_stride, a->x.token_stride, 2 * esz, esz) &&
+                aligned(a->dout.data, a->dout.batch_stride, a->dout.token_stride, 2 * esz, esz);
+    for (const void* x : {a->initial_state, a->dstate, (const void*)a->dx, (const void*)a->dinitial_state}) even = even && aligned(x, 0, 0, 2 * esz, 1);
+    pl->vec = vec_of(a->D, even);
     const bool packed = a->cu_seqlens != nullptr;
-    pl->CH = chunk_tokens(a->n, a->S, packed, a->D / pl->vec);
+    pl->CH = chunk_tokens(a->n, a->S, packed, a->D / pl->vec, MOST_BWD);
     const Seqs q = make_seqs(a->n, a->S, a->cu_seqlens, pl->CH);
-    const int TY = pl->vec == 1 ? 4 : 8;
+    const int TY = pl->vec == 1 ? 4 : 8;   // 256 / TX of the launch
     const long groups = (slots_of(q) + TY - 1) / TY;
     if (slots_of(q) > (long)1 << 30) return unsupported("too many tokens");
     pl->groups = (int)groups;
@@ -410,14 +408,14 @@ mimo_status mamba_conv_fwd(const mamba_conv_fwd_args* a, void* stream) {
     if (s != MIMO_OK || (s = check_filter(a->W, a->weight)) != MIMO_OK) return s;
     if (!a->x.data || !a->out) return bad("x and out must not be NULL");
     const int esz = a->dtype == F32 ? 4 : 2;
-    bool even = aligned(a->x.data, a->x.batch_stride, a->x.token_stride, 16, esz);
-    for (const void* x : {a->initial_state, (const void*)a->out, (const void*)a->state}) even = even && aligned(x, 0, 0, 16, 1);
-    const int vec = vec_of(a->dtype, a->W, a->D, even);
+    bool even = aligned(a->x.data, a->x.batch_stride, a->x.token_stride, 2 * esz, esz);
+    for (const void* x : {a->initial_state, (const void*)a->out, (const void*)a->state}) even = even && aligned(x, 0, 0, 2 * esz, 1);
+    const int vec = vec_of(a->D, even);
     const bool packed = a->cu_seqlens != nullptr;
     ConvParams p{};
     p.D = (int)a->D;
     p.nvec = p.D / vec;
-    p.q = make_seqs(a->n, a->S, a->cu_seqlens, chunk_tokens(a->n, a->S, packed, p.nvec));
+    p.q = make_seqs(a->n, a->S, a->cu_seqlens, chunk_tokens(a->n, a->S, packed, p.nvec, MOST_FWD));
     p.items = slots_of(p.q) * p.nvec;
     if (slots_of(p.q) > (long)1 << 30 || p.items > (long)1 << 38) return unsupported("too many tokens");
     p.silu = a->silu;
@@ -478,11 +476,11 @@ mimo_status mamba_conv_step(const mamba_conv_step_args* a, void* stream) {
     if (a->slots < 1 || a->slots > (int64_t)1 << 30) return bad("slots must be in [1, 2^30]");
     if (!a->indices && a->slots < a->n) return bad("without indices the state needs a slot for each row");
     const int esz = a->dtype == F32 ? 4 : 2;
-    const bool even = aligned(a->x, a->x_stride, 0, 16, esz) && aligned(a->state, a->slot_stride, 0, 16, esz) && aligned(a->out, 0, 0, 16, 1);
+    const bool even = aligned(a->x, a->x_stride, 0, 2 * esz, esz) && aligned(a->state, a->slot_stride, 0, 2 * esz, esz) && aligned(a->out, 0, 0, 2 * esz, 1);
     const StepParams p{(int)a->n, (int)a->D, (int)a->slots, a->silu, (long)a->slot_stride, (long)a->x_stride, a->x, a->state, a->out,
                        a->weight, a->bias, a->indices};
     if ((s = require_gfx950()) != MIMO_OK) return s;
-    return dispatch(a->dtype, a->W, vec_of(a->dtype, a->W, a->D, even), StepRun{p, static_cast<hipStream_t>(stream)});
+    return dispatch(a->dtype, a->W, vec_of(a->D, even), StepRun{p, static_cast<hipStream_t>(stream)});
 }
 
 }  // extern "C"

@@ -5,9 +5,12 @@
 //   backward: dp from dout;  dw = sum dp hat;  db = sum dp;  q = dp w;
 //             dv = r (q - [mean(q)] - hat mean(q hat)), then through the gate
 //
-// TPR threads share a group of a row and keep it in registers (IT accesses of VEC elements each), so
-// every input is read once: memory binds. Sums run over lanes; groups that need a whole block join the
-// waves' sums in LDS. The variance is taken from the centred values, not from a difference of sums.
+// TPR threads share a group of a row and keep it in registers (IT accesses of VEC elements each, up to
+// 16 bytes), so every input is read once: memory binds ([8192, 2048] bf16 in 8 groups with z: forward 18.4 us, 5.5 TB/s;
+// backward 37 us, 4.5 TB/s). Parameters are loaded before the sums, and nothing in an element's loop
+// branches: with one load a parameter and branches inside, the forward pass took 39 us. Sums run over
+// lanes; groups that need more than a wave join the waves' sums in LDS. The variance is taken from the
+// centred values, not from a difference of sums.
 // The backward pass gives each block one group and every nth row, keeps the sums for dw and db in
 // registers over the rows, and leaves one partial row a block, added up in order by k_norm_sums.
 #include "layer.hpp"
@@ -16,11 +19,14 @@ namespace mimo {
 namespace layer {
 namespace {
 
+// what becomes of the normalised p, or of x: nothing, x silu(z), p silu(z), silu(p)
+enum { PLAIN, BEFORE, AFTER, SILU };
+
 struct NormParams {
     long rows, xs, zs, gs;          // row strides of x, z, dout
     int D, G, W;                    // channels, groups, channels of a group
-    int center, after, silu, has_z;
-    float eps;
+    int center, mode;
+    float eps, inv;                 // inv: 1 / W
     const void *x, *z, *dout;
     const float *w, *b;
     void *out, *dz;                 // out: also dx
@@ -28,7 +34,9 @@ struct NormParams {
     int nblk;
 };
 
-// the sum over the TPR threads of a group, in all of them; `s`: LDS of four floats, safe to use again after
+constexpr int threads_of(int TPR) { return TPR < 256 ? 256 : TPR; }
+
+// the sum over the TPR threads of a group, in all of them; `s`: LDS of a float a wave, safe to use again after
 // the next call on another one
 template <int TPR> __device__ __forceinline__ float sum_group(float x, float* s) {
     if constexpr (TPR <= 64) return sum_wave<TPR>(x);
@@ -36,7 +44,11 @@ template <int TPR> __device__ __forceinline__ float sum_group(float x, float* s)
         x = sum_wave<64>(x);
         if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = x;
         __syncthreads();
-        return (s[0] + s[1]) + (s[2] + s[3]);
+        const int first = threadIdx.x / TPR * (TPR / 64);
+        x = 0.f;
+#pragma unroll
+        for (int k = 0; k < TPR / 64; ++k) x += s[first + k];
+        return x;
     }
 }
 
@@ -45,33 +57,62 @@ template <int DT, int VEC, int TPR, int IT> struct Group {
     float x[IT][VEC], z[IT][VEC], hat[IT][VEC];
     float r;
     __device__ __forceinline__ static int col(int k) { return (threadIdx.x % TPR + k * TPR) * VEC; }
-    // element col(k) of row data at p, zeros past the group
-    __device__ __forceinline__ static void read(const raw* p, int W, float (&x)[IT][VEC]) {
+    // elements col(k) of row data at p; zeros past the group once unpacked
+    struct Raw {
         Pack<DT, VEC> t[IT];
+    };
+    __device__ __forceinline__ static Raw fetch(const raw* p, int W) {
+        Raw r;
 #pragma unroll
         for (int k = 0; k < IT; ++k)
-            if (col(k) < W) t[k] = load<DT, VEC>(p + col(k));
+            if (col(k) < W) r.t[k] = load<DT, VEC>(p + col(k));
+        return r;
+    }
+    __device__ __forceinline__ static void read(const Raw& r, int W, float (&x)[IT][VEC]) {
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
-            if (col(k) < W) unpack<DT, VEC>(t[k], x[k]);
+            if (col(k) < W) unpack<DT, VEC>(r.t[k], x[k]);
             else {
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) x[k][v] = 0.f;
             }
         }
     }
-    __device__ __forceinline__ void normalise(const NormParams& p, float (*s)[4]) {
-        const float inv = 1.f / (float)p.W;
-        float m = 0.f;
+    // the same of an fp32 parameter (NULL: zeros)
+    __device__ __forceinline__ static void param(const float* p, int W, float (&x)[IT][VEC]) {
+        constexpr int V = VEC < 4 ? VEC : 4;
 #pragma unroll
         for (int k = 0; k < IT; ++k)
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                hat[k][v] = x[k][v];
-                if (p.has_z && !p.after) hat[k][v] *= z[k][v] * sigmoid(z[k][v]);
-                m += hat[k][v];
+            for (int v = 0; v < VEC; v += V) {
+                Pack<F32, V> t;
+                if (p != nullptr && col(k) < W) t = load<F32, V>(p + col(k) + v);
+                else {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) t.v[i] = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) x[k][v + i] = t.v[i];
             }
+    }
+    __device__ __forceinline__ void normalise(const NormParams& p, float (*s)[16]) {
+        const float inv = p.inv;
+#pragma unroll
+        for (int k = 0; k < IT; ++k)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) hat[k][v] = x[k][v];
+        if (p.mode == BEFORE) {
+#pragma unroll
+            for (int k = 0; k < IT; ++k)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) hat[k][v] *= z[k][v] * sigmoid(z[k][v]);
+        }
         if (p.center) {
+            float m = 0.f;
+#pragma unroll
+            for (int k = 0; k < IT; ++k)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) m += hat[k][v];
             m = sum_group<TPR>(m, s[0]) * inv;
 #pragma unroll
             for (int k = 0; k < IT; ++k)
@@ -92,17 +133,24 @@ template <int DT, int VEC, int TPR, int IT> struct Group {
     }
 };
 
-template <int DT, int VEC, int TPR, int IT> __global__ __launch_bounds__(256) void k_norm_fwd(NormParams p) {
+template <int DT, int VEC, int TPR, int IT> __global__ __launch_bounds__(threads_of(TPR)) void k_norm_fwd(NormParams p) {
     typedef raw_t<DT> raw;
     typedef Group<DT, VEC, TPR, IT> Grp;
-    __shared__ float s[2][4];
-    const long item = (long)blockIdx.x * (256 / TPR) + threadIdx.x / TPR, items = p.rows * p.G;
-    const bool act = item < items;
-    const long row = act ? item / p.G : 0;
-    const int c0 = act ? (int)(item - row * p.G) * p.W : 0;
+    __shared__ float s[2][16];
+    const unsigned item = blockIdx.x * (threads_of(TPR) / TPR) + threadIdx.x / TPR;
+    const bool act = item < (unsigned)p.rows * (unsigned)p.G;
+    const unsigned in = act ? item / (unsigned)p.G : 0;
+    const long row = in;
+    const int c0 = act ? (int)(item - in * (unsigned)p.G) * p.W : 0;
     Grp g;
-    Grp::read(static_cast<const raw*>(p.x) + row * p.xs + c0, p.W, g.x);
-    if (p.has_z) Grp::read(static_cast<const raw*>(p.z) + row * p.zs + c0, p.W, g.z);
+    const auto rx = Grp::fetch(static_cast<const raw*>(p.x) + row * p.xs + c0, p.W);
+    typename Grp::Raw rz;
+    if (p.z) rz = Grp::fetch(static_cast<const raw*>(p.z) + row * p.zs + c0, p.W);
+    float w[IT][VEC], b[IT][VEC];
+    Grp::param(p.w + c0, p.W, w);
+    Grp::param(p.b ? p.b + c0 : nullptr, p.W, b);
+    Grp::read(rx, p.W, g.x);
+    if (p.z) Grp::read(rz, p.W, g.z);
     g.normalise(p, s);
     if (!act) return;
     raw* out = static_cast<raw*>(p.out) + row * p.D + c0;
@@ -112,58 +160,84 @@ template <int DT, int VEC, int TPR, int IT> __global__ __launch_bounds__(256) vo
         if (c >= p.W) continue;
         float y[VEC];
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            float t = g.hat[k][v] * p.w[c0 + c + v];
-            if (p.b) t += p.b[c0 + c + v];
-            if (p.has_z && p.after) t *= g.z[k][v] * sigmoid(g.z[k][v]);
-            else if (p.silu) t *= sigmoid(t);
-            y[v] = t;
+        for (int v = 0; v < VEC; ++v) y[v] = __builtin_fmaf(g.hat[k][v], w[k][v], b[k][v]);
+        if (p.mode == AFTER) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) y[v] *= g.z[k][v] * sigmoid(g.z[k][v]);
+        } else if (p.mode == SILU) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) y[v] *= sigmoid(y[v]);
         }
         store<DT, VEC>(out + c, y);
     }
 }
 
-template <int DT, int VEC, int TPR, int IT> __global__ __launch_bounds__(256) void k_norm_bwd(NormParams p) {
+template <int DT, int VEC, int TPR, int IT> __global__ __launch_bounds__(threads_of(TPR)) void k_norm_bwd(NormParams p) {
     typedef raw_t<DT> raw;
     typedef Group<DT, VEC, TPR, IT> Grp;
-    constexpr int RPB = 256 / TPR;
-    __shared__ float s[4][4];
+    constexpr int RPB = threads_of(TPR) / TPR;
+    __shared__ float s[4][16];
     __shared__ float s_sum[RPB > 1 ? 256 * VEC : 1];
     const int sub = threadIdx.x / TPR, c0 = blockIdx.y * p.W;
-    const float inv = 1.f / (float)p.W;
+    const float inv = p.inv;
     float w[IT][VEC], b[IT][VEC], dw[IT][VEC] = {}, db[IT][VEC] = {};
-#pragma unroll
-    for (int k = 0; k < IT; ++k)
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            const int c = Grp::col(k) + v;
-            w[k][v] = c < p.W ? p.w[c0 + c] : 0.f;
-            b[k][v] = c < p.W && p.b ? p.b[c0 + c] : 0.f;
-        }
-    for (long row0 = (long)blockIdx.x * RPB; row0 < p.rows; row0 += (long)gridDim.x * RPB) {
+    Grp::param(p.w + c0, p.W, w);
+    Grp::param(p.b ? p.b + c0 : nullptr, p.W, b);
+    // the next row's loads are in flight during a row, with 16-bit types: [8192, 2048] bf16 44 us instead of 48, but
+    // [4100, 2048] fp32 38 us instead of 34
+    constexpr bool AHEAD = DT != F32;
+    typename Grp::Raw rx, rz, rd;
+    auto fetch = [&](long row) {
+        row = row < p.rows ? row : p.rows - 1;
+        rx = Grp::fetch(static_cast<const raw*>(p.x) + row * p.xs + c0, p.W);
+        if (p.z) rz = Grp::fetch(static_cast<const raw*>(p.z) + row * p.zs + c0, p.W);
+        rd = Grp::fetch(static_cast<const raw*>(p.dout) + row * p.gs + c0, p.W);
+    };
+    const long step = (long)gridDim.x * RPB;
+    if (AHEAD) fetch((long)blockIdx.x * RPB + sub);
+    for (long row0 = (long)blockIdx.x * RPB; row0 < p.rows; row0 += step) {
         const bool act = row0 + sub < p.rows;
         const long row = act ? row0 + sub : p.rows - 1;
         Grp g;
         float dy[IT][VEC];
-        Grp::read(static_cast<const raw*>(p.x) + row * p.xs + c0, p.W, g.x);
-        if (p.has_z) Grp::read(static_cast<const raw*>(p.z) + row * p.zs + c0, p.W, g.z);
-        Grp::read(static_cast<const raw*>(p.dout) + row * p.gs + c0, p.W, dy);
+        if (!AHEAD) fetch(row);
+        Grp::read(rx, p.W, g.x);
+        if (p.z) Grp::read(rz, p.W, g.z);
+        Grp::read(rd, p.W, dy);
+        if (AHEAD && row0 + step < p.rows) fetch(row0 + step + sub);
         g.normalise(p, s);
         float dz[IT][VEC], m1 = 0.f, m2 = 0.f;
+        if (p.mode == AFTER) {
+#pragma unroll
+            for (int k = 0; k < IT; ++k)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    const float z = g.z[k][v], gate = sigmoid(z);
+                    dz[k][v] = dy[k][v] * __builtin_fmaf(g.hat[k][v], w[k][v], b[k][v]) * silu_slope(z, gate);
+                    dy[k][v] *= z * gate;
+                }
+        } else if (p.mode == SILU) {
+#pragma unroll
+            for (int k = 0; k < IT; ++k)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    const float t = __builtin_fmaf(g.hat[k][v], w[k][v], b[k][v]);
+                    dy[k][v] *= silu_slope(t, sigmoid(t));
+                }
+        }
+        if (!act) {
+#pragma unroll
+            for (int k = 0; k < IT; ++k)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) dy[k][v] = 0.f;
+        }
 #pragma unroll
         for (int k = 0; k < IT; ++k)
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                const float hat = g.hat[k][v], t = __builtin_fmaf(hat, w[k][v], b[k][v]);
-                if (p.has_z && p.after) {
-                    const float z = g.z[k][v], gate = sigmoid(z);
-                    dz[k][v] = dy[k][v] * t * silu_slope(z, gate);
-                    dy[k][v] *= z * gate;
-                } else if (p.silu) dy[k][v] *= silu_slope(t, sigmoid(t));
-                if (act) {
-                    dw[k][v] = __builtin_fmaf(dy[k][v], hat, dw[k][v]);
-                    db[k][v] += dy[k][v];
-                }
+                const float hat = g.hat[k][v];
+                dw[k][v] = __builtin_fmaf(dy[k][v], hat, dw[k][v]);
+                db[k][v] += dy[k][v];
                 dy[k][v] *= w[k][v];
                 m1 += dy[k][v];
                 m2 = __builtin_fmaf(dy[k][v], hat, m2);
@@ -171,16 +245,17 @@ template <int DT, int VEC, int TPR, int IT> __global__ __launch_bounds__(256) vo
         m1 = p.center ? sum_group<TPR>(m1, s[2]) * inv : 0.f;
         m2 = sum_group<TPR>(m2, s[3]) * inv;
         raw* dx = static_cast<raw*>(p.out) + row * p.D + c0;
-        raw* pz = p.has_z ? static_cast<raw*>(p.dz) + row * p.D + c0 : nullptr;
+        raw* pz = p.z ? static_cast<raw*>(p.dz) + row * p.D + c0 : nullptr;
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
             const int c = Grp::col(k);
             if (!act || c >= p.W) continue;
             float o[VEC];
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                o[v] = g.r * (dy[k][v] - m1 - g.hat[k][v] * m2);
-                if (p.has_z && !p.after) {
+            for (int v = 0; v < VEC; ++v) o[v] = g.r * (dy[k][v] - m1 - g.hat[k][v] * m2);
+            if (p.mode == BEFORE) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
                     const float z = g.z[k][v], gate = sigmoid(z);
                     dz[k][v] = o[v] * g.x[k][v] * silu_slope(z, gate);
                     o[v] *= z * gate;
@@ -217,30 +292,36 @@ template <int DT, int VEC, int TPR, int IT> __global__ __launch_bounds__(256) vo
 
 __global__ __launch_bounds__(256) void k_norm_sums(NormParams p) {
     const long D = p.D;
-    column_sums(p.part, 2 * D, p.nblk, (long)blockIdx.x * 64, 2 * D, [&](long col, float s) {
+    column_sums(p.part, 2 * D, p.nblk, (long)blockIdx.x * SUM_COLS, 2 * D, [&](long col, float s) {
         if (col < D) p.dw[col] = s;
         else if (p.db) p.db[col - D] = s;
     });
 }
 
 // ---------------------------------------------------------------- host side
-// Threads of a group: the fewest lanes that take it in one access each, up to a wave; a wave takes four
-// accesses a thread (its sums need no LDS), wider groups a block.
+// Threads of a group: one access each where 1024 threads allow it (a group's values cost a thread about
+// a hundred registers an access in the backward pass), in whole waves beyond 32.
 template <int DT, int VEC, class F> mimo_status with_shape(int W, F f) {
     const int nv = (W + VEC - 1) / VEC;
     if (nv <= 8) return f.template operator()<DT, VEC, 8, 1>();
     if (nv <= 16) return f.template operator()<DT, VEC, 16, 1>();
     if (nv <= 32) return f.template operator()<DT, VEC, 32, 1>();
     if (nv <= 64) return f.template operator()<DT, VEC, 64, 1>();
-    if (nv <= 128) return f.template operator()<DT, VEC, 64, 2>();
-    if (nv <= 256) return f.template operator()<DT, VEC, 64, 4>();
-    if (nv <= 512) return f.template operator()<DT, VEC, 256, 2>();
-    if (VEC == 8 || nv <= 1024) return f.template operator()<DT, VEC, 256, 4>();
+    if (nv <= 128) return f.template operator()<DT, VEC, 128, 1>();
+    if (nv <= 256) return f.template operator()<DT, VEC, 256, 1>();
+    if (nv <= 512) return f.template operator()<DT, VEC, 512, 1>();
+    if (VEC == 8 || nv <= 1024) return f.template operator()<DT, VEC, 1024, 1>();
     if constexpr (VEC <= 4) {
-        if (VEC == 4 || nv <= 2048) return f.template operator()<DT, VEC, 256, 8>();
-        if constexpr (VEC == 1) return f.template operator()<DT, VEC, 256, 32>();
+        if (VEC == 4 || nv <= 2048) return f.template operator()<DT, VEC, 1024, 2>();
+        if constexpr (VEC == 1) return f.template operator()<DT, VEC, 1024, 8>();
     }
     return unsupported("group too wide");
+}
+int lanes_of(int W, int VEC) {
+    const int nv = (W + VEC - 1) / VEC;
+    int t = 8;
+    while (t < nv && t < 1024) t *= 2;
+    return t;
 }
 template <class F> mimo_status dispatch(int dtype, bool even, int W, F f) {
     if (dtype == BF16) return even ? with_shape<BF16, 8>(W, f) : with_shape<BF16, 1>(W, f);
@@ -255,8 +336,9 @@ mimo_status check_norm(int64_t rows, int64_t D, int64_t G, int dtype, float eps,
     if (!(eps >= 0.f)) return bad("eps must not be negative");
     if (silu && z) return bad("silu and a gate z exclude each other");
     if (D / G > MAMBA_NORM_MAX_WIDTH) return unsupported("more than 8192 channels in a group");
+    if (rows > (int64_t)1 << 31) return unsupported("more than 2^31 rows");
     if (G > 65535 || D > (int64_t)1 << 20) return unsupported("more than 65535 groups or 2^20 channels");
-    if (rows > (int64_t)1 << 36) return unsupported("too many rows");
+    if (rows * G > (int64_t)1 << 31) return unsupported("more than 2^31 groups of rows");
     return MIMO_OK;
 }
 
@@ -264,25 +346,35 @@ struct FwdRun {
     NormParams p;
     hipStream_t st;
     template <int DT, int VEC, int TPR, int IT> mimo_status operator()() {
-        const long per = 256 / TPR, blocks = (p.rows * p.G + per - 1) / per;
-        if (blocks > 0x7fffffffL) return unsupported("too many rows");
-        return launch(&k_norm_fwd<DT, VEC, TPR, IT>, dim3((unsigned)blocks), 256, 0, st, p);
+        const long per = threads_of(TPR) / TPR, blocks = (p.rows * p.G + per - 1) / per;
+        return launch(&k_norm_fwd<DT, VEC, TPR, IT>, dim3((unsigned)blocks), threads_of(TPR), 0, st, p);
     }
 };
 struct BwdRun {
     NormParams p;
     hipStream_t st;
     template <int DT, int VEC, int TPR, int IT> mimo_status operator()() {
-        const mimo_status s = launch(&k_norm_bwd<DT, VEC, TPR, IT>, dim3(p.nblk, p.G), 256, 0, st, p);
+        const mimo_status s = launch(&k_norm_bwd<DT, VEC, TPR, IT>, dim3(p.nblk, p.G), threads_of(TPR), 0, st, p);
         if (s != MIMO_OK) return s;
-        return launch(&k_norm_sums, dim3((unsigned)((2L * p.D + 63) / 64)), 256, 0, st, p);
+        return launch(&k_norm_sums, dim3((unsigned)((2L * p.D + SUM_COLS - 1) / SUM_COLS)), 256, 0, st, p);
     }
 };
 
-// blocks of a group: about 1024 blocks in all, none without a row of its own
+bool even_of(const mamba_norm_bwd_args* a) {
+    const int esz = a->dtype == F32 ? 4 : 2;
+    bool even = a->D / a->G % (16 / esz) == 0 && aligned(a->x, a->x_stride, 0, 16, esz) && aligned(a->dout, a->dout_stride, 0, 16, esz) &&
+                aligned(a->z, a->z ? a->z_stride : 0, 0, 16, esz);
+    for (const void* x : {(const void*)a->dx, (const void*)a->dz, (const void*)a->weight, (const void*)a->bias}) even = even && aligned(x, 0, 0, 16, 1);
+    return even;
+}
+
+// blocks of a group: 1024 threads a CU in all, none without a row of its own
 int64_t bwd_blocks(const mamba_norm_bwd_args* a) {
-    const int64_t want = 1024 / a->G < 1 ? 1 : 1024 / a->G;
-    return a->rows < want ? a->rows : want;
+    const int lanes = lanes_of((int)(a->D / a->G), !even_of(a) ? 1 : a->dtype == F32 ? 4 : 8), threads = threads_of(lanes);
+    int64_t want = 256 * 1024 / threads / a->G;
+    want = want < 1 ? 1 : want;
+    const int64_t have = (a->rows + threads / lanes - 1) / (threads / lanes);
+    return have < want ? have : want;
 }
 
 }  // namespace
@@ -302,11 +394,12 @@ mimo_status mamba_norm_fwd(const mamba_norm_fwd_args* a, void* stream) {
     NormParams p{};
     p.rows = a->rows, p.D = (int)a->D, p.G = (int)a->G, p.W = p.D / p.G;
     p.xs = a->x_stride, p.zs = a->z_stride;
-    p.center = a->center, p.after = a->gate_after, p.silu = a->silu, p.has_z = a->z != nullptr, p.eps = a->eps;
+    p.center = a->center, p.mode = a->z ? (a->gate_after ? AFTER : BEFORE) : a->silu ? SILU : PLAIN;
+    p.eps = a->eps, p.inv = 1.f / (float)p.W;
     p.x = a->x, p.z = a->z, p.w = a->weight, p.b = a->bias, p.out = a->out;
     const int esz = a->dtype == F32 ? 4 : 2;
     const bool even = p.W % (16 / esz) == 0 && aligned(a->x, a->x_stride, 0, 16, esz) && aligned(a->z, a->z ? a->z_stride : 0, 0, 16, esz) &&
-                      aligned(a->out, 0, 0, 16, 1);
+                      aligned(a->out, 0, 0, 16, 1) && aligned(a->weight, 0, 0, 16, 1) && aligned(a->bias, 0, 0, 16, 1);
     if ((s = require_gfx950()) != MIMO_OK) return s;
     return dispatch(a->dtype, even, p.W, FwdRun{p, static_cast<hipStream_t>(stream)});
 }
@@ -331,16 +424,13 @@ mimo_status mamba_norm_bwd(const mamba_norm_bwd_args* a, void* stream) {
     NormParams p{};
     p.rows = a->rows, p.D = (int)a->D, p.G = (int)a->G, p.W = p.D / p.G;
     p.xs = a->x_stride, p.zs = a->z_stride, p.gs = a->dout_stride;
-    p.center = a->center, p.after = a->gate_after, p.silu = a->silu, p.has_z = a->z != nullptr, p.eps = a->eps;
+    p.center = a->center, p.mode = a->z ? (a->gate_after ? AFTER : BEFORE) : a->silu ? SILU : PLAIN;
+    p.eps = a->eps, p.inv = 1.f / (float)p.W;
     p.x = a->x, p.z = a->z, p.dout = a->dout, p.w = a->weight, p.b = a->bias;
     p.out = a->dx, p.dz = a->dz, p.part = static_cast<float*>(a->workspace), p.dw = a->dweight, p.db = a->dbias;
     p.nblk = (int)bwd_blocks(a);
-    const int esz = a->dtype == F32 ? 4 : 2;
-    bool even = p.W % (16 / esz) == 0 && aligned(a->x, a->x_stride, 0, 16, esz) && aligned(a->dout, a->dout_stride, 0, 16, esz) &&
-                aligned(a->z, a->z ? a->z_stride : 0, 0, 16, esz);
-    even = even && aligned(a->dx, 0, 0, 16, 1) && aligned(a->dz, 0, 0, 16, 1);
     if ((s = require_gfx950()) != MIMO_OK) return s;
-    return dispatch(a->dtype, even, p.W, BwdRun{p, static_cast<hipStream_t>(stream)});
+    return dispatch(a->dtype, even_of(a), p.W, BwdRun{p, static_cast<hipStream_t>(stream)});
 }
 
 }  // extern "C"

@@ -309,15 +309,15 @@ __host__ __device__ inline int blocks_of(long n, int per) { return (int)((n + pe
 // channel tiles of a group
 template <int DT> __global__ __launch_bounds__(256) void k_sums(ScanParams p) {
     const long D = p.D, N = p.N;
-    const int na = blocks_of(N * D, 64), nd = blocks_of(2 * D, 64);
+    const int na = blocks_of(N * D, SUM_COLS), nd = blocks_of(2 * D, SUM_COLS);
     int blk = blockIdx.x;
     if (blk < na) {
-        column_sums(p.agg, N * D, p.slots, (long)blk * 64, N * D, [&](long col, float s) { p.da[(col % D) * N + col / D] = s; });
+        column_sums(p.agg, N * D, p.slots, (long)blk * SUM_COLS, N * D, [&](long col, float s) { p.da[(col % D) * N + col / D] = s; });
         return;
     }
     blk -= na;
     if (blk < nd) {
-        column_sums(p.pdd, 2 * D, p.slots, (long)blk * 64, 2 * D, [&](long col, float s) {
+        column_sums(p.pdd, 2 * D, p.slots, (long)blk * SUM_COLS, 2 * D, [&](long col, float s) {
             if (col < D) {
                 if (p.dd) p.dd[col] = s;
             } else if (p.dbias) p.dbias[col - D] = s;
@@ -398,7 +398,7 @@ template <int DT> struct Run {
         s = launch(&k_scan_bwd<DT, NS, Q>, dim3((unsigned)p.slots, p.G * p.tpg), 256, Shape<NS, Q>::lds, st, p);
         if (s != MIMO_OK) return s;
         const long per = p.tokens * p.G * 2 * p.N;
-        const long blocks = (long)blocks_of((long)p.N * p.D, 64) + blocks_of(2L * p.D, 64) + (per + 255) / 256;
+        const long blocks = (long)blocks_of((long)p.N * p.D, SUM_COLS) + blocks_of(2L * p.D, SUM_COLS) + (per + 255) / 256;
         return launch(&k_sums<DT>, dim3((unsigned)blocks), 256, 0, st, p);
     }
 };

@@ -21,7 +21,7 @@ import torch
 
 from . import _lib
 from .api import _BWD2_DTYPES as _DTYPES
-from .api import _aligned, _check_output, _check_tensor, _is_gfx950, _raise, _workspace
+from .api import _check_output, _check_tensor, _is_gfx950, _raise, _workspace
 
 __all__ = ["MambaConvOutputs", "MambaConvGrads", "MambaScanOutputs", "MambaScanGrads", "MambaNormGrads", "mamba_conv_fwd",
            "mamba_conv_bwd", "mamba_conv_step", "mamba_scan_fwd", "mamba_scan_bwd", "mamba_scan_step", "mamba_norm_fwd",
@@ -68,56 +68,52 @@ class MambaNormGrads(NamedTuple):
 
 
 # ---------------------------------------------------------------- checks
+# A step of one token takes the GPU about three microseconds, so what happens here is kept short: a tensor is
+# looked at once, its pointer taken once, and the arguments packed as bytes instead of ctypes fields.
 def _data_dtype(name, x):
-    if x.dtype not in _DTYPES:
+    code = _DTYPES.get(x.dtype)
+    if code is None:
         raise TypeError(f"{name} must use torch.bfloat16, torch.float16 or torch.float32, got {x.dtype}")
-    return _DTYPES[x.dtype]
+    return code
 
 
 def _device(what, name, x):
     """The device of the first tensor; every other one has to be there too."""
-    if x.device.type != "cuda":
-        raise ValueError(f"{what} requires GPU (HIP) tensors, got {name} on {x.device}")
-    if not _is_gfx950(x.device.index if x.device.index is not None else torch.cuda.current_device()):
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError(f"{what} requires GPU (HIP) tensors, got {name} on {dev}")
+    if not _is_gfx950(dev.index if dev.index is not None else torch.cuda.current_device()):
         raise NotImplementedError(f"{what} supports gfx950 (MI355X) devices only")
-    return x.device
+    return dev
 
 
-def _sequences(name, x, cu_seqlens, inner):
-    """(n, S, leading shape): a dense batch [B, S, ...] or, with cu_seqlens, tokens [T, ...]."""
-    if cu_seqlens is None:
-        if x.dim() != 2 + inner:
-            raise ValueError(f"{name} must have {2 + inner} axes (batch, tokens, ...), got shape {list(x.shape)}")
-        n, S = int(x.shape[0]), int(x.shape[1])
-        lead = (n, S)
-    else:
-        if x.dim() != 1 + inner:
-            raise ValueError(f"{name} must have {1 + inner} axes (tokens, ...) with cu_seqlens, got shape {list(x.shape)}")
-        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
-            raise ValueError("cu_seqlens must have shape [n + 1] with at least one sequence")
-        n, S = int(cu_seqlens.shape[0]) - 1, int(x.shape[0])
-        lead = (S,)
-    if min(n, S) < 1 or x.numel() == 0:
-        raise ValueError(f"{name} must not be empty, got shape {list(x.shape)}")
-    return n, S, lead
+def _fits(name, x, shape, dtype, device):
+    """_check_tensor, without its cost where all is well."""
+    if x.shape != shape or x.dtype != dtype or x.device != device:
+        _check_tensor(name, x, shape, dtype, device)
 
 
-def _cu(cu_seqlens, device):
-    if cu_seqlens is None:
+def _param(name, x, shape, dtype, device):
+    """A tensor that has to be dense (None stays None): checked, a copy where it is not dense. The caller
+    keeps it until the call is queued."""
+    if x is None:
         return None
-    _check_tensor("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, device)
-    return cu_seqlens.contiguous()
+    _fits(name, x, shape, dtype, device)
+    return x if x.is_contiguous() else x.contiguous()
 
 
-def _check(table, dtype, device):
-    """(name, tensor or None, shape, dtype or None for the data dtype) of every tensor."""
-    for name, x, shape, dt in table:
-        if x is not None:
-            _check_tensor(name, x, shape, dt or dtype, device)
+def _data(name, x, shape, dtype, device, inner=1):
+    """A tensor whose last ``inner`` axes have to be dense: checked, a copy where they are not."""
+    if x is None:
+        return None
+    _fits(name, x, shape, dtype, device)
+    return _dense_inner(x, inner)
 
 
 def _dense_inner(x, inner):
     """x as it is if its last ``inner`` axes are dense, else a contiguous copy."""
+    if x.is_contiguous():
+        return x
     step = 1
     for k in range(1, inner + 1):
         if x.shape[-k] != 1 and x.stride(-k) != step:
@@ -126,54 +122,107 @@ def _dense_inner(x, inner):
     return x
 
 
+def _sequences(name, x, cu_seqlens, inner):
+    """(n, S, leading shape): a dense batch [B, S, ...] or, with cu_seqlens, tokens [T, ...]."""
+    shape = tuple(x.shape)
+    if cu_seqlens is None:
+        if len(shape) != 2 + inner:
+            raise ValueError(f"{name} must have {2 + inner} axes (batch, tokens, ...), got shape {list(shape)}")
+        n, S = shape[:2]
+        lead = (n, S)
+    else:
+        if len(shape) != 1 + inner:
+            raise ValueError(f"{name} must have {1 + inner} axes (tokens, ...) with cu_seqlens, got shape {list(shape)}")
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+            raise ValueError("cu_seqlens must have shape [n + 1] with at least one sequence")
+        n, S = cu_seqlens.shape[0] - 1, shape[0]
+        lead = (S,)
+    if 0 in shape:
+        raise ValueError(f"{name} must not be empty, got shape {list(shape)}")
+    return n, S, lead
+
+
+def _cu(cu_seqlens, device):
+    return None if cu_seqlens is None else _param("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, device)
+
+
+_NO_ROWS = (0, 0, 0)
+
+
 def _rows(x, packed):
-    """The mamba_rows view of a tensor whose inner axes are dense (None: no tensor)."""
+    """The mamba_rows fields of a tensor whose inner axes are dense (None: no tensor)."""
     if x is None:
-        return _lib.MambaRows(None, 0, 0)
-    return _lib.MambaRows(x.data_ptr(), 0 if packed else x.stride(0), x.stride(0 if packed else 1))
+        return _NO_ROWS
+    return (x.data_ptr(), 0, x.stride(0)) if packed else (x.data_ptr(), x.stride(0), x.stride(1))
+
+
+def _row(x):
+    """The same for the rows [n, ...] of a step."""
+    return _NO_ROWS if x is None else (x.data_ptr(), x.stride(0), 0)
 
 
 def _ptr(x):
-    return None if x is None else x.data_ptr()
+    return 0 if x is None else x.data_ptr()
 
 
 def _span(x):
     """First and last byte (exclusive) that a tensor's elements lie in."""
-    last = sum((s - 1) * st for s, st in zip(x.shape, x.stride()))
-    return x.data_ptr(), x.data_ptr() + (last + 1) * x.element_size()
+    lo = x.data_ptr()
+    if x.is_contiguous():
+        return lo, lo + x.nbytes
+    return lo, lo + (sum((s - 1) * st for s, st in zip(x.shape, x.stride())) + 1) * x.element_size()
 
 
 def _apart(name, x, others):
-    """A caller's output must not lie over an input."""
+    """A tensor that is written must not lie over one that is read."""
     lo, hi = _span(x)
     for other, y in others:
-        if y is not None and y.numel() and y.device == x.device:
-            a, b = _span(y)
-            if lo < b and a < hi:
-                raise ValueError(f"{name} must not overlap {other}")
+        if y is None:
+            continue
+        p = y.data_ptr()
+        if p < hi and (p >= lo or _span(y)[1] > lo):
+            raise ValueError(f"{name} must not overlap {other}")
 
 
-def _out(out, shape, dtype, device, inputs):
+def _new_like(x):
+    """A dense tensor of x's shape, type and device."""
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
+
+
+def _out(out, x, inputs):
+    """The output: a new tensor like x, or the caller's."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _check_output("out", out, shape, dtype, device)
+        return _new_like(x)
+    _check_output("out", out, x.shape, x.dtype, x.device)
     _apart("out", out, inputs)
     return out
 
 
-def _call(fn, args, device, workspace=None):
-    """Queue one library call on the device's current stream, with its workspace where it has one."""
-    L = _lib.lib()
-    if _lib.LAYER_CALLS[fn][1]:
+_QUEUE = {}   # entry point -> (C function, its workspace query or None, packer of the argument struct)
+
+
+def _call(fn, values, device, workspace=None):
+    """Queue one library call on the device's current stream. ``values``: the fields of its argument struct in
+    order, without the workspace, which is added where the call has one."""
+    entry = _QUEUE.get(fn)
+    if entry is None:
+        L = _lib.lib()
+        cls, ws = _lib.LAYER_CALLS[fn]
+        entry = _QUEUE[fn] = (getattr(L, fn), getattr(L, fn + "_workspace_size") if ws else None, _lib.packer(cls))
+    call, query, pack = entry
+    if query is not None:
         need = ctypes.c_size_t(0)
-        st = getattr(L, fn + "_workspace_size")(ctypes.byref(args), ctypes.byref(need))
+        st = query(pack(*values, 0, 0), ctypes.byref(need))
         if st != _lib.MIMO_OK:
             _raise(st)
         workspace = _workspace(workspace, need.value, device)
-        if workspace is not None:
-            args.workspace, args.workspace_bytes = workspace.data_ptr(), workspace.numel()
-    with torch.cuda.device(device):
-        st = getattr(L, fn)(ctypes.byref(args), torch.cuda.current_stream(device).cuda_stream)
+        values = (*values, 0, 0) if workspace is None else (*values, workspace.data_ptr(), workspace.numel())
+    args, stream = pack(*values), torch._C._cuda_getCurrentRawStream(device.index)
+    if torch.cuda.current_device() == device.index:
+        st = call(args, stream)
+    else:
+        with torch.cuda.device(device):
+            st = call(args, stream)
     if st != _lib.MIMO_OK:
         _raise(st)
 
@@ -188,11 +237,11 @@ def _activation(activation):
 def _check_filter(weight, bias, D, device):
     if weight.dim() != 2 or weight.shape[0] != D:
         raise ValueError(f"weight must have shape [{D}, taps], got {list(weight.shape)}")
-    _check([("weight", weight, weight.shape, _F32), ("bias", bias, (D,), _F32)], None, device)
-    W = int(weight.shape[1])
+    W = weight.shape[1]
+    weight, bias = _param("weight", weight, weight.shape, _F32, device), _param("bias", bias, (D,), _F32, device)
     if not 2 <= W <= 8:
         raise NotImplementedError(f"mamba_conv supports 2 to 8 taps, got {W}")
-    return W
+    return W, weight, bias
 
 
 def mamba_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, *, activation: Optional[str] = None,
@@ -209,16 +258,14 @@ def mamba_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, *,
     code = _data_dtype("x", x)
     silu = _activation(activation)
     n, S, lead = _sequences("x", x, cu_seqlens, 1)
-    D = int(x.shape[-1])
-    W = _check_filter(weight, bias, D, dev)
-    _check([("initial_state", initial_state, (n, W - 1, D), None)], x.dtype, dev)
+    D = x.shape[-1]
+    W, weight, bias = _check_filter(weight, bias, D, dev)
+    initial_state = _param("initial_state", initial_state, (n, W - 1, D), x.dtype, dev)
     cu, x = _cu(cu_seqlens, dev), _dense_inner(x, 1)
-    weight, bias, initial_state = _aligned(weight), _aligned(bias), _aligned(initial_state)
-    res = _out(out, (*lead, D), x.dtype, dev, (("x", x), ("initial_state", initial_state)))
-    state = torch.empty((n, W - 1, D), dtype=x.dtype, device=dev) if return_state else None
-    a = _lib.MambaConvFwdArgs(n, S, D, W, code, silu, int(out is None), _ptr(cu), _rows(x, cu is not None), _ptr(weight),
-                              _ptr(bias), _ptr(initial_state), _ptr(res), _ptr(state))
-    _call("mamba_conv_fwd", a, dev)
+    res = _out(out, x, (("x", x), ("initial_state", initial_state)))
+    state = x.new_empty((n, W - 1, D)) if return_state else None
+    _call("mamba_conv_fwd", (n, S, D, W, code, silu, int(out is None), _ptr(cu), *_rows(x, cu is not None), _ptr(weight),
+                             _ptr(bias), _ptr(initial_state), _ptr(res), _ptr(state)), dev)
     return MambaConvOutputs(res, state)
 
 
@@ -231,45 +278,41 @@ def mamba_conv_bwd(dout, x, weight, bias=None, initial_state=None, dstate=None, 
     code = _data_dtype("x", x)
     silu = _activation(activation)
     n, S, lead = _sequences("x", x, cu_seqlens, 1)
-    D = int(x.shape[-1])
-    W = _check_filter(weight, bias, D, dev)
-    _check([("dout", dout, x.shape, None), ("initial_state", initial_state, (n, W - 1, D), None),
-            ("dstate", dstate, (n, W - 1, D), None)], x.dtype, dev)
-    cu, x, dout = _cu(cu_seqlens, dev), _dense_inner(x, 1), _dense_inner(dout, 1)
-    weight, bias, initial_state, dstate = (_aligned(t) for t in (weight, bias, initial_state, dstate))
-    dx = torch.empty((*lead, D), dtype=x.dtype, device=dev)
-    dweight = torch.empty((D, W), dtype=_F32, device=dev)
-    dbias = None if bias is None else torch.empty((D,), dtype=_F32, device=dev)
-    dinit = None if initial_state is None else torch.empty((n, W - 1, D), dtype=x.dtype, device=dev)
+    D = x.shape[-1]
+    W, weight, bias = _check_filter(weight, bias, D, dev)
+    dout = _data("dout", dout, x.shape, x.dtype, dev)
+    initial_state = _param("initial_state", initial_state, (n, W - 1, D), x.dtype, dev)
+    dstate = _param("dstate", dstate, (n, W - 1, D), x.dtype, dev)
+    cu, x = _cu(cu_seqlens, dev), _dense_inner(x, 1)
+    dx, dweight = _new_like(x), torch.empty_like(weight)
+    dbias = None if bias is None else torch.empty_like(bias)
+    dinit = None if initial_state is None else torch.empty_like(initial_state)
     packed = cu is not None
-    a = _lib.MambaConvBwdArgs(n, S, D, W, code, silu, 0, _ptr(cu), _rows(dout, packed), _rows(x, packed), _ptr(weight), _ptr(bias),
-                              _ptr(initial_state), _ptr(dstate), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(dinit))
-    _call("mamba_conv_bwd", a, dev, workspace)
+    _call("mamba_conv_bwd", (n, S, D, W, code, silu, 0, _ptr(cu), *_rows(dout, packed), *_rows(x, packed), _ptr(weight), _ptr(bias),
+                             _ptr(initial_state), _ptr(dstate), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(dinit)), dev, workspace)
     return MambaConvGrads(dx, dweight, dbias, dinit)
 
 
 def _check_pool(state, inner, dtype, indices, n, device):
     """A pool of states [slots, ...]: dense inside a slot, slots that do not overlap, updated in place."""
-    if state.dim() != 1 + len(inner) or tuple(state.shape[1:]) != tuple(inner):
+    if state.dim() != 3 or state.shape[1:] != inner:
         raise ValueError(f"state must have shape [slots, {', '.join(map(str, inner))}], got {list(state.shape)}")
-    _check_tensor("state", state, state.shape, dtype, device)
-    size = 1
-    for k in (-1, -2):
-        if state.shape[k] != 1 and state.stride(k) != size:
-            raise ValueError("state must be dense inside a slot: it is updated in place")
-        size *= int(state.shape[k])
-    slots = int(state.shape[0])
+    slots, size = state.shape[0], inner[0] * inner[1]
+    _fits("state", state, (slots, *inner), dtype, device)
     if slots < 1:
         raise ValueError("state must have at least one slot")
-    if slots > 1 and state.stride(0) < size:
-        raise ValueError("the slots of state must not overlap")
-    if indices is None:
-        if slots < n:
-            raise ValueError(f"state has {slots} slots for {n} rows: without state_indices each row needs its own")
-    else:
-        _check_tensor("state_indices", indices, (n,), torch.int32, device)
-        indices = indices.contiguous()
-    return slots, state.stride(0) if slots > 1 else size, indices
+    stride = size
+    if not state.is_contiguous():
+        if (inner[1] != 1 and state.stride(2) != 1) or (inner[0] != 1 and state.stride(1) != inner[1]):
+            raise ValueError("state must be dense inside a slot: it is updated in place")
+        stride = state.stride(0) if slots > 1 else size
+        if stride < size:
+            raise ValueError("the slots of state must not overlap")
+    if indices is not None:
+        indices = _param("state_indices", indices, (n,), torch.int32, device)
+    elif slots < n:
+        raise ValueError(f"state has {slots} slots for {n} rows: without state_indices each row needs its own")
+    return slots, stride, indices
 
 
 def mamba_conv_step(x, state, weight, bias=None, state_indices=None, *, activation: Optional[str] = None,
@@ -283,36 +326,34 @@ def mamba_conv_step(x, state, weight, bias=None, state_indices=None, *, activati
     silu = _activation(activation)
     if x.dim() != 2 or x.numel() == 0:
         raise ValueError(f"x must have shape [n, D] and not be empty, got {list(x.shape)}")
-    n, D = (int(s) for s in x.shape)
-    W = _check_filter(weight, bias, D, dev)
+    n, D = x.shape
+    W, weight, bias = _check_filter(weight, bias, D, dev)
     slots, stride, idx = _check_pool(state, (W - 1, D), x.dtype, state_indices, n, dev)
-    x, weight, bias = _dense_inner(x, 1), _aligned(weight), _aligned(bias)
+    x = _dense_inner(x, 1)
     _apart("state", state, (("x", x), ("weight", weight), ("bias", bias), ("state_indices", idx)))
-    res = _out(out, (n, D), x.dtype, dev, (("x", x), ("state", state)))
-    a = _lib.MambaConvStepArgs(n, D, slots, stride, x.stride(0), W, code, silu, 0, _ptr(x), _ptr(state), _ptr(weight), _ptr(bias),
-                               _ptr(idx), _ptr(res))
-    _call("mamba_conv_step", a, dev)
+    res = _out(out, x, (("x", x), ("state", state)))
+    _call("mamba_conv_step", (n, D, slots, stride, x.stride(0), W, code, silu, 0, x.data_ptr(), state.data_ptr(), weight.data_ptr(),
+                              _ptr(bias), _ptr(idx), res.data_ptr()), dev)
     return res
 
 
 # ---------------------------------------------------------------- selective scan
 def _check_scan(u, dt, a, b, c, d, z, dt_bias, lead, dev):
     """Sizes and the tensors with dense inner axes, parameters contiguous."""
-    D = int(u.shape[-1])
+    D, dtype = u.shape[-1], u.dtype
     if a.dim() != 2 or a.shape[0] != D:
         raise ValueError(f"a must have shape [{D}, N], got {list(a.shape)}")
-    N = int(a.shape[1])
-    if b.dim() != len(lead) + 2 or tuple(b.shape[:-2]) != lead or b.shape[-1] != N:
-        raise ValueError(f"b must have shape {[*lead, 'G', N]}, got {list(b.shape)}")
-    G = int(b.shape[-2])
+    N, shape = a.shape[1], b.shape
+    if len(shape) != len(lead) + 2 or shape[:-2] != lead or shape[-1] != N:
+        raise ValueError(f"b must have shape {[*lead, 'G', N]}, got {list(shape)}")
+    G = shape[-2]
     if G < 1 or N < 1 or D % G:
         raise ValueError(f"the {D} channels must be divisible by the {G} groups of b and c, and a must have states")
     if N > 128:
         raise NotImplementedError(f"mamba_scan supports at most 128 states, got {N}")
-    _check([("dt", dt, u.shape, None), ("a", a, (D, N), _F32), ("b", b, (*lead, G, N), None), ("c", c, (*lead, G, N), None),
-            ("d", d, (D,), _F32), ("z", z, u.shape, None), ("dt_bias", dt_bias, (D,), _F32)], u.dtype, dev)
-    data = tuple(None if t is None else _dense_inner(t, k) for t, k in ((u, 1), (dt, 1), (b, 2), (c, 2), (z, 1)))
-    return D, G, N, data, tuple(_aligned(t) for t in (a, d, dt_bias))
+    data = (_dense_inner(u, 1), _data("dt", dt, u.shape, dtype, dev), _data("b", b, shape, dtype, dev, 2), _data("c", c, shape, dtype, dev, 2),
+            _data("z", z, u.shape, dtype, dev))
+    return D, G, N, data, (_param("a", a, (D, N), _F32, dev), _param("d", d, (D,), _F32, dev), _param("dt_bias", dt_bias, (D,), _F32, dev))
 
 
 def mamba_scan_fwd(u, dt, a, b, c, d=None, z=None, dt_bias=None, initial_state=None, cu_seqlens=None, *, dt_softplus: bool = False,
@@ -333,15 +374,13 @@ def mamba_scan_fwd(u, dt, a, b, c, d=None, z=None, dt_bias=None, initial_state=N
     code = _data_dtype("u", u)
     n, S, lead = _sequences("u", u, cu_seqlens, 1)
     D, G, N, (u, dt, b, c, z), (a, d, dt_bias) = _check_scan(u, dt, a, b, c, d, z, dt_bias, lead, dev)
-    _check([("initial_state", initial_state, (n, D, N), _F32)], None, dev)
-    cu, initial_state = _cu(cu_seqlens, dev), _aligned(initial_state)
-    res = _out(out, (*lead, D), u.dtype, dev, (("u", u), ("dt", dt), ("b", b), ("c", c), ("z", z), ("initial_state", initial_state)))
-    state = torch.empty((n, D, N), dtype=_F32, device=dev) if return_state else None
+    cu, initial_state = _cu(cu_seqlens, dev), _param("initial_state", initial_state, (n, D, N), _F32, dev)
+    res = _out(out, u, (("u", u), ("dt", dt), ("b", b), ("c", c), ("z", z), ("initial_state", initial_state)))
+    state = a.new_empty((n, D, N)) if return_state else None
     packed = cu is not None
-    args = _lib.MambaScanFwdArgs(n, S, D, G, N, code, int(bool(dt_softplus)), int(out is None), 0, _ptr(cu),
-                                 *(_rows(t, packed) for t in (u, dt, b, c, z)), _ptr(a), _ptr(d), _ptr(dt_bias),
-                                 _ptr(initial_state), _ptr(res), _ptr(state))
-    _call("mamba_scan_fwd", args, dev, workspace)
+    _call("mamba_scan_fwd", (n, S, D, G, N, code, int(bool(dt_softplus)), int(out is None), 0, _ptr(cu), *_rows(u, packed), *_rows(dt, packed),
+                             *_rows(b, packed), *_rows(c, packed), *_rows(z, packed), _ptr(a), _ptr(d), _ptr(dt_bias), _ptr(initial_state),
+                             _ptr(res), _ptr(state)), dev, workspace)
     return MambaScanOutputs(res, state)
 
 
@@ -355,22 +394,16 @@ def mamba_scan_bwd(dout, u, dt, a, b, c, d=None, z=None, dt_bias=None, initial_s
     code = _data_dtype("u", u)
     n, S, lead = _sequences("u", u, cu_seqlens, 1)
     D, G, N, (u, dt, b, c, z), (a, d, dt_bias) = _check_scan(u, dt, a, b, c, d, z, dt_bias, lead, dev)
-    _check([("dout", dout, u.shape, None), ("initial_state", initial_state, (n, D, N), _F32), ("dstate", dstate, (n, D, N), _F32)],
-           u.dtype, dev)
-    cu, dout, initial_state, dstate = _cu(cu_seqlens, dev), _dense_inner(dout, 1), _aligned(initial_state), _aligned(dstate)
+    dout = _data("dout", dout, u.shape, u.dtype, dev)
+    initial_state = _param("initial_state", initial_state, (n, D, N), _F32, dev)
+    cu, dstate = _cu(cu_seqlens, dev), _param("dstate", dstate, (n, D, N), _F32, dev)
     packed = cu is not None
 
-    def new(*shape, dtype=_F32, like=True):
-        return None if like is None else torch.empty(shape, dtype=dtype, device=dev)
-
-    g = MambaScanGrads(du=new(*lead, D, dtype=u.dtype), ddt=new(*lead, D, dtype=u.dtype), da=new(D, N), db=new(*lead, G, N, dtype=u.dtype),
-                       dc=new(*lead, G, N, dtype=u.dtype), dd=new(D, like=d), dz=new(*lead, D, dtype=u.dtype, like=z),
-                       ddt_bias=new(D, like=dt_bias), dinitial_state=new(n, D, N, like=initial_state))
-    args = _lib.MambaScanBwdArgs(n, S, D, G, N, code, int(bool(dt_softplus)), 0, 0, _ptr(cu),
-                                 *(_rows(t, packed) for t in (dout, u, dt, b, c, z)), _ptr(a), _ptr(d), _ptr(dt_bias),
-                                 _ptr(initial_state), _ptr(dstate), *(_ptr(t) for t in (g.du, g.ddt, g.db, g.dc, g.dz)),
-                                 *(_ptr(t) for t in (g.da, g.dd, g.ddt_bias, g.dinitial_state)))
-    _call("mamba_scan_bwd", args, dev, workspace)
+    g = MambaScanGrads(*(None if t is None else _new_like(t) for t in (u, dt, a, b, c, d, z, dt_bias, initial_state)))
+    _call("mamba_scan_bwd", (n, S, D, G, N, code, int(bool(dt_softplus)), 0, 0, _ptr(cu), *_rows(dout, packed), *_rows(u, packed),
+                             *_rows(dt, packed), *_rows(b, packed), *_rows(c, packed), *_rows(z, packed), _ptr(a), _ptr(d), _ptr(dt_bias),
+                             _ptr(initial_state), _ptr(dstate), _ptr(g.du), _ptr(g.ddt), _ptr(g.db), _ptr(g.dc), _ptr(g.dz), _ptr(g.da),
+                             _ptr(g.dd), _ptr(g.ddt_bias), _ptr(g.dinitial_state)), dev, workspace)
     return g
 
 
@@ -382,16 +415,14 @@ def mamba_scan_step(u, dt, state, a, b, c, d=None, z=None, dt_bias=None, state_i
     code = _data_dtype("u", u)
     if u.dim() != 2 or u.numel() == 0:
         raise ValueError(f"u must have shape [n, D] and not be empty, got {list(u.shape)}")
-    n = int(u.shape[0])
+    n = u.shape[0]
     D, G, N, (u, dt, b, c, z), (a, d, dt_bias) = _check_scan(u, dt, a, b, c, d, z, dt_bias, (n,), dev)
     slots, stride, idx = _check_pool(state, (D, N), _F32, state_indices, n, dev)
     inputs = (("u", u), ("dt", dt), ("b", b), ("c", c), ("z", z))
     _apart("state", state, (*inputs, ("a", a), ("d", d), ("dt_bias", dt_bias), ("state_indices", idx)))
-    res = _out(out, (n, D), u.dtype, dev, (*inputs, ("state", state)))
-    rows = (_lib.MambaRows(None, 0, 0) if t is None else _lib.MambaRows(t.data_ptr(), t.stride(0), 0) for t in (u, dt, b, c, z))
-    args = _lib.MambaScanStepArgs(n, D, G, N, slots, stride, code, int(bool(dt_softplus)), *rows, _ptr(a), _ptr(d), _ptr(dt_bias),
-                                  _ptr(state), _ptr(idx), _ptr(res))
-    _call("mamba_scan_step", args, dev)
+    res = _out(out, u, (*inputs, ("state", state)))
+    _call("mamba_scan_step", (n, D, G, N, slots, stride, code, int(bool(dt_softplus)), *_row(u), *_row(dt), *_row(b), *_row(c), *_row(z),
+                              a.data_ptr(), _ptr(d), _ptr(dt_bias), state.data_ptr(), _ptr(idx), res.data_ptr()), dev)
     return res
 
 
@@ -412,15 +443,17 @@ def _check_norm(what, x, weight, bias, z, groups, eps, gate, activation):
         raise ValueError("activation and a gate z exclude each other")
     if x.dim() < 1 or x.numel() == 0:
         raise ValueError(f"x must have shape [..., D] and not be empty, got {list(x.shape)}")
-    D = int(x.shape[-1])
+    D = x.shape[-1]
     if isinstance(groups, bool) or not isinstance(groups, int) or groups < 1 or D % groups:
         raise ValueError(f"groups must be a positive int that divides the {D} channels, got {groups!r}")
     if not eps >= 0:
         raise ValueError(f"eps must not be negative, got {eps}")
     if D // groups > 8192:
         raise NotImplementedError(f"mamba_norm supports at most 8192 channels in a group, got {D // groups}")
-    _check([("weight", weight, (D,), _F32), ("bias", bias, (D,), _F32), ("z", z, x.shape, None)], x.dtype, dev)
-    return dev, code, silu, D, _row_view(x, D), None if z is None else _row_view(z, D), _aligned(weight), _aligned(bias)
+    if z is not None:
+        _fits("z", z, x.shape, x.dtype, dev)
+        z = _row_view(z, D)
+    return dev, code, silu, D, _row_view(x, D), z, _param("weight", weight, (D,), _F32, dev), _param("bias", bias, (D,), _F32, dev)
 
 
 def mamba_norm_fwd(x, weight, bias=None, z=None, *, groups: int = 1, eps: float = 1e-5, center: bool = False, gate: str = "before",
@@ -433,10 +466,9 @@ def mamba_norm_fwd(x, weight, bias=None, z=None, *, groups: int = 1, eps: float 
     and out = p * silu(z) (z given, gate "after"), silu(p) (activation "silu", without z), or p. x, z, out
     [..., D]; weight, bias [D] float32."""
     dev, code, silu, D, rows, zr, weight, bias = _check_norm("mamba_norm_fwd", x, weight, bias, z, groups, eps, gate, activation)
-    res = _out(out, x.shape, x.dtype, dev, (("x", rows), ("z", zr)))
-    a = _lib.MambaNormFwdArgs(rows.shape[0], D, groups, rows.stride(0), 0 if zr is None else zr.stride(0), code, int(bool(center)),
-                              int(gate == "after"), silu, eps, 0, _ptr(rows), _ptr(zr), _ptr(weight), _ptr(bias), _ptr(res))
-    _call("mamba_norm_fwd", a, dev)
+    res = _out(out, x, (("x", rows), ("z", zr)))
+    _call("mamba_norm_fwd", (rows.shape[0], D, groups, rows.stride(0), 0 if zr is None else zr.stride(0), code, int(bool(center)),
+                             int(gate == "after"), silu, eps, 0, _ptr(rows), _ptr(zr), _ptr(weight), _ptr(bias), _ptr(res)), dev)
     return res
 
 
@@ -445,14 +477,11 @@ def mamba_norm_bwd(dout, x, weight, bias=None, z=None, *, groups: int = 1, eps: 
     """Gradients of ``sum(out * dout)`` for the arguments of ``mamba_norm_fwd``: dx and dz in x's dtype, dweight and
     dbias float32; dbias and dz are None without the input. The statistics are recomputed from x and z."""
     dev, code, silu, D, rows, zr, weight, bias = _check_norm("mamba_norm_bwd", x, weight, bias, z, groups, eps, gate, activation)
-    _check([("dout", dout, x.shape, None)], x.dtype, dev)
+    _fits("dout", dout, x.shape, x.dtype, dev)
     dr = _row_view(dout, D)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    dz = None if z is None else torch.empty(x.shape, dtype=x.dtype, device=dev)
-    dweight = torch.empty((D,), dtype=_F32, device=dev)
-    dbias = None if bias is None else torch.empty((D,), dtype=_F32, device=dev)
-    a = _lib.MambaNormBwdArgs(rows.shape[0], D, groups, dr.stride(0), rows.stride(0), 0 if zr is None else zr.stride(0), code,
-                              int(bool(center)), int(gate == "after"), silu, eps, 0, _ptr(dr), _ptr(rows), _ptr(zr), _ptr(weight),
-                              _ptr(bias), _ptr(dx), _ptr(dz), _ptr(dweight), _ptr(dbias))
-    _call("mamba_norm_bwd", a, dev, workspace)
+    dx, dweight = _new_like(x), torch.empty_like(weight)
+    dz, dbias = None if z is None else _new_like(z), None if bias is None else torch.empty_like(bias)
+    _call("mamba_norm_bwd", (rows.shape[0], D, groups, dr.stride(0), rows.stride(0), 0 if zr is None else zr.stride(0), code,
+                             int(bool(center)), int(gate == "after"), silu, eps, 0, _ptr(dr), _ptr(rows), _ptr(zr), _ptr(weight),
+                             _ptr(bias), _ptr(dx), _ptr(dz), _ptr(dweight), _ptr(dbias)), dev, workspace)
     return MambaNormGrads(dx, dweight, dbias, dz)
