@@ -57,17 +57,16 @@ __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2
 __device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + exp2_hw(-LOG2E * x)); }
 // d silu(x) / dx from g = sigmoid(x)
 __device__ __forceinline__ float silu_slope(float x, float g) { return g * __builtin_fmaf(x, 1.f - g, 1.f); }
-// softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|). The product -|x| log2(e) is carried
-// with its rounding error, so that e is good to about 1e-7 for large |x| too; log1p(e)/e on
-// [0, 1] is a polynomial of degree 9 (interpolated at Chebyshev nodes: 1e-7 relative in fp32),
-// so small step sizes keep their relative precision. NaN passes (max takes the other operand,
-// the product does not).
+// softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|). The error of |x| log2(e) rounded is put back, so that e is
+// good to about 1e-7 for large |x| too; log1p(e)/e on [0, 1] is a polynomial of degree 9 (interpolated at
+// Chebyshev nodes: 1e-7 relative in fp32), so small step sizes keep their relative precision. Beyond
+// |x| = 100, e is below fp32's range. NaN passes through the first term.
 __device__ __forceinline__ float softplus(float x) {
-    const float m = -__builtin_fabsf(x);
-    const float hi = m * LOG2E;
-    const float lo = __builtin_fmaf(m, LOG2E, -hi) + m * 1.92596299e-8f;   // log2(e) - fp32(log2(e))
+    const float m = __builtin_fminf(__builtin_fabsf(x), 100.f), hi = -LOG2E * m;
+    float r = __builtin_fmaf(hi, -LN2, -m);
+    r = __builtin_fmaf(hi, 1.904654323e-9f, r);     // fp32(ln 2) - ln 2
     float e = exp2_hw(hi);
-    if (hi > -150.f) e = __builtin_fmaf(e * LN2, lo, e);                       // not for m = -inf
+    e = __builtin_fmaf(e, r, e);
     float q = -3.176057013e-03f;
     q = __builtin_fmaf(q, e, 1.954252645e-02f);
     q = __builtin_fmaf(q, e, -5.637361109e-02f);
@@ -78,7 +77,7 @@ __device__ __forceinline__ float softplus(float x) {
     q = __builtin_fmaf(q, e, 3.332971036e-01f);
     q = __builtin_fmaf(q, e, -4.999989271e-01f);
     q = __builtin_fmaf(q, e, 1.f);
-    return __builtin_fmaf(q, e, __builtin_fmaxf(x, 0.f));
+    return __builtin_fmaf(q, e, x < 0.f ? 0.f : x);
 }
 
 // ---------------------------------------------------------------- lane exchanges

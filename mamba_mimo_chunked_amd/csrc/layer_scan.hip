@@ -110,9 +110,10 @@ mimo_status plan_fwd(const mamba_scan_fwd_args* a, FwdPlan* pl) {
     const bool packed = a->cu_seqlens != nullptr;
     pl->tpg = (int)((a->D / a->G + 63) / 64);
     const int64_t waves = a->G * pl->tpg * waves_for(a->N), T = packed ? a->S : a->n * a->S;
-    int64_t CH = (T * waves / 2048 + TT - 1) / TT * TT;
+    int64_t CH = (T * waves / 3072 + 15) / 16 * 16;
+    if (CH < 64) CH = (T * waves / 2048 + 15) / 16 * 16 < 64 ? (T * waves / 2048 + 15) / 16 * 16 : 64;
     CH = CH < 32 ? 32 : CH > 4096 ? 4096 : CH;
-    if (a->S <= 64 || (!packed && a->n * waves >= 512)) CH = (a->S + TT - 1) / TT * TT;
+    if (a->S <= 64 || (!packed && a->n * waves >= 512)) CH = (a->S + 15) / 16 * 16;
     pl->q = Seqs{a->cu_seqlens, (int)a->n, (int)a->S, (int)CH, (int)((a->S + CH - 1) / CH)};
     pl->slots = slots_of(pl->q);
     if (pl->slots > 0x7fffffffL) return unsupported("too many tokens");
@@ -126,7 +127,7 @@ template <int DT> mimo_status run_fwd(const ScanParams& p, hipStream_t st) {
     if (p.chunked) {
         mimo_status s = launch_walk<DT, AGG>(p, st);
         if (s != MIMO_OK) return s;
-        s = launch(&k_carry<false>, dim3((p.D + 255) / 256, p.N, p.q.n), 256, 0, st, p);
+        s = launch_carry<false>(p, p.q.nc, st);
         if (s != MIMO_OK) return s;
     }
     return launch_walk<DT, FWD>(p, st);
@@ -168,6 +169,7 @@ mimo_status mamba_scan_fwd(const mamba_scan_fwd_args* a, void* stream) {
     p.agg = static_cast<float*>(a->workspace);
     p.sdt = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + pl.off_sdt);
     p.slots = pl.slots;
+    p.vec = p.N % 4 == 0 && aligned(p.a, 0, 0, 16, 1) && aligned(p.init, 0, 0, 16, 1) && aligned(p.state, 0, 0, 16, 1);
     if ((s = require_gfx950()) != MIMO_OK) return s;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     return a->dtype == BF16 ? run_fwd<BF16>(p, st) : a->dtype == F16 ? run_fwd<F16>(p, st) : run_fwd<F32>(p, st);

@@ -22,21 +22,21 @@ namespace layer {
 struct ScanParams {
     Seqs q;
     int D, G, N, Dg, tpg;           // channels, groups, states, channels and channel tiles of a group
-    int softplus, zero_tail, chunked, has_z;
+    int softplus, zero_tail, chunked, has_z, vec;   // vec: rows of N floats in 16-byte accesses
     Rows u, dt, b, c, z, dout;
     const float *a, *d, *bias;
     const float *init, *dstate;
     void* out;
     float* state;
-    float *agg, *gagg, *sdt;        // [slots][N][D] twice, [slots][D]
+    float *agg, *gagg, *sdt;        // [slots][D][N] twice, [slots][D]
     // backward
     void *du, *ddt, *db, *dc, *dz;
     float *da, *dd, *dbias, *dinit;
     float *pbc, *pdd;               // [tpg][tokens][G][2][N], [slots][2][D]
+    float *uh, *udt;                // units of a chunk: state from zero and sum of dt in front, [slots * units][D][N] and [..][D]
+    int units;                      // of a chunk: CH / UNIT
     long slots, tokens;
 };
-
-constexpr int TT = 16;   // tokens of a tile
 
 // first row of the flat token axis of a place
 __device__ __forceinline__ long flat_row(const Seqs& q, const Place& pl) { return q.cu ? (long)pl.row0 : (long)pl.i * q.S; }
@@ -54,190 +54,286 @@ template <int CPB> __device__ __forceinline__ Tile tile_of(const ScanParams& p, 
     return t;
 }
 
+// K floats of a row of N, from state n0 on, `none` past the row
+template <int K> __device__ __forceinline__ void load_states(const float* row, int n0, int N, bool vec, float none, float (&x)[K]) {
+#pragma unroll
+    for (int k = 0; k < K; k += 4) {
+        if (vec && n0 + k < N) {
+            const float4 v = *reinterpret_cast<const float4*>(row + n0 + k);
+            x[k] = v.x, x[k + 1] = v.y, x[k + 2] = v.z, x[k + 3] = v.w;
+        } else {
+#pragma unroll
+            for (int i = k; i < k + 4; ++i) x[i] = !vec && n0 + i < N ? row[n0 + i] : none;
+        }
+    }
+}
+template <int K> __device__ __forceinline__ void store_states(float* row, int n0, int N, bool vec, const float (&x)[K]) {
+#pragma unroll
+    for (int k = 0; k < K; k += 4) {
+        if (vec) {
+            if (n0 + k < N) *reinterpret_cast<float4*>(row + n0 + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+        } else {
+#pragma unroll
+            for (int i = k; i < k + 4; ++i)
+                if (n0 + i < N) row[n0 + i] = x[i];
+        }
+    }
+}
+// the decay's base: exp(dt a) = exp2(dt * decay_base(a)); finite, so that a step of zero is no decay for a = -inf too
+__device__ __forceinline__ float decay_base(float a) { return __builtin_fmaxf(a * LOG2E, -3e38f); }
+
 // FWD: the outputs. AGG: a chunk's last state from zero. AGG2: also the adjoint that leaves it to the
 // left, sum_t exp(a sum_{s <= t} dt) c[t] dy[t], from the same exponentials.
 enum { FWD, AGG, AGG2 };
+#ifndef WALK_WAVES
+#define WALK_WAVES 2
+#endif
 
-template <int DT, int NS, int KS, int MODE> __global__ __launch_bounds__(64 * KS) void k_walk(ScanParams p) {
+constexpr int UNIT = 16;   // tokens of a unit (backward)
+
+// tokens of a tile: what a lane keeps in registers, or the waves of a block share in LDS
+constexpr int tile_tokens(int KS) { return KS == 1 ? 8 : 16; }
+
+template <int DT, int NS, int KS, int MODE> __global__ __launch_bounds__(64 * KS, KS == 1 ? WALK_WAVES : 2) void k_walk(ScanParams p) {
     typedef raw_t<DT> raw;
-    constexpr int NP = NS * KS, TPW = (TT + KS - 1) / KS, NB = (TT * NP) / (64 * KS);
-    constexpr bool C = MODE != AGG, OUT = MODE == FWD;
-    __shared__ float s_dt[TT][64], s_du[TT][64], s_dy[MODE == AGG2 ? TT : 1][64];
+    constexpr int TT = tile_tokens(KS), NP = NS * KS, TPW = TT / KS, NB = (TT * NP + 64 * KS - 1) / (64 * KS);
+    constexpr bool C = MODE != AGG, OUT = MODE == FWD, ONE = KS == 1;
+    __shared__ float s_dt[ONE ? 1 : TT][64], s_du[ONE ? 1 : TT][64], s_dy[!ONE && MODE == AGG2 ? TT : 1][64];
     __shared__ __attribute__((aligned(16))) float s_b[TT][NP], s_c[C ? TT : 1][NP];
-    __shared__ float s_y[OUT ? KS : 1][OUT ? TT : 1][64];
+    __shared__ float s_y[OUT && !ONE ? KS : 1][OUT && !ONE ? TT : 1][64];
     const Place pl = place(p.q, blockIdx.x);
     if (!pl.ok) return;
     const int t0 = pl.j * p.q.CH, t1 = min(t0 + p.q.CH, pl.len);
     if (MODE == AGG && (pl.i == p.q.n || t1 == pl.len)) return;
     if (MODE == AGG2 && pl.i == p.q.n) return;
-    const int lane = threadIdx.x & 63, w = KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, w = ONE ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Tile tile = tile_of<64>(p, blockIdx.y);
     const bool act = lane < tile.left;
-    const int d = tile.c0 + (act ? lane : 0);
+    const unsigned off = act ? lane : 0;    // rows are addressed as a scalar base and this offset
+    const int d = tile.c0 + off;
     const long D = p.D;
-    raw* out = static_cast<raw*>(p.out) + flat_row(p.q, pl) * D + d;
+    raw* out = static_cast<raw*>(p.out) + flat_row(p.q, pl) * D + tile.c0;
     if (OUT && pl.i == p.q.n) {
         if (p.zero_tail && act)
-            for (int t = t0 + w; t < t1; t += KS) out[t * D] = to_raw<DT>(0.f);
+            for (int t = t0 + w; t < t1; t += KS) (out + t * D)[off] = to_raw<DT>(0.f);
         return;
     }
-    const raw *u = at<DT>(p.u, pl) + d, *dt = at<DT>(p.dt, pl) + d;
-    const raw *z = p.has_z ? at<DT>(p.z, pl) + d : nullptr, *dout = MODE == AGG2 ? at<DT>(p.dout, pl) + d : nullptr;
+    const raw *u = at<DT>(p.u, pl) + tile.c0, *dt = at<DT>(p.dt, pl) + tile.c0;
+    const raw *z = p.has_z ? at<DT>(p.z, pl) + tile.c0 : nullptr, *dout = MODE == AGG2 ? at<DT>(p.dout, pl) + tile.c0 : nullptr;
     const raw *b = at<DT>(p.b, pl) + tile.g * p.N, *c = C ? at<DT>(p.c, pl) + tile.g * p.N : nullptr;
     const float bias = p.bias ? p.bias[d] : 0.f, skip = OUT && p.d ? p.d[d] : 0.f;
 
     float a[NS], h[NS], gr[MODE == AGG2 ? NS : 1], pr[MODE == AGG2 ? NS : 1];
     float total = 0.f;
+    load_states(p.a + d * (long)p.N, w * NS, p.N, p.vec, 0.f, a);
+    const float* from = !OUT ? nullptr : p.chunked ? p.agg + blockIdx.x * D * p.N : p.init ? p.init + pl.i * D * p.N : nullptr;
+    if (from) load_states(from + d * (long)p.N, w * NS, p.N, p.vec, 0.f, h);
 #pragma unroll
     for (int k = 0; k < NS; ++k) {
-        const int n = w * NS + k;
-        a[k] = n < p.N ? p.a[(long)d * p.N + n] * LOG2E : 0.f;
-        h[k] = 0.f;
+        a[k] = decay_base(a[k]);
+        if (!from) h[k] = 0.f;
         if (MODE == AGG2) gr[k] = 0.f, pr[k] = 1.f;
-        if (OUT && n < p.N) {
-            if (p.chunked) h[k] = p.agg[((long)blockIdx.x * p.N + n) * D + d];
-            else if (p.init) h[k] = p.init[((long)pl.i * D + d) * p.N + n];
-        }
     }
 
     raw r_dt[TPW], r_u[TPW], r_z[TPW], r_g[TPW], r_b[NB], r_c[NB];
+    // this thread's elements of b and c: rows e / NP + t0, from tile to tile TT rows on
+    const int e0 = threadIdx.x, bn = e0 % NP, br = e0 / NP;
+    constexpr int BR = 64 * KS / NP;            // rows between a thread's elements
+    const bool bon = bn < p.N && (64 * KS <= TT * NP || e0 < TT * NP);
+    const raw *pb = b + (long)(t0 + br) * p.b.ts + bn, *pc = C ? c + (long)(t0 + br) * p.c.ts + bn : nullptr;
     auto fetch = [&](int t) {
 #pragma unroll
         for (int k = 0; k < TPW; ++k) {
             const long row = min(t + w * TPW + k, t1 - 1);
-            if (w * TPW + k < TT) {
-                r_dt[k] = dt[row * p.dt.ts];
-                r_u[k] = u[row * p.u.ts];
-                if (C && z) r_z[k] = z[row * p.z.ts];
-                if (MODE == AGG2) r_g[k] = dout[row * p.dout.ts];
-            }
+            r_dt[k] = (dt + row * p.dt.ts)[off];
+            r_u[k] = (u + row * p.u.ts)[off];
+            if (C && z) r_z[k] = (z + row * p.z.ts)[off];
+            if (MODE == AGG2) r_g[k] = (dout + row * p.dout.ts)[off];
         }
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-            const int e = threadIdx.x + k * 64 * KS, n = e % NP;
-            const long row = min(t + e / NP, t1 - 1);
-            r_b[k] = n < p.N ? b[row * p.b.ts + n] : raw(0);
-            if (C) r_c[k] = n < p.N ? c[row * p.c.ts + n] : raw(0);
+            const bool on = bon && t + br + k * BR < t1;
+            r_b[k] = raw(0);
+            if (on) r_b[k] = pb[(long)k * BR * p.b.ts];
+            if (C) {
+                r_c[k] = raw(0);
+                if (on) r_c[k] = pc[(long)k * BR * p.c.ts];
+            }
         }
+        pb += (long)TT * p.b.ts;
+        if (C) pc += (long)TT * p.c.ts;
+    };
+    // one token of step v: the states, and <c, h> (or, with dy = g, the adjoint). A step of zero changes nothing: so
+    // pass the tokens of a tile behind the chunk.
+    auto token = [&](int t, float v, float vu, float g) {
+        float y[2] = {0.f, 0.f};
+        if (MODE != FWD) total += v;
+#pragma unroll
+        for (int k = 0; k < NS; ++k) {
+            const float e = exp2_hw(v * a[k]);
+            h[k] = __builtin_fmaf(e, h[k], vu * s_b[t][w * NS + k]);
+            if (OUT) y[k & 1] = __builtin_fmaf(h[k], s_c[t][w * NS + k], y[k & 1]);
+            if (MODE == AGG2) {
+                pr[k] *= e;
+                gr[k] = __builtin_fmaf(pr[k], g * s_c[t][w * NS + k], gr[k]);
+            }
+        }
+        return y[0] + y[1];
     };
     if (t0 < t1) fetch(t0);
     for (int tt = t0; tt < t1; tt += TT) {
-        float fu[TPW], fz[TPW];
+        float f_v[TPW], f_u[TPW], f_z[TPW], f_g[TPW];   // step, input, gate, dy of this wave's tokens
 #pragma unroll
         for (int k = 0; k < TPW; ++k) {
-            const int t = w * TPW + k;
-            if (t < TT) {
-                const float x = to_f<DT>(r_dt[k]) + bias, v = p.softplus ? softplus(x) : x;
-                fu[k] = to_f<DT>(r_u[k]);
-                s_dt[t][lane] = v;
-                s_du[t][lane] = v * fu[k];
-                if (OUT) fz[k] = z ? to_f<DT>(r_z[k]) : 0.f;
-                if (MODE == AGG2) {
-                    float dy = to_f<DT>(r_g[k]);
-                    if (z) {
-                        const float x = to_f<DT>(r_z[k]);
-                        dy *= x * sigmoid(x);
-                    }
-                    s_dy[t][lane] = dy;
-                }
+            f_v[k] = to_f<DT>(r_dt[k]) + bias;
+            f_u[k] = to_f<DT>(r_u[k]);
+            f_z[k] = 1.f;
+        }
+        if (p.softplus) {
+#pragma unroll
+            for (int k = 0; k < TPW; ++k) f_v[k] = softplus(f_v[k]);
+        }
+        if (C && z) {
+#pragma unroll
+            for (int k = 0; k < TPW; ++k) {
+                const float x = to_f<DT>(r_z[k]);
+                f_z[k] = x * sigmoid(x);
+            }
+        }
+        if (tt + TT > t1) {
+#pragma unroll
+            for (int k = 0; k < TPW; ++k)
+                if (tt + w * TPW + k >= t1) f_v[k] = f_u[k] = f_z[k] = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < TPW; ++k) {
+            f_g[k] = MODE == AGG2 ? to_f<DT>(r_g[k]) * f_z[k] : 0.f;
+            if (!ONE) {
+                s_dt[w * TPW + k][lane] = f_v[k];
+                s_du[w * TPW + k][lane] = f_v[k] * f_u[k];
+                if (MODE == AGG2) s_dy[w * TPW + k][lane] = f_g[k];
             }
         }
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-            const int e = threadIdx.x + k * 64 * KS;
-            s_b[e / NP][e % NP] = to_f<DT>(r_b[k]);
-            if (C) s_c[e / NP][e % NP] = to_f<DT>(r_c[k]);
+            if (64 * KS > TT * NP && e0 >= TT * NP) continue;
+            s_b[br + k * BR][bn] = to_f<DT>(r_b[k]);
+            if (C) s_c[br + k * BR][bn] = to_f<DT>(r_c[k]);
         }
         __syncthreads();
         if (tt + TT < t1) fetch(tt + TT);
-        const int cnt = min(TT, t1 - tt);
-#pragma unroll 2
-        for (int t = 0; t < cnt; ++t) {
-            const float v = s_dt[t][lane], vu = s_du[t][lane];
-            const float g = MODE == AGG2 ? s_dy[t][lane] : 0.f;
-            float y[4] = {0.f, 0.f, 0.f, 0.f};
-            if (MODE != FWD) total += v;
-#pragma unroll
-            for (int k = 0; k < NS; ++k) {
-                const float e = exp2_hw(v * a[k]);
-                h[k] = __builtin_fmaf(e, h[k], vu * s_b[t][w * NS + k]);
-                if (OUT) y[k & 3] = __builtin_fmaf(h[k], s_c[t][w * NS + k], y[k & 3]);
-                if (MODE == AGG2) {
-                    pr[k] *= e;
-                    gr[k] = __builtin_fmaf(pr[k], g * s_c[t][w * NS + k], gr[k]);
-                }
+        if constexpr (MODE == AGG2) {   // the backward pass starts again from every unit
+            const int k = (tt - t0) / UNIT;
+            if (k > 0 && (tt - t0) % UNIT == 0 && act) {
+                const long at = (long)blockIdx.x * p.units + k;
+                store_states(p.uh + (at * D + d) * p.N, w * NS, p.N, p.vec, h);
+                if (w == 0) p.udt[at * D + d] = total;
             }
-            if (OUT) s_y[w][t][lane] = (y[0] + y[1]) + (y[2] + y[3]);
+        }
+        if (ONE) {
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                const float y = token(t, f_v[t], f_v[t] * f_u[t], f_g[t]);
+                if (OUT && act && tt + t < t1) (out + (tt + t) * D)[off] = to_raw<DT>(__builtin_fmaf(skip, f_u[t], y) * f_z[t]);
+            }
+        } else {
+#pragma unroll 4
+            for (int t = 0; t < TT; ++t) {
+                const float y = token(t, s_dt[t][lane], s_du[t][lane], MODE == AGG2 ? s_dy[t][lane] : 0.f);
+                if (OUT) s_y[w][t][lane] = y;
+            }
         }
         __syncthreads();
-        if (OUT && act) {
+        if (OUT && !ONE && act) {
 #pragma unroll
             for (int k = 0; k < TPW; ++k) {
                 const int t = w * TPW + k;
-                if (t < cnt) {
-                    float y = skip * fu[k];
+                if (tt + t < t1) {
+                    float y = skip * f_u[k];
 #pragma unroll
                     for (int v = 0; v < KS; ++v) y += s_y[v][t][lane];
-                    if (z) y *= fz[k] * sigmoid(fz[k]);
-                    out[(tt + t) * D] = to_raw<DT>(y);
+                    (out + (tt + t) * D)[off] = to_raw<DT>(y * f_z[k]);
                 }
             }
         }
     }
     if (!act) return;
-#pragma unroll
-    for (int k = 0; k < NS; ++k) {
-        const int n = w * NS + k;
-        if (n >= p.N) continue;
-        if (OUT) {
-            if (p.state && t1 == pl.len) p.state[((long)pl.i * D + d) * p.N + n] = h[k];
-        } else {
-            p.agg[((long)blockIdx.x * p.N + n) * D + d] = h[k];
-            if (MODE == AGG2) p.gagg[((long)blockIdx.x * p.N + n) * D + d] = gr[k];
-        }
-    }
-    if (!OUT && w == 0) p.sdt[(long)blockIdx.x * D + d] = total;
+    float* to = !OUT ? p.agg + blockIdx.x * D * p.N : p.state && t1 == pl.len ? p.state + pl.i * D * p.N : nullptr;
+    if (to) store_states(to + d * (long)p.N, w * NS, p.N, p.vec, h);
+    if constexpr (MODE == AGG2) store_states(p.gagg + (blockIdx.x * D + d) * p.N, w * NS, p.N, p.vec, gr);
+    if (!OUT && w == 0) p.sdt[blockIdx.x * D + d] = total;
 }
 
-// The states that enter the chunks of sequence blockIdx.z, in place of the aggregates: a thread for each
-// (channel, state blockIdx.y), AHEAD chunks of loads in flight. With ADJ, odd blockIdx.y run the adjoints
-// from the last chunk to the first, from dstate, and leave the gradient of the initial state.
-constexpr int AHEAD = 8;
-template <bool ADJ> __global__ __launch_bounds__(256) void k_carry(ScanParams p) {
-    const int d = blockIdx.x * 256 + threadIdx.x, i = blockIdx.z;
-    const int n = ADJ ? blockIdx.y >> 1 : blockIdx.y;
-    const bool rev = ADJ && (blockIdx.y & 1);
-    if (d >= p.D) return;
-    const long D = p.D, N = p.N, step = N * D;
+// The states that enter the chunks of sequence blockIdx.z, in place of the aggregates, for 64 times V of the
+// D * N states.
+// Wave w of a block takes SPAN chunks of every SPAN * waves: it folds them from zero, the waves'
+// folds are chained in LDS, and it walks them again from what enters them, so that all loads of up to 128 chunks
+// are in flight together. With ADJ, blockIdx.y = 1 runs the adjoints from the last chunk to the first, from dstate,
+// and leave the gradient of the initial state.
+constexpr int SPAN = 8, SPAN_WAVES = 16;
+template <bool ADJ, int V> __global__ __launch_bounds__(64 * SPAN_WAVES) void k_carry(ScanParams p) {
+    typedef float vec __attribute__((ext_vector_type(V)));
+    __shared__ vec s_h[SPAN_WAVES][64], s_p[SPAN_WAVES][64];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    const int i = blockIdx.z;
+    const unsigned step = (unsigned)p.D * p.N, s = min((blockIdx.x * 64 + lane) * V, step - V), d = s / (unsigned)p.N;
+    const bool rev = ADJ && blockIdx.y, act = (blockIdx.x * 64 + lane) * V < step;
+    const long D = p.D;
     const int slot0 = p.q.cu ? p.q.base(i) : i * p.q.nc;
     const int len = p.q.cu ? max((i < p.q.n ? p.q.start(i + 1) : p.q.S) - p.q.start(i), 0) : p.q.S;
     const int nc = max((len + p.q.CH - 1) / p.q.CH, 1);
-    const float a = p.a[d * N + n] * LOG2E;
-    const long own = ((long)i * D + d) * N + n;
-    const float* from = rev ? p.dstate : p.init;
-    float h = from ? from[own] : 0.f;
-    float* agg = (rev ? p.gagg : p.agg) + (long)slot0 * step + n * D + d;
-    const float* sdt = p.sdt + (long)slot0 * D + d;
-    // FWD has no aggregate of the last chunk, and needs none
-    for (int j0 = 0; j0 < nc; j0 += AHEAD) {
-        float x[AHEAD], s[AHEAD];
+    const int have = ADJ ? (len > 0 ? nc : 0) : nc - 1;    // chunks with an aggregate: FWD needs none of the last
+    auto get = [](const float* x) { return *reinterpret_cast<const vec*>(x); };
+    vec a = get(p.a + s);
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            const int j = min(j0 + k, nc - 1), at = rev ? nc - 1 - j : j;
-            const bool have = ADJ ? len > 0 : j < nc - 1;
-            x[k] = have ? agg[at * step] : 0.f;
-            s[k] = have ? sdt[(long)at * D] : 0.f;
+    for (int v = 0; v < V; ++v) a[v] = decay_base(a[v]);
+    const long own = (long)i * step + s;
+    const float* from = rev ? p.dstate : p.init;
+    vec h = from ? get(from + own) : vec(0.f);
+    float* agg = (rev ? p.gagg : p.agg) + (long)slot0 * step + s;
+    const float* sdt = p.sdt + (long)slot0 * D + d;
+    for (int j0 = 0; j0 < nc; j0 += SPAN * waves) {
+        vec x[SPAN], e[SPAN], fold = vec(0.f), prod = vec(1.f);
+        float dt[SPAN];
+#pragma unroll
+        for (int k = 0; k < SPAN; ++k) {
+            const int j = j0 + w * SPAN + k, at = rev ? nc - 1 - j : j;
+            x[k] = j < have ? get(agg + (long)at * step) : vec(0.f);
+            dt[k] = j < have ? sdt[(long)at * D] : 0.f;
         }
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            const int j = j0 + k;
-            if (j < nc) {
-                agg[(rev ? nc - 1 - j : j) * step] = h;
-                h = __builtin_fmaf(exp2_hw(a * s[k]), h, x[k]);
+        for (int k = 0; k < SPAN; ++k)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                e[k][v] = exp2_hw(a[v] * dt[k]);
+                fold[v] = __builtin_fmaf(e[k][v], fold[v], x[k][v]);
+                prod[v] *= e[k][v];
             }
+        vec g = h;
+        if (waves > 1) {
+            s_h[w][lane] = fold;
+            s_p[w][lane] = prod;
+            __syncthreads();
+            for (int o = 0; o < waves; ++o) {
+                if (o == w) g = h;
+                const vec f = s_h[o][lane], q = s_p[o][lane];
+#pragma unroll
+                for (int v = 0; v < V; ++v) h[v] = __builtin_fmaf(q[v], h[v], f[v]);
+            }
+            __syncthreads();
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) h[v] = __builtin_fmaf(prod[v], h[v], fold[v]);
+        }
+#pragma unroll
+        for (int k = 0; k < SPAN; ++k) {
+            const int j = j0 + w * SPAN + k;
+            if (j < nc && act) *reinterpret_cast<vec*>(agg + (long)(rev ? nc - 1 - j : j) * step) = g;
+#pragma unroll
+            for (int v = 0; v < V; ++v) g[v] = __builtin_fmaf(e[k][v], g[v], x[k][v]);
         }
     }
-    if (rev && p.dinit) p.dinit[own] = h;
+    if (rev && p.dinit && w == 0 && act) *reinterpret_cast<vec*>(p.dinit + own) = h;
 }
 
 // ---------------------------------------------------------------- host side
@@ -250,6 +346,13 @@ template <int DT, int MODE> mimo_status launch_walk(const ScanParams& p, hipStre
     if (p.N <= 32) return launch(&k_walk<DT, 16, 2, MODE>, grid, 128, 0, st, p);
     if (p.N <= 64) return launch(&k_walk<DT, 16, 4, MODE>, grid, 256, 0, st, p);
     return launch(&k_walk<DT, 16, 8, MODE>, grid, 512, 0, st, p);
+}
+// at most `chunks` chunks in a sequence
+template <bool ADJ> mimo_status launch_carry(const ScanParams& p, long chunks, hipStream_t st) {
+    const long waves = (chunks + SPAN - 1) / SPAN;
+    const int V = p.vec ? 4 : 1, block = 64 * (int)(waves < SPAN_WAVES ? waves : SPAN_WAVES);
+    const dim3 grid((unsigned)(((long)p.D * p.N / V + 63) / 64), ADJ ? 2 : 1, p.q.n);
+    return p.vec ? launch(&k_carry<ADJ, 4>, grid, block, 0, st, p) : launch(&k_carry<ADJ, 1>, grid, block, 0, st, p);
 }
 inline int waves_for(int64_t N) { return N <= 16 ? 1 : N <= 32 ? 2 : N <= 64 ? 4 : 8; }
 

@@ -10,11 +10,11 @@
 // k_scan_bwd. A wave holds 64 / Q channels; the Q lanes of a channel hold NS states each, so <c, h>,
 // <g, b> and <X, a> are sums over Q neighbouring lanes, and the sums over channels (db, dc) are folds
 // of NS values over the 64 / Q others: each fold halves the values a lane keeps, two operations a
-// pair. A block walks its chunk forward in sub-tiles of ST tokens and keeps the state in front of each in
-// LDS, then takes the sub-tiles from the last to the first: forward once more with the states and
-// decays of its ST tokens in registers (2 * NS * ST = 128), then backward through them. So each
-// exponential is computed three times in all (aggregate, walk, sub-tile), and no state but the chunks'
-// goes to memory.
+// pair. A chunk is taken in units of 16 tokens from the last to the first, a unit in sub-tiles of ST
+// tokens likewise: forward with the states and decays of its ST tokens in registers (2 * NS * ST = 128),
+// then backward through them. The state in front of a unit comes from the walk, which leaves it (from
+// zero, at the chunk's start) with the sum of dt to there: h = uh + exp(a udt) h(chunk). So an
+// exponential is computed twice (walk, sub-tile) and no state but every sixteenth goes to memory.
 #include "layer_scan.hpp"
 
 namespace mimo {
@@ -22,13 +22,11 @@ namespace layer {
 namespace {
 
 // channels of a block, LDS floats: staging of dt, dt u, dy, three sums; b, c; fold results of four
-// waves; checkpoints
+// waves; the states in front of a unit's later sub-tiles
 template <int NS, int Q> struct Shape {
     static constexpr int ST = 64 / NS, NP = NS * Q, CPW = 64 / Q, CPB = 4 * CPW;
     static constexpr int ROWS = ST * CPB, BC = ST * NP, FOLD = 4 * 2 * BC;
-    // tokens of the longest chunk: two blocks fit the 160 KB of a CU
-    static constexpr int CK = NS == 4 ? (Q == 2 ? 64 : 128) : Q == 16 ? 32 : 48;
-    static constexpr int CKPT = CK / ST * 256 * NS;
+    static constexpr int SUBS = UNIT / ST, CKPT = SUBS > 1 ? (SUBS - 1) * 256 * NS : 0;
     static constexpr size_t lds = sizeof(float) * (6 * ROWS + 2 * BC + FOLD + CKPT);
 };
 
@@ -51,22 +49,22 @@ template <int NS, int Q> __device__ __forceinline__ void fold_channels(float (&v
 template <int DT, int NS, int Q> __global__ __launch_bounds__(256, 2) void k_scan_bwd(ScanParams p) {
     typedef raw_t<DT> raw;
     typedef Shape<NS, Q> H;
-    constexpr int ST = H::ST, NP = H::NP, CPB = H::CPB, NT = (ST * CPB + 255) / 256, NB = (H::BC + 255) / 256;
+    constexpr int ST = H::ST, NP = H::NP, CPB = H::CPB, SUBS = H::SUBS, NT = (ST * CPB + 255) / 256, NB = (H::BC + 255) / 256;
     constexpr int LEFT = H::CPW == 4 ? NS / 4 : 1;    // values a lane keeps of a fold
-    static_assert(CPB <= 256 && 256 % CPB == 0 && H::FOLD >= 512, "staging");
+    constexpr int SD = 256 / CPB;                     // tokens staged at a time
+    static_assert(CPB <= 256 && 256 % CPB == 0 && H::FOLD >= 512 && UNIT % ST == 0, "staging");
     extern __shared__ __attribute__((aligned(16))) float lds[];
-    float *s_dt = lds, *s_du = s_dt + H::ROWS, *s_dy = s_du + H::ROWS;          // [ST][CPB]
-    float *s_y = s_dy + H::ROWS, *s_gb = s_y + H::ROWS, *s_xa = s_gb + H::ROWS; // [ST][CPB]
-    float *s_b = s_xa + H::ROWS, *s_c = s_b + H::BC;                            // [ST][NP]
-    float *s_fold = s_c + H::BC;                                                // [4][2][ST][NP]
-    float *s_ck = s_fold + H::FOLD;                                             // [sub-tile][NS/4][256][4]
+    float *s_dt = lds, *s_du = s_dt + H::ROWS, *s_dy = s_du + H::ROWS;   // [ST][CPB]
+    float* s_sum = s_dy + H::ROWS;                                       // y, s, <X, a>: [3][ST][CPB]
+    float *s_b = s_sum + 3 * H::ROWS, *s_c = s_b + H::BC;                // [ST][NP]
+    float* s_fold = s_c + H::BC;                                         // [4][2][ST][NP]
+    float* s_ck = s_fold + H::FOLD;                                      // [SUBS - 1][NS/4][256][4]
     const Place pl = place(p.q, blockIdx.x);
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, q = lane % Q, cb = w * H::CPW + lane / Q;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), q = lane % Q, cb = w * H::CPW + lane / Q;
     const Tile tile = tile_of<CPB>(p, blockIdx.y);
     const long D = p.D, N = p.N, G = p.G;
     if (!pl.ok || pl.i == p.q.n) {  // no tokens of a sequence: nothing for the parameters' gradients
-        for (int e = tid; e < CPB * p.N; e += 256)
-            if (e % CPB < tile.left) p.agg[((long)blockIdx.x * N + e / CPB) * D + tile.c0 + e % CPB] = 0.f;
+        for (int e = tid; e < min(CPB, tile.left) * p.N; e += 256) p.agg[(blockIdx.x * D + tile.c0) * N + e] = 0.f;
         for (int e = tid; e < CPB * 2; e += 256)
             if (e % CPB < tile.left) p.pdd[((long)blockIdx.x * 2 + e / CPB) * D + tile.c0 + e % CPB] = 0.f;
         if (!pl.ok) return;
@@ -76,218 +74,256 @@ template <int DT, int NS, int Q> __global__ __launch_bounds__(256, 2) void k_sca
     const int in_group = blockIdx.y - tile.g * p.tpg;
     // partial db, dc of this channel tile: [token][group][2][N]
     float* pbc = p.pbc + (((long)in_group * p.tokens + flat) * G + tile.g) * 2 * N;
-    // staging: thread -> channel sc of the tile, tokens st + k * (256 / CPB)
-    const int sc = tid % CPB, st = tid / CPB;
-    constexpr int SD = 256 / CPB;
+    // Staging: a thread takes channel sc of the tile and tokens st + k * SD (the same for a whole wave where
+    // the tile has 64 channels: the row's address is scalar then)
+    const int sc = tid % CPB, st = CPB >= 64 ? __builtin_amdgcn_readfirstlane(tid / CPB) : tid / CPB;
     const bool sact = sc < tile.left;
-    const int sd = tile.c0 + (sact ? sc : 0);
-    raw *du = static_cast<raw*>(p.du) + flat * D + sd, *ddt = static_cast<raw*>(p.ddt) + flat * D + sd;
-    raw* dz = p.has_z ? static_cast<raw*>(p.dz) + flat * D + sd : nullptr;
+    const unsigned off = sact ? sc : 0;
+    const int sd = tile.c0 + off;
+    raw *du = static_cast<raw*>(p.du) + flat * D + tile.c0, *ddt = static_cast<raw*>(p.ddt) + flat * D + tile.c0;
+    raw* dz = p.has_z ? static_cast<raw*>(p.dz) + flat * D + tile.c0 : nullptr;
     if (pl.i == p.q.n) {            // behind the last sequence
         const raw zero = to_raw<DT>(0.f);
         for (int t = t0 + st; t < t1; t += SD)
             if (sact) {
-                du[t * D] = zero;
-                ddt[t * D] = zero;
-                if (dz) dz[t * D] = zero;
+                (du + t * D)[off] = zero;
+                (ddt + t * D)[off] = zero;
+                if (dz) (dz + t * D)[off] = zero;
             }
         for (int e = tid; e < (t1 - t0) * 2 * p.N; e += 256) pbc[(long)(t0 + e / (2 * p.N)) * G * 2 * N + e % (2 * p.N)] = 0.f;
         return;
     }
-    const raw *gu = at<DT>(p.u, pl) + sd, *gdt = at<DT>(p.dt, pl) + sd, *gdo = at<DT>(p.dout, pl) + sd;
-    const raw *gz = p.has_z ? at<DT>(p.z, pl) + sd : nullptr;
-    const raw *gb = at<DT>(p.b, pl) + tile.g * p.N, *gc = at<DT>(p.c, pl) + tile.g * p.N;
+    const raw *gu = at<DT>(p.u, pl) + tile.c0, *gdt = at<DT>(p.dt, pl) + tile.c0, *gdo = at<DT>(p.dout, pl) + tile.c0;
+    const raw* gz = p.has_z ? at<DT>(p.z, pl) + tile.c0 : nullptr;
     const float bias = p.bias ? p.bias[sd] : 0.f, skip = p.d ? p.d[sd] : 0.f;
+    // element tid (and tid + 256, ...) of the rows of b and c
+    const int bn = tid % NP, br = tid / NP;
+    constexpr int BR = 256 / NP;
+    const bool bon = bn < p.N && br < ST;
+    const raw *gb = at<DT>(p.b, pl) + (long)br * p.b.ts + tile.g * p.N + bn, *gc = at<DT>(p.c, pl) + (long)br * p.c.ts + tile.g * p.N + bn;
 
     const bool act = cb < tile.left;
     const int d = tile.c0 + (act ? cb : 0);
-    float a[NS], h[NS], g[NS], da[NS];
+    float a[NS], hc[NS], h[NS], g[NS], da[NS] = {};   // hc: the chunk's first state
+    const long dn = d * N;
+    const float* h0 = p.chunked ? p.agg + blockIdx.x * D * N : p.init ? p.init + pl.i * D * N : nullptr;
+    const float* g0 = p.chunked ? p.gagg + blockIdx.x * D * N : p.dstate ? p.dstate + pl.i * D * N : nullptr;
+    load_states(p.a + dn, q * NS, p.N, p.vec, 0.f, a);
+    if (h0) load_states(h0 + dn, q * NS, p.N, p.vec, 0.f, hc);
+    if (g0) load_states(g0 + dn, q * NS, p.N, p.vec, 0.f, g);
 #pragma unroll
     for (int k = 0; k < NS; ++k) {
-        const int n = q * NS + k;
-        const bool on = act && n < p.N;
-        a[k] = on ? p.a[d * N + n] * LOG2E : 0.f;
-        const long own = ((long)pl.i * D + d) * N + n, cut = ((long)blockIdx.x * N + n) * D + d;
-        h[k] = !on ? 0.f : p.chunked ? p.agg[cut] : p.init ? p.init[own] : 0.f;
-        g[k] = !on ? 0.f : p.chunked ? p.gagg[cut] : p.dstate ? p.dstate[own] : 0.f;
-        da[k] = 0.f;
+        a[k] = act ? decay_base(a[k]) : 0.f;
+        hc[k] = h0 && act ? hc[k] : 0.f;
+        g[k] = g0 && act ? g[k] : 0.f;
     }
-    const int nsub = (t1 - t0 + ST - 1) / ST;
+    const int nunit = (t1 - t0 + UNIT - 1) / UNIT;
 
     raw r_dt[NT], r_u[NT], r_z[NT], r_g[NT], r_b[NB], r_c[NB];
     auto fetch = [&](int tt, bool all) {
 #pragma unroll
         for (int k = 0; k < NT; ++k) {
-            const long row = min(tt + st + k * SD, t1 - 1);
             if (NT * SD > ST && st + k * SD >= ST) continue;
-            r_dt[k] = gdt[row * p.dt.ts];
-            r_u[k] = gu[row * p.u.ts];
+            const long row = min(tt + st + k * SD, t1 - 1);
+            r_dt[k] = (gdt + row * p.dt.ts)[off];
+            r_u[k] = (gu + row * p.u.ts)[off];
             if (all) {
-                r_g[k] = gdo[row * p.dout.ts];
-                if (gz) r_z[k] = gz[row * p.z.ts];
+                r_g[k] = (gdo + row * p.dout.ts)[off];
+                if (gz) r_z[k] = (gz + row * p.z.ts)[off];
             }
         }
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-            const int e = tid + k * 256, n = e % NP;
-            const long row = min(tt + e / NP, t1 - 1);
-            const bool on = e < H::BC && n < p.N;
-            r_b[k] = on ? gb[row * p.b.ts + n] : raw(0);
-            if (all) r_c[k] = on ? gc[row * p.c.ts + n] : raw(0);
+            const bool on = bon && tt + br + k * BR < t1;
+            r_b[k] = raw(0);
+            if (on) r_b[k] = gb[(tt + k * BR) * p.b.ts];
+            if (all) {
+                r_c[k] = raw(0);
+                if (on) r_c[k] = gc[(tt + k * BR) * p.c.ts];
+            }
         }
     };
-    float f_u[NT], f_z[NT], f_g[NT], f_x[NT], f_dt[NT], f_dy[NT];
-    // a tile's values to LDS; tokens past the chunk and lanes past the group take no step (dt = 0)
+    float f_u[NT], f_z[NT], f_g[NT], f_x[NT], f_dt[NT], f_dy[NT], f_gate[NT];
+    // A tile's values to LDS. Tokens past the chunk and lanes past the group take no step (dt = 0): they pass the
+    // state and the adjoint on and add nothing.
     auto stage = [&](int tt, bool all) {
+#pragma unroll
+        for (int k = 0; k < NT; ++k) {
+            f_x[k] = to_f<DT>(r_dt[k]) + bias;
+            f_u[k] = to_f<DT>(r_u[k]);
+            f_dt[k] = f_x[k];
+        }
+        if (p.softplus) {
+#pragma unroll
+            for (int k = 0; k < NT; ++k) f_dt[k] = softplus(f_x[k]);
+        }
+        if (all) {
+#pragma unroll
+            for (int k = 0; k < NT; ++k) f_dy[k] = f_g[k] = to_f<DT>(r_g[k]);
+            if (gz) {
+#pragma unroll
+                for (int k = 0; k < NT; ++k) {
+                    f_z[k] = to_f<DT>(r_z[k]);
+                    f_gate[k] = sigmoid(f_z[k]);
+                    f_dy[k] *= f_z[k] * f_gate[k];
+                }
+            }
+        }
 #pragma unroll
         for (int k = 0; k < NT; ++k) {
             const int t = st + k * SD;
             if (NT * SD > ST && t >= ST) continue;
-            const bool on = sact && tt + t < t1;
-            f_x[k] = to_f<DT>(r_dt[k]) + bias;
-            f_u[k] = to_f<DT>(r_u[k]);
-            f_dt[k] = on ? (p.softplus ? softplus(f_x[k]) : f_x[k]) : 0.f;
+            if (!sact || tt + t >= t1) f_dt[k] = f_u[k] = f_dy[k] = 0.f;
             s_dt[t * CPB + sc] = f_dt[k];
-            s_du[t * CPB + sc] = on ? f_dt[k] * f_u[k] : 0.f;
-            if (all) {
-                f_g[k] = to_f<DT>(r_g[k]);
-                f_z[k] = gz ? to_f<DT>(r_z[k]) : 0.f;
-                f_dy[k] = on ? (gz ? f_g[k] * f_z[k] * sigmoid(f_z[k]) : f_g[k]) : 0.f;
-                s_dy[t * CPB + sc] = f_dy[k];
+            s_du[t * CPB + sc] = f_dt[k] * f_u[k];
+            if (all) s_dy[t * CPB + sc] = f_dy[k];
+        }
+#pragma unroll
+        for (int k = 0; k < NB; ++k)
+            if (br + k * BR < ST) {
+                s_b[(br + k * BR) * NP + bn] = to_f<DT>(r_b[k]);
+                if (all) s_c[(br + k * BR) * NP + bn] = to_f<DT>(r_c[k]);
             }
-        }
-#pragma unroll
-        for (int k = 0; k < NB; ++k) {
-            const int e = tid + k * 256;
-            if (e < H::BC) {
-                const bool on = tt + e / NP < t1;
-                s_b[e] = on ? to_f<DT>(r_b[k]) : 0.f;
-                if (all) s_c[e] = on ? to_f<DT>(r_c[k]) : 0.f;
-            }
-        }
     };
-    auto checkpoint = [&](int s) {
-#pragma unroll
-        for (int k = 0; k < NS; k += 4)
-            *reinterpret_cast<float4*>(s_ck + ((s * (NS / 4) + k / 4) * 256 + tid) * 4) = make_float4(h[k], h[k + 1], h[k + 2], h[k + 3]);
+    float uh[NS], ut = 0.f;
+    auto fetch_unit = [&](int k) {
+        const long at = (long)blockIdx.x * p.units + k;
+        load_states(p.uh + at * D * N + dn, q * NS, p.N, p.vec, 0.f, uh);
+        ut = p.udt[at * D + d];
     };
+    // the state a lane's first kept value of a fold belongs to; which of the three sums lane q of a channel writes
+    const int own = q * NS + ((lane >> 5) & 1) * (NS / 2) + ((lane >> 4) & 1) * (NS / 4) + (NS == 8 && H::CPW >= 8 ? (lane >> 3) & 1 : 0);
+    float* fold_at = s_fold + w * 2 * H::BC + own;
+    float* sum_at = s_sum + min(q, 2) * H::ROWS + cb;
 
-    // forward: the state in front of every sub-tile
-    if (nsub > 1) fetch(t0, false);
-    for (int s = 0; s < nsub; ++s) {
-        checkpoint(s);
-        if (s + 1 == nsub) break;
-        const int tt = t0 + s * ST;
-        stage(tt, false);
-        __syncthreads();
-        if (s + 2 < nsub) fetch(tt + ST, false);
-#pragma unroll
-        for (int t = 0; t < ST; ++t) {
-            const float v = s_dt[t * CPB + cb], vu = s_du[t * CPB + cb];
-#pragma unroll
-            for (int k = 0; k < NS; ++k) h[k] = __builtin_fmaf(exp2_hw(v * a[k]), h[k], vu * s_b[t * NP + q * NS + k]);
-        }
-        __syncthreads();
-    }
-
-    // backward
     float acc_d = 0.f, acc_bias = 0.f;
-    if (nsub > 0) fetch(t0 + (nsub - 1) * ST, true);
-    for (int s = nsub - 1; s >= 0; --s) {
-        const int tt = t0 + s * ST;
-        stage(tt, true);
-        __syncthreads();
-        if (s > 0) fetch(tt - ST, true);
-        float hp[ST][NS], e[ST][NS];   // the state in front of each token, its decay
+    if (nunit > 1) fetch_unit(nunit - 1);
+    // A unit's sub-tiles but the last are walked for the states behind them (SUBS > 1), then all taken from the last
+    // to the first. What a stage writes is not read behind the barrier at the end of the computation, and what that
+    // computation left is read before the next stage's barrier, so two barriers a sub-tile suffice.
+    if (nunit > 0) fetch(t0 + (nunit - 1) * UNIT, SUBS == 1);
+    for (int unit = nunit - 1; unit >= 0; --unit) {
+        const int tu = t0 + unit * UNIT;
+        float hu[NS];
 #pragma unroll
-        for (int k = 0; k < NS; k += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(s_ck + ((s * (NS / 4) + k / 4) * 256 + tid) * 4);
-            h[k] = x.x, h[k + 1] = x.y, h[k + 2] = x.z, h[k + 3] = x.w;
-        }
+        for (int k = 0; k < NS; ++k) hu[k] = unit > 0 && act ? __builtin_fmaf(exp2_hw(a[k] * ut), hc[k], uh[k]) : hc[k];
+        if (unit > 1) fetch_unit(unit - 1);
+        if constexpr (SUBS > 1) {
 #pragma unroll
-        for (int t = 0; t < ST; ++t) {
-            const float v = s_dt[t * CPB + cb], vu = s_du[t * CPB + cb];
+            for (int k = 0; k < NS; ++k) h[k] = hu[k];
+#pragma unroll 1
+            for (int s = 0; s + 1 < SUBS; ++s) {
+                stage(tu + s * ST, false);
+                __syncthreads();
+                fetch(tu + (s + 1) * ST, s + 2 == SUBS);
 #pragma unroll
-            for (int k = 0; k < NS; ++k) {
-                hp[t][k] = h[k];
-                e[t][k] = exp2_hw(v * a[k]);
-                h[k] = __builtin_fmaf(e[t][k], h[k], vu * s_b[t * NP + q * NS + k]);
+                for (int t = 0; t < ST; ++t) {
+                    const float v = s_dt[t * CPB + cb], vu = s_du[t * CPB + cb];
+#pragma unroll
+                    for (int k = 0; k < NS; ++k) h[k] = __builtin_fmaf(exp2_hw(v * a[k]), h[k], vu * s_b[t * NP + q * NS + k]);
+                }
+#pragma unroll
+                for (int k = 0; k < NS; k += 4)
+                    *reinterpret_cast<float4*>(s_ck + ((s * (NS / 4) + k / 4) * 256 + tid) * 4) = make_float4(h[k], h[k + 1], h[k + 2], h[k + 3]);
+                __syncthreads();
             }
         }
+#pragma unroll 1
+        for (int s = SUBS - 1; s >= 0; --s) {
+            const int tt = tu + s * ST;
+            stage(tt, true);
+            __syncthreads();
+            if (s > 0) fetch(tt - ST, true);
+            else if (unit > 0) fetch(tu - UNIT, SUBS == 1);
+            float hp[ST][NS], e[ST][NS];   // the state in front of each token, its decay
 #pragma unroll
-        for (int t = ST - 1; t >= 0; --t) {
-            const float v = s_dt[t * CPB + cb], vu = s_du[t * CPB + cb], dy = s_dy[t * CPB + cb];
-            float y = 0.f, sgb = 0.f, sxa = 0.f, vb[NS], vc[NS];
+            for (int k = 0; k < NS; ++k) h[k] = hu[k];
+            if (s > 0) {
 #pragma unroll
-            for (int k = 0; k < NS; ++k) {
-                const float b = s_b[t * NP + q * NS + k], c = s_c[t * NP + q * NS + k];
-                const float ht = t == ST - 1 ? h[k] : hp[t + 1 < ST ? t + 1 : 0][k];
-                g[k] = __builtin_fmaf(c, dy, g[k]);
-                y = __builtin_fmaf(c, ht, y);
-                sgb = __builtin_fmaf(g[k], b, sgb);
-                vc[k] = dy * ht;
-                vb[k] = g[k] * vu;
-                g[k] *= e[t][k];
-                const float x = g[k] * hp[t][k];
-                sxa = __builtin_fmaf(x, a[k], sxa);
-                da[k] = __builtin_fmaf(x, v, da[k]);
+                for (int k = 0; k < NS; k += 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(s_ck + (((s - 1) * (NS / 4) + k / 4) * 256 + tid) * 4);
+                    h[k] = x.x, h[k + 1] = x.y, h[k + 2] = x.z, h[k + 3] = x.w;
+                }
             }
-            y = sum_lanes<Q>(y);
-            sgb = sum_lanes<Q>(sgb);
-            sxa = sum_lanes<Q>(sxa);
-            if (q == 0) {
-                s_y[t * CPB + cb] = y;
-                s_gb[t * CPB + cb] = sgb;
-                s_xa[t * CPB + cb] = sxa;
-            }
-            fold_channels<NS, Q>(vb, lane & 8);
-            fold_channels<NS, Q>(vc, lane & 8);
-            // the state a lane's first kept value belongs to
-            const int own = q * NS + ((lane >> 5) & 1) * (NS / 2) + ((lane >> 4) & 1) * (NS / 4) +
-                            (NS == 8 && H::CPW >= 8 ? (lane >> 3) & 1 : 0);
 #pragma unroll
-            for (int k = 0; k < LEFT; ++k) {
-                s_fold[((w * 2 + 0) * ST + t) * NP + own + k] = vb[k];
-                s_fold[((w * 2 + 1) * ST + t) * NP + own + k] = vc[k];
+            for (int t = 0; t < ST; ++t) {
+                const float v = s_dt[t * CPB + cb], vu = s_du[t * CPB + cb];
+#pragma unroll
+                for (int k = 0; k < NS; ++k) {
+                    hp[t][k] = h[k];
+                    e[t][k] = exp2_hw(v * a[k]);
+                    h[k] = __builtin_fmaf(e[t][k], h[k], vu * s_b[t * NP + q * NS + k]);
+                }
+            }
+#pragma unroll
+            for (int t = ST - 1; t >= 0; --t) {
+                const float v = s_dt[t * CPB + cb], vu = s_du[t * CPB + cb], dy = s_dy[t * CPB + cb];
+                float y = 0.f, sgb = 0.f, sxa = 0.f, vb[NS], vc[NS];
+#pragma unroll
+                for (int k = 0; k < NS; ++k) {
+                    const float b = s_b[t * NP + q * NS + k], c = s_c[t * NP + q * NS + k];
+                    const float ht = t == ST - 1 ? h[k] : hp[t + 1 < ST ? t + 1 : 0][k];
+                    g[k] = __builtin_fmaf(c, dy, g[k]);
+                    y = __builtin_fmaf(c, ht, y);
+                    sgb = __builtin_fmaf(g[k], b, sgb);
+                    vc[k] = dy * ht;
+                    vb[k] = g[k] * vu;
+                    g[k] *= e[t][k];
+                    const float x = g[k] * hp[t][k];
+                    sxa = __builtin_fmaf(x, a[k], sxa);
+                    da[k] = __builtin_fmaf(x, v, da[k]);
+                }
+                y = sum_lanes<Q>(y);
+                sgb = sum_lanes<Q>(sgb);
+                sxa = sum_lanes<Q>(sxa);
+                if constexpr (Q >= 4) sum_at[t * CPB] = q == 0 ? y : q == 1 ? sgb : sxa;
+                else {
+                    sum_at[t * CPB] = q == 0 ? y : sgb;
+                    if (q == 0) s_sum[2 * H::ROWS + t * CPB + cb] = sxa;
+                }
+                fold_channels<NS, Q>(vb, lane & 8);
+                fold_channels<NS, Q>(vc, lane & 8);
+#pragma unroll
+                for (int k = 0; k < LEFT; ++k) {
+                    fold_at[t * NP + k] = vb[k];
+                    fold_at[(ST + t) * NP + k] = vc[k];
+                }
+            }
+            __syncthreads();
+            if (sact) {
+#pragma unroll
+                for (int k = 0; k < NT; ++k) {
+                    const int t = st + k * SD;
+                    if (t >= ST || tt + t >= t1) continue;
+                    const float* s = s_sum + t * CPB + sc;
+                    const float y = s[0], sgb = s[H::ROWS], sxa = s[2 * H::ROWS] * LN2;
+                    float x = __builtin_fmaf(f_u[k], sgb, sxa);
+                    if (p.softplus) x *= sigmoid(f_x[k]);
+                    const long row = (tt + t) * D;
+                    (du + row)[off] = to_raw<DT>(__builtin_fmaf(f_dt[k], sgb, skip * f_dy[k]));
+                    (ddt + row)[off] = to_raw<DT>(x);
+                    if (dz) (dz + row)[off] = to_raw<DT>(f_g[k] * __builtin_fmaf(skip, f_u[k], y) * silu_slope(f_z[k], f_gate[k]));
+                    acc_d = __builtin_fmaf(f_dy[k], f_u[k], acc_d);
+                    acc_bias += x;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < (2 * H::BC + 255) / 256; ++k) {   // [m][token][state] of the four waves
+                const int i = tid + k * 256, n = i % NP, row = i / NP, m = row / ST, t = row % ST;
+                if (i < 2 * H::BC && n < p.N && tt + t < t1) {
+                    const float* f = s_fold + i;
+                    pbc[(tt + t) * G * 2 * N + m * N + n] = (f[0] + f[2 * H::BC]) + (f[4 * H::BC] + f[6 * H::BC]);
+                }
             }
         }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < NT; ++k) {
-            const int t = st + k * SD;
-            if (sact && t < ST && tt + t < t1) {
-                const float y = s_y[t * CPB + sc], sgb = s_gb[t * CPB + sc], sxa = s_xa[t * CPB + sc] * LN2;
-                float x = __builtin_fmaf(f_u[k], sgb, sxa);
-                if (p.softplus) x *= sigmoid(f_x[k]);
-                const long row = (long)(tt + t) * D;
-                du[row] = to_raw<DT>(__builtin_fmaf(f_dt[k], sgb, skip * f_dy[k]));
-                ddt[row] = to_raw<DT>(x);
-                if (dz) dz[row] = to_raw<DT>(f_g[k] * __builtin_fmaf(skip, f_u[k], y) * silu_slope(f_z[k], sigmoid(f_z[k])));
-                acc_d = __builtin_fmaf(f_dy[k], f_u[k], acc_d);
-                acc_bias += x;
-            }
-        }
-        for (int i = tid; i < 2 * H::BC; i += 256) {
-            const int n = i % NP, m = (i / NP) & 1, t = i / (2 * NP);
-            if (n < p.N && tt + t < t1) {
-                const float* f = s_fold + (m * ST + t) * NP + n;
-                pbc[(long)(tt + t) * G * 2 * N + m * N + n] = (f[0] + f[2 * H::BC]) + (f[4 * H::BC] + f[6 * H::BC]);
-            }
-        }
-        __syncthreads();
     }
 
     // this chunk's share of da, dd, d(dt_bias); the gradient of the initial state where nothing was cut
     if (act) {
-#pragma unroll
-        for (int k = 0; k < NS; ++k) {
-            const int n = q * NS + k;
-            if (n < p.N) {
-                p.agg[((long)blockIdx.x * N + n) * D + d] = da[k];
-                if (!p.chunked && p.dinit) p.dinit[((long)pl.i * D + d) * N + n] = g[k];
-            }
-        }
+        store_states(p.agg + blockIdx.x * D * N + dn, q * NS, p.N, p.vec, da);
+        if (!p.chunked && p.dinit) store_states(p.dinit + pl.i * D * N + dn, q * NS, p.N, p.vec, g);
     }
+    __syncthreads();
     s_fold[tid] = acc_d;
     s_fold[256 + tid] = acc_bias;
     __syncthreads();
@@ -312,7 +348,7 @@ template <int DT> __global__ __launch_bounds__(256) void k_sums(ScanParams p) {
     const int na = blocks_of(N * D, SUM_COLS), nd = blocks_of(2 * D, SUM_COLS);
     int blk = blockIdx.x;
     if (blk < na) {
-        column_sums(p.agg, N * D, p.slots, (long)blk * SUM_COLS, N * D, [&](long col, float s) { p.da[(col % D) * N + col / D] = s; });
+        column_sums(p.agg, N * D, p.slots, (long)blk * SUM_COLS, N * D, [&](long col, float s) { p.da[col] = s; });
         return;
     }
     blk -= na;
@@ -339,7 +375,8 @@ struct BwdPlan {
     int tpg;
     long slots, tokens;
     bool chunked;
-    size_t off_gagg, off_sdt, off_pdd, off_pbc, bytes;
+    bool walked;                    // chunks of more than a unit, or more than one chunk
+    size_t off_gagg, off_sdt, off_pdd, off_uh, off_udt, off_pbc, bytes;
 };
 
 // f<NS, Q>() for the smallest pair that holds N states
@@ -351,14 +388,15 @@ template <class F> auto with_shape(int64_t N, F f) {
     return f.template operator()<8, 16>();
 }
 struct Sizes {
-    int cpb, st, ck;
+    int cpb;
 };
 struct GetSizes {
-    template <int NS, int Q> Sizes operator()() { return Sizes{Shape<NS, Q>::CPB, Shape<NS, Q>::ST, Shape<NS, Q>::CK}; }
+    template <int NS, int Q> Sizes operator()() { return Sizes{Shape<NS, Q>::CPB}; }
 };
 
-// The longest chunks the checkpoints allow (fewer aggregates and partial sums), halved while fewer than
-// 1024 blocks would walk, down to 16 tokens.
+// Chunks of 128 tokens, halved while fewer than 1024 blocks would walk, down to 16: longer ones leave fewer
+// aggregates and partial sums, but too few blocks to even out the GPU's load.
+constexpr int LONGEST = 128;
 mimo_status plan_bwd(const mamba_scan_bwd_args* a, BwdPlan* pl) {
     if (a == nullptr) return bad("args must not be NULL");
     const mimo_status s = check_scan(a->n, a->S, a->D, a->G, a->N, a->dtype);
@@ -367,19 +405,23 @@ mimo_status plan_bwd(const mamba_scan_bwd_args* a, BwdPlan* pl) {
     const Sizes z = with_shape(a->N, GetSizes{});
     pl->tpg = (int)((a->D / a->G + z.cpb - 1) / z.cpb);
     pl->tokens = packed ? a->S : a->n * a->S;
-    int CH = z.ck;
-    while (CH > 16 && pl->tokens / CH * a->G * pl->tpg < 1024) CH = (CH / 2 + z.st - 1) / z.st * z.st;
-    if (a->S <= z.ck && a->S <= 2 * CH) CH = z.ck;
+    int CH = LONGEST;
+    while (CH > UNIT && pl->tokens / CH * a->G * pl->tpg < 1024) CH /= 2;
+    if (a->S <= LONGEST && a->S <= 2 * CH) CH = LONGEST;
     pl->q = Seqs{a->cu_seqlens, (int)a->n, (int)a->S, CH, (int)((a->S + CH - 1) / CH)};
     pl->slots = slots_of(pl->q);
     pl->chunked = a->S > CH;
+    pl->walked = a->S > UNIT;
     const long per = pl->tokens * a->G * 2 * a->N;
     if (pl->slots > 0x7fffffffL || per / 256 > 0x70000000L || a->G * pl->tpg > 65535) return unsupported("too many tokens or channels");
     const size_t agg = up256((size_t)pl->slots * a->N * a->D * sizeof(float));
     pl->off_gagg = agg;
-    pl->off_sdt = pl->off_gagg + (pl->chunked ? agg : 0);
+    pl->off_sdt = pl->off_gagg + (pl->walked ? agg : 0);
     pl->off_pdd = pl->off_sdt + up256((size_t)pl->slots * a->D * sizeof(float));
-    pl->off_pbc = pl->off_pdd + up256((size_t)pl->slots * 2 * a->D * sizeof(float));
+    pl->off_uh = pl->off_pdd + up256((size_t)pl->slots * 2 * a->D * sizeof(float));
+    const size_t units = a->S > UNIT ? (size_t)pl->slots * (CH / UNIT) * a->D : 0;
+    pl->off_udt = pl->off_uh + up256(units * a->N * sizeof(float));
+    pl->off_pbc = pl->off_udt + up256(units * sizeof(float));
     pl->bytes = pl->off_pbc + up256((size_t)pl->tpg * per * sizeof(float));
     return MIMO_OK;
 }
@@ -389,11 +431,13 @@ template <int DT> struct Run {
     hipStream_t st;
     template <int NS, int Q> mimo_status operator()() {
         mimo_status s;
-        if (p.chunked) {
+        if (p.uh) {
             ScanParams w = p;      // the walk's channel tiles are 64 wide
             w.tpg = (p.Dg + 63) / 64;
             if ((s = launch_walk<DT, AGG2>(w, st)) != MIMO_OK) return s;
-            if ((s = launch(&k_carry<true>, dim3((p.D + 255) / 256, 2 * p.N, p.q.n), 256, 0, st, p)) != MIMO_OK) return s;
+        }
+        if (p.chunked) {
+            if ((s = launch_carry<true>(p, p.q.nc, st)) != MIMO_OK) return s;
         }
         s = launch(&k_scan_bwd<DT, NS, Q>, dim3((unsigned)p.slots, p.G * p.tpg), 256, Shape<NS, Q>::lds, st, p);
         if (s != MIMO_OK) return s;
@@ -446,7 +490,12 @@ mimo_status mamba_scan_bwd(const mamba_scan_bwd_args* a, void* stream) {
     p.sdt = reinterpret_cast<float*>(ws + pl.off_sdt);
     p.pdd = reinterpret_cast<float*>(ws + pl.off_pdd);
     p.pbc = reinterpret_cast<float*>(ws + pl.off_pbc);
+    p.uh = pl.walked ? reinterpret_cast<float*>(ws + pl.off_uh) : nullptr;
+    p.udt = reinterpret_cast<float*>(ws + pl.off_udt);
+    p.units = pl.q.CH / UNIT;
     p.slots = pl.slots, p.tokens = pl.tokens;
+    p.vec = p.N % 4 == 0;
+    for (const void* x : {(const void*)p.a, (const void*)p.init, (const void*)p.dstate, (const void*)p.dinit}) p.vec = p.vec && aligned(x, 0, 0, 16, 1);
     if ((s = require_gfx950()) != MIMO_OK) return s;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     if (a->dtype == BF16) return with_shape(a->N, Run<BF16>{p, st});
