@@ -7,7 +7,8 @@
 // registers, so a token of x is read once and W - 1 rows more at each chunk's start. Memory binds.
 // Two channels a thread and many threads beat wider accesses, whose windows cost the registers that
 // keep waves, and so loads, in flight: [8192, 2048] bf16 forward 18.5 us with eight channels, 17.1 with
-// four, 16.1 with two; [4, 4100, 2048] bf16 backward 156, 60 and 57 us.
+// four, 16.1 with two; [4, 4100, 2048] bf16 backward 156, 60 and 57 us. With scalar rows and the blocks' order
+// below, 15.1 us (4.4 TB/s) and 52 us; 8 x 8192 x 2048 forward 104 us (5.2 TB/s, as a copy).
 #include "layer.hpp"
 
 namespace mimo {
@@ -15,12 +16,13 @@ namespace layer {
 namespace {
 
 constexpr int UNROLL = 8;   // rows of loads in flight in a thread (forward)
-constexpr int UNROLL_B = 4; // backward: two streams, and the windows of both in registers
+constexpr int UNROLL_B = 4; // backward (twice that for one channel): two streams, the windows of both in registers
 
 struct ConvParams {
     Seqs q;
     int D, nvec, silu, zero_tail;
-    long items;                     // threads with work (forward), slots (backward)
+    long slots;
+    unsigned tiles;                 // blocks along the channels
     Rows x, dout;
     const float *w, *bias;
     const void *init, *dstate;
@@ -44,42 +46,46 @@ template <int VEC, int W> struct Filter {
 
 // row t of x, or of the state in front of it where t < 0
 template <int DT, int VEC, int W>
-__device__ __forceinline__ void row_before(const raw_t<DT>* x, long ts, const raw_t<DT>* init, long D, int t, float (&e)[VEC]) {
-    if (t >= 0) unpack<DT, VEC>(load<DT, VEC>(x + t * ts), e);
-    else if (init != nullptr) unpack<DT, VEC>(load<DT, VEC>(init + (t + W - 1) * D), e);
+__device__ __forceinline__ void row_before(const raw_t<DT>* x, long ts, const raw_t<DT>* init, long D, int t, unsigned d, float (&e)[VEC]) {
+    if (t >= 0) unpack<DT, VEC>(load<DT, VEC>(x + t * ts + d), e);
+    else if (init != nullptr) unpack<DT, VEC>(load<DT, VEC>(init + (t + W - 1) * D + d), e);
     else {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) e[v] = 0.f;
     }
 }
 
+// A wave takes one chunk (slot) and 64 channel vectors, so places, row addresses and conditions on tokens are
+// scalar. Blocks of one chunk follow each other, so that the blocks in flight read whole rows: with the chunks
+// following each other, 8 x 8192 x 2048 bf16 forward took 141 us instead of 107.
 template <int DT, int VEC, int W> __global__ __launch_bounds__(256) void k_conv_fwd(ConvParams p) {
     typedef raw_t<DT> raw;
-    const long g = (long)blockIdx.x * 256 + threadIdx.x;
-    if (g >= p.items) return;
-    const int slot = (int)(g / p.nvec), d = (int)(g - (long)slot * p.nvec) * VEC;
+    const unsigned slot = blockIdx.x / p.tiles, tile = blockIdx.x - slot * p.tiles;
     const Place pl = place(p.q, slot);
     if (!pl.ok) return;
+    const int vec = tile * blockDim.x + threadIdx.x;
+    if (vec >= p.nvec) return;
+    const unsigned d = vec * VEC;
     const int t0 = pl.j * p.q.CH, t1 = min(t0 + p.q.CH, pl.len);
     const long D = p.D;
-    raw* out = static_cast<raw*>(p.out) + ((long)(p.q.cu ? pl.row0 : pl.i * (long)p.q.S)) * D + d;
+    raw* out = static_cast<raw*>(p.out) + (p.q.cu ? (long)pl.row0 : (long)pl.i * p.q.S) * D;
     if (pl.i == p.q.n) {            // behind the last sequence
         const float zero[VEC] = {};
         if (p.zero_tail)
-            for (int t = t0; t < t1; ++t) store<DT, VEC>(out + t * D, zero);
+            for (int t = t0; t < t1; ++t) store<DT, VEC>(out + t * D + d, zero);
         return;
     }
-    const raw* x = at<DT>(p.x, pl) + d;
+    const raw* x = at<DT>(p.x, pl);
     const long ts = p.x.ts;
-    const raw* init = p.init ? static_cast<const raw*>(p.init) + (long)pl.i * (W - 1) * D + d : nullptr;
+    const raw* init = p.init ? static_cast<const raw*>(p.init) + (long)pl.i * (W - 1) * D : nullptr;
     const Filter<VEC, W> f(p.w, p.bias, d);
     float e[W - 1 + UNROLL][VEC];
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) row_before<DT, VEC, W>(x, ts, init, D, t0 - (W - 1) + k, e[k]);
+    for (int k = 0; k < W - 1; ++k) row_before<DT, VEC, W>(x, ts, init, D, t0 - (W - 1) + k, d, e[k]);
     for (int t = t0; t < t1; t += UNROLL) {
         Pack<DT, VEC> r[UNROLL];
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) r[u] = load<DT, VEC>(x + (long)min(t + u, t1 - 1) * ts);
+        for (int u = 0; u < UNROLL; ++u) r[u] = load<DT, VEC>(x + (long)min(t + u, t1 - 1) * ts + d);
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) unpack<DT, VEC>(r[u], e[W - 1 + u]);
 #pragma unroll
@@ -92,7 +98,7 @@ template <int DT, int VEC, int W> __global__ __launch_bounds__(256) void k_conv_
                 for (int k = 0; k < W; ++k) s = __builtin_fmaf(f.w[k][v], e[u + k][v], s);
                 y[v] = p.silu ? s * sigmoid(s) : s;
             }
-            if (t + u < t1) store<DT, VEC>(out + (long)(t + u) * D, y);
+            if (t + u < t1) store<DT, VEC>(out + (t + u) * D + d, y);
         }
 #pragma unroll
         for (int k = 0; k < W - 1; ++k)
@@ -104,80 +110,84 @@ template <int DT, int VEC, int W> __global__ __launch_bounds__(256) void k_conv_
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) {
             float s[VEC];
-            row_before<DT, VEC, W>(x, ts, init, D, pl.len - (W - 1) + k, s);
+            row_before<DT, VEC, W>(x, ts, init, D, pl.len - (W - 1) + k, d, s);
             store<DT, VEC>(state + k * D, s);
         }
     }
 }
 
-// Backward. A block takes TY slots by TX channel vectors. A thread walks s over its chunk and W - 1
-// tokens more: dpre[s] from the window of x, then dx[s - (W-1)] from the window of dpre. In a
-// sequence's first chunk the rows in front of token 0 are those of the state. The sums for dw and
-// db stay in registers, are joined over the TY slots in LDS and leave one partial row for each block,
-// which k_conv_sums adds up in order (no atomics).
-template <int DT, int VEC, int W, int TX> __global__ __launch_bounds__(256) void k_conv_bwd(ConvParams p) {
+// Backward. A wave walks s over its chunk and W - 1 tokens more: dpre[s] from the window of x, then
+// dx[s - (W-1)] from the window of dpre. In a sequence's first chunk the rows in front of token 0 are those of
+// the state. The sums for dw and db stay in registers, are joined over the block's slots in LDS and leave one
+// partial row for each block, which k_conv_sums adds up in order (no atomics). A block takes WS neighbouring slots of 64 channel vectors.
+constexpr int WS = 4;
+template <int DT, int VEC, int W> __global__ __launch_bounds__(64 * WS) void k_conv_bwd(ConvParams p) {
     typedef raw_t<DT> raw;
-    constexpr int TY = 256 / TX;
-    __shared__ float s_sum[TY][TX * VEC];
-    const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
-    const int vec = blockIdx.y * TX + tx, d = vec * VEC;
-    const long slot = (long)blockIdx.x * TY + ty, D = p.D;
+    constexpr int U = UNROLL_B * (3 - VEC);
+    constexpr int TC = 64;
+    __shared__ float s_sum[WS][TC * VEC];
+    const int tx = threadIdx.x % TC, ty = __builtin_amdgcn_readfirstlane(threadIdx.x / TC);
+    const unsigned group = blockIdx.x / p.tiles, tile = blockIdx.x - group * p.tiles;
+    const int vec = tile * TC + tx;
+    const unsigned d = vec * VEC;
+    const long slot = (long)group * WS + ty, D = p.D;
     float acc[W + 1][VEC] = {};
     Place pl = {};
-    if (slot < p.items && vec < p.nvec) pl = place(p.q, (int)slot);
-    if (pl.ok) {
+    if (slot < p.slots) pl = place(p.q, (int)slot);
+    if (pl.ok && vec < p.nvec) {
         const int t0 = pl.j * p.q.CH, t1 = min(t0 + p.q.CH, pl.len);
-        raw* dx = static_cast<raw*>(p.out) + ((long)(p.q.cu ? pl.row0 : pl.i * (long)p.q.S)) * D + d;
+        raw* dx = static_cast<raw*>(p.out) + (p.q.cu ? (long)pl.row0 : (long)pl.i * p.q.S) * D;
         if (pl.i == p.q.n) {
             const float zero[VEC] = {};
-            for (int t = t0; t < t1; ++t) store<DT, VEC>(dx + t * D, zero);
+            for (int t = t0; t < t1; ++t) store<DT, VEC>(dx + t * D + d, zero);
         } else {
-            const raw* x = at<DT>(p.x, pl) + d;
-            const raw* dout = at<DT>(p.dout, pl) + d;
-            const long xs = p.x.ts, gs = p.dout.ts, sd = (long)pl.i * (W - 1) * D + d;
+            const raw *x = at<DT>(p.x, pl), *dout = at<DT>(p.dout, pl);
+            const long xs = p.x.ts, gs = p.dout.ts, sd = (long)pl.i * (W - 1) * D;
             const raw* init = p.init ? static_cast<const raw*>(p.init) + sd : nullptr;
             const raw* dstate = p.dstate ? static_cast<const raw*>(p.dstate) + sd : nullptr;
             raw* dinit = p.dinit ? static_cast<raw*>(p.dinit) + sd : nullptr;
             const Filter<VEC, W> f(p.w, p.bias, d);
-            float e[W - 1 + UNROLL_B][VEC], g[W - 1 + UNROLL_B][VEC];
+            float e[W - 1 + U][VEC], g[W - 1 + U][VEC];
 #pragma unroll
             for (int k = 0; k < W - 1; ++k) {
-                row_before<DT, VEC, W>(x, xs, init, D, t0 - (W - 1) + k, e[k]);
+                row_before<DT, VEC, W>(x, xs, init, D, t0 - (W - 1) + k, d, e[k]);
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) g[k][v] = 0.f;
             }
             const int s1 = t1 + W - 1;   // dx up to t1 - 1
-            for (int s = t0; s < s1; s += UNROLL_B) {
-                Pack<DT, VEC> rx[UNROLL_B], rg[UNROLL_B];
+            for (int s = t0; s < s1; s += U) {
+                Pack<DT, VEC> rx[U], rg[U];
 #pragma unroll
-                for (int u = 0; u < UNROLL_B; ++u) {
-                    const long t = max(min(min(s + u, s1 - 1), pl.len - 1), 0);
+                for (int u = 0; u < U; ++u) {
+                    const long t = max(min(s + u, pl.len - 1), 0);
                     if (pl.len > 0) {
-                        rx[u] = load<DT, VEC>(x + t * xs);
-                        rg[u] = load<DT, VEC>(dout + t * gs);
+                        rx[u] = load<DT, VEC>(x + t * xs + d);
+                        rg[u] = load<DT, VEC>(dout + t * gs + d);
                     } else {
                         rx[u] = Pack<DT, VEC>{};
                         rg[u] = Pack<DT, VEC>{};
                     }
                 }
 #pragma unroll
-                for (int u = 0; u < UNROLL_B; ++u) {
+                for (int u = 0; u < U; ++u) {
                     unpack<DT, VEC>(rx[u], e[W - 1 + u]);
-                    float dy[VEC];
-                    unpack<DT, VEC>(rg[u], dy);
-                    const bool in = s + u < pl.len, mine = s + u < t1;
+                    unpack<DT, VEC>(rg[u], g[W - 1 + u]);
+                    if (s + u >= pl.len) {
 #pragma unroll
-                    for (int v = 0; v < VEC; ++v) {
-                        float dp = dy[v];
-                        if (p.silu) {
+                        for (int v = 0; v < VEC; ++v) g[W - 1 + u][v] = 0.f;
+                    } else if (p.silu) {
+#pragma unroll
+                        for (int v = 0; v < VEC; ++v) {
                             float pre = f.bias[v];
 #pragma unroll
                             for (int k = 0; k < W; ++k) pre = __builtin_fmaf(f.w[k][v], e[u + k][v], pre);
-                            dp *= silu_slope(pre, sigmoid(pre));
+                            g[W - 1 + u][v] *= silu_slope(pre, sigmoid(pre));
                         }
-                        dp = in ? dp : 0.f;
-                        g[W - 1 + u][v] = dp;
-                        if (mine) {
+                    }
+                    if (s + u < t1) {
+#pragma unroll
+                        for (int v = 0; v < VEC; ++v) {
+                            const float dp = g[W - 1 + u][v];
 #pragma unroll
                             for (int k = 0; k < W; ++k) acc[k][v] = __builtin_fmaf(dp, e[u + k][v], acc[k][v]);
                             acc[W][v] += dp;
@@ -195,35 +205,35 @@ template <int DT, int VEC, int W, int TX> __global__ __launch_bounds__(256) void
                         const int k = t - (pl.len - (W - 1));   // this row's place in the last state
                         if (dstate != nullptr && k >= 0) {
                             float a[VEC];
-                            unpack<DT, VEC>(load<DT, VEC>(dstate + k * D), a);
+                            unpack<DT, VEC>(load<DT, VEC>(dstate + k * D + d), a);
 #pragma unroll
                             for (int v = 0; v < VEC; ++v) r[v] += a[v];
                         }
-                        if (t >= 0) store<DT, VEC>(dx + t * D, r);
-                        else if (dinit != nullptr) store<DT, VEC>(dinit + (t + W - 1) * D, r);
+                        if (t >= 0) store<DT, VEC>(dx + t * D + d, r);
+                        else if (dinit != nullptr) store<DT, VEC>(dinit + (t + W - 1) * D + d, r);
                     }
                 }
 #pragma unroll
                 for (int k = 0; k < W - 1; ++k)
 #pragma unroll
                     for (int v = 0; v < VEC; ++v) {
-                        e[k][v] = e[UNROLL_B + k][v];
-                        g[k][v] = g[UNROLL_B + k][v];
+                        e[k][v] = e[U + k][v];
+                        g[k][v] = g[U + k][v];
                     }
             }
         }
     }
-    float* part = p.part + (long)blockIdx.x * (W + 1) * D;
+    float* part = p.part + (long)group * (W + 1) * D;
 #pragma unroll
     for (int k = 0; k <= W; ++k) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) s_sum[ty][tx * VEC + v] = acc[k][v];
         __syncthreads();
-        for (int c = threadIdx.x; c < TX * VEC; c += 256) {
+        if (threadIdx.x < TC * VEC) {
             float s = 0.f;
 #pragma unroll
-            for (int y = 0; y < TY; ++y) s += s_sum[y][c];
-            const long col = (long)blockIdx.y * TX * VEC + c;
+            for (int y = 0; y < WS; ++y) s += s_sum[y][threadIdx.x];
+            const long col = (long)tile * TC * VEC + threadIdx.x;
             if (col < D) part[k * D + col] = s;
         }
         __syncthreads();
@@ -346,15 +356,19 @@ struct FwdRun {
     ConvParams p;
     hipStream_t st;
     template <int DT, int VEC, int W> mimo_status operator()() {
-        return launch(&k_conv_fwd<DT, VEC, W>, dim3((unsigned)((p.items + 255) / 256)), 256, 0, st, p);
+        const int block = p.nvec >= 256 ? 256 : (p.nvec + 63) / 64 * 64;
+        p.tiles = (p.nvec + block - 1) / block;
+        if (p.slots * p.tiles > 0x7fffffffL) return unsupported("too many tokens");
+        return launch(&k_conv_fwd<DT, VEC, W>, dim3((unsigned)(p.slots * p.tiles)), block, 0, st, p);
     }
 };
 struct BwdRun {
     ConvParams p;
     hipStream_t st;
     template <int DT, int VEC, int W> mimo_status operator()() {
-        constexpr int TX = 32 * (3 - VEC);
-        mimo_status s = launch(&k_conv_bwd<DT, VEC, W, TX>, dim3(p.groups, (p.nvec + TX - 1) / TX), 256, 0, st, p);
+        p.tiles = (p.nvec + 63) / 64;
+        if ((long)p.groups * p.tiles > 0x7fffffffL) return unsupported("too many tokens");
+        mimo_status s = launch(&k_conv_bwd<DT, VEC, W>, dim3(p.groups * p.tiles), 64 * WS, 0, st, p);
         if (s != MIMO_OK) return s;
         return launch(&k_conv_sums<W>, dim3((unsigned)(((W + 1) * (long)p.D + SUM_COLS - 1) / SUM_COLS)), 256, 0, st, p);
     }
@@ -385,8 +399,7 @@ mimo_status plan_bwd(const mamba_conv_bwd_args* a, BwdPlan* pl) {
     const bool packed = a->cu_seqlens != nullptr;
     pl->CH = chunk_tokens(a->n, a->S, packed, a->D / pl->vec, MOST_BWD);
     const Seqs q = make_seqs(a->n, a->S, a->cu_seqlens, pl->CH);
-    const int TY = pl->vec == 1 ? 4 : 8;   // 256 / TX of the launch
-    const long groups = (slots_of(q) + TY - 1) / TY;
+    const long groups = (slots_of(q) + WS - 1) / WS;
     if (slots_of(q) > (long)1 << 30) return unsupported("too many tokens");
     pl->groups = (int)groups;
     pl->bytes = up256((size_t)groups * (a->W + 1) * a->D * sizeof(float));
@@ -416,8 +429,8 @@ mimo_status mamba_conv_fwd(const mamba_conv_fwd_args* a, void* stream) {
     p.D = (int)a->D;
     p.nvec = p.D / vec;
     p.q = make_seqs(a->n, a->S, a->cu_seqlens, chunk_tokens(a->n, a->S, packed, p.nvec, MOST_FWD));
-    p.items = slots_of(p.q) * p.nvec;
-    if (slots_of(p.q) > (long)1 << 30 || p.items > (long)1 << 38) return unsupported("too many tokens");
+    p.slots = slots_of(p.q);
+    if (p.slots > (long)1 << 30) return unsupported("too many tokens");
     p.silu = a->silu;
     p.zero_tail = a->zero_tail;
     p.x = rows_of(a->x, packed);
@@ -450,7 +463,7 @@ mimo_status mamba_conv_bwd(const mamba_conv_bwd_args* a, void* stream) {
     p.D = (int)a->D;
     p.nvec = p.D / pl.vec;
     p.q = make_seqs(a->n, a->S, a->cu_seqlens, pl.CH);
-    p.items = slots_of(p.q);
+    p.slots = slots_of(p.q);
     p.groups = pl.groups;
     p.silu = a->silu;
     p.x = rows_of(a->x, packed);

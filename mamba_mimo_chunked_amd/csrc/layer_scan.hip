@@ -17,73 +17,96 @@ struct StepParams {
 
 // One token of row blockIdx.y. LPC lanes share a channel, each with four consecutive states: a wave
 // reads and writes whole lines of the state [D, N], which is nearly all the traffic (8 bytes a state
-// against some twenty operations), and <c, h> is a sum over LPC lanes. VEC: 16-byte accesses.
+// against some twenty operations), and <c, h> is a sum over LPC lanes. A thread takes STEP_CH channels,
+// and everything it reads is asked for before the first use: the chain from a row's index to its store is
+// what a wave waits for. VEC: four states (and four of b, of c) in one access.
+constexpr int STEP_CH = 2;
 template <int DT, int LPC, bool VEC> __global__ __launch_bounds__(256) void k_step(StepParams p) {
     typedef raw_t<DT> raw;
-    const int q = threadIdx.x % LPC, d0 = blockIdx.x * (256 / LPC) + threadIdx.x / LPC;
-    const bool act = d0 < p.D;
-    const int d = act ? d0 : p.D - 1;
+    constexpr int U = STEP_CH, CPB = 256 / LPC;
+    const int q = threadIdx.x % LPC, n0 = q * 4;
     int row = blockIdx.y;
     const long D = p.D;
-    raw* out = static_cast<raw*>(p.out) + d;
     const int slot = p.idx ? p.idx[row] : row;
+    int d[U];
+    bool act[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+        d[j] = (blockIdx.x * U + j) * CPB + threadIdx.x / LPC;
+        act[j] = d[j] < p.D;
+        d[j] = act[j] ? d[j] : p.D - 1;
+    }
+    raw* out = static_cast<raw*>(p.out);
     if (slot < 0 || slot >= p.slots) {
-        if (act && q == 0) out[row * D] = to_raw<DT>(0.f);
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (act[j] && q == 0) out[row * D + d[j]] = to_raw<DT>(0.f);
         return;
     }
-    const int n0 = q * 4, g = d / p.Dg;
-    float* state = p.state + slot * p.slot_stride + (long)d * p.N + n0;
-    const float* pa = p.a + (long)d * p.N + n0;
-    float h[4] = {}, a[4] = {};
-    if (VEC) {
-        if (n0 < p.N) {
-            const float4 x = *reinterpret_cast<const float4*>(state), y = *reinterpret_cast<const float4*>(pa);
-            h[0] = x.x, h[1] = x.y, h[2] = x.z, h[3] = x.w;
-            a[0] = y.x, a[1] = y.y, a[2] = y.z, a[3] = y.w;
-        }
-    } else {
+    float* state = p.state + slot * p.slot_stride;
+    float h[U][4], a[U][4], bias[U], skip[U];
+    raw r_u[U], r_dt[U], r_z[U], r_b[U][4], r_c[U][4];
+    auto four = [&](const raw* x, raw (&r)[4]) {
+        if (VEC) {
+            Pack<DT, 4> v{};
+            if (n0 < p.N) v = load<DT, 4>(x);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (n0 + k < p.N) h[k] = state[k], a[k] = pa[k];
+            for (int k = 0; k < 4; ++k) r[k] = v.v[k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) r[k] = n0 + k < p.N ? x[k] : raw(0);
+        }
+    };
+    auto inputs = [&](int row) {
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int at = d[j] / p.Dg * p.N + n0;
+            r_u[j] = static_cast<const raw*>(p.u.p)[row * p.u.bs + d[j]];
+            r_dt[j] = static_cast<const raw*>(p.dt.p)[row * p.dt.bs + d[j]];
+            if (p.z.p) r_z[j] = static_cast<const raw*>(p.z.p)[row * p.z.bs + d[j]];
+            four(static_cast<const raw*>(p.b.p) + row * p.b.bs + at, r_b[j]);
+            four(static_cast<const raw*>(p.c.p) + row * p.c.bs + at, r_c[j]);
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+        load_states(state + (long)d[j] * p.N, n0, p.N, VEC, 0.f, h[j]);
+        load_states(p.a + (long)d[j] * p.N, n0, p.N, VEC, 0.f, a[j]);
+        bias[j] = p.bias ? p.bias[d[j]] : 0.f;
+        skip[j] = p.d ? p.d[d[j]] : 0.f;
     }
-    const float bias = p.bias ? p.bias[d] : 0.f, skip = p.d ? p.d[d] : 0.f;
+    inputs(row);
     if (p.idx && !first_of(p.idx, row, slot)) return;
     for (;;) {
-        const float u = to_f<DT>(static_cast<const raw*>(p.u.p)[row * p.u.bs + d]);
-        const float x = to_f<DT>(static_cast<const raw*>(p.dt.p)[row * p.dt.bs + d]) + bias;
-        const raw* b = static_cast<const raw*>(p.b.p) + row * p.b.bs + g * p.N + n0;
-        const raw* c = static_cast<const raw*>(p.c.p) + row * p.c.bs + g * p.N + n0;
-        const float dt = p.softplus ? softplus(x) : x, du = dt * u;
-        float y = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (n0 + k < p.N) {
-                h[k] = __builtin_fmaf(exp2_hw(dt * (a[k] * LOG2E)), h[k], du * to_f<DT>(b[k]));
-                y = __builtin_fmaf(h[k], to_f<DT>(c[k]), y);
+        for (int j = 0; j < U; ++j) {
+            const float u = to_f<DT>(r_u[j]), x = to_f<DT>(r_dt[j]) + bias[j], dt = p.softplus ? softplus(x) : x, du = dt * u;
+            float y = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                h[j][k] = __builtin_fmaf(exp2_hw(dt * decay_base(a[j][k])), h[j][k], du * to_f<DT>(r_b[j][k]));
+                y = __builtin_fmaf(h[j][k], to_f<DT>(r_c[j][k]), y);
             }
-        y = sum_lanes<LPC < 16 ? LPC : 16>(y);
-        if (LPC == 32) y += __shfl_xor(y, 16);
-        y = __builtin_fmaf(skip, u, y);
-        if (p.z.p) {
-            const float z = to_f<DT>(static_cast<const raw*>(p.z.p)[row * p.z.bs + d]);
-            y *= z * sigmoid(z);
+            y = sum_lanes<LPC < 16 ? LPC : 16>(y);
+            if (LPC == 32) y += __shfl_xor(y, 16);
+            y = __builtin_fmaf(skip[j], u, y);
+            if (p.z.p) {
+                const float z = to_f<DT>(r_z[j]);
+                y *= z * sigmoid(z);
+            }
+            if (act[j] && q == 0) out[row * D + d[j]] = to_raw<DT>(y);
         }
-        if (act && q == 0) out[row * D] = to_raw<DT>(y);
         row = p.idx ? next_of(p.idx, row, p.n, slot) : p.n;
         if (row >= p.n) break;
+        inputs(row);
     }
-    if (!act) return;
-    if (VEC) {
-        if (n0 < p.N) *reinterpret_cast<float4*>(state) = make_float4(h[0], h[1], h[2], h[3]);
-    } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (n0 + k < p.N) state[k] = h[k];
-    }
+    for (int j = 0; j < U; ++j)
+        if (act[j]) store_states(state + (long)d[j] * p.N, n0, p.N, VEC, h[j]);
 }
 
 template <int DT, bool VEC> mimo_status launch_step(const StepParams& p, hipStream_t st) {
-    auto grid = [&](int lpc) { return dim3((unsigned)(((long)p.D * lpc + 255) / 256), p.n); };
+    auto grid = [&](int lpc) { return dim3((unsigned)(((long)p.D * lpc + 256 * STEP_CH - 1) / (256 * STEP_CH)), p.n); };
     if (p.N <= 4) return launch(&k_step<DT, 1, VEC>, grid(1), 256, 0, st, p);
     if (p.N <= 8) return launch(&k_step<DT, 2, VEC>, grid(2), 256, 0, st, p);
     if (p.N <= 16) return launch(&k_step<DT, 4, VEC>, grid(4), 256, 0, st, p);
@@ -192,7 +215,9 @@ mimo_status mamba_scan_step(const mamba_scan_step_args* a, void* stream) {
     p.state = a->state, p.idx = a->indices, p.out = a->out;
     if ((s = require_gfx950()) != MIMO_OK) return s;
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    const bool vec = p.N % 4 == 0 && aligned(p.state, p.slot_stride, 0, 16, 4) && aligned(p.a, 0, 0, 16, 1);
+    const int esz = a->dtype == F32 ? 4 : 2;
+    const bool vec = p.N % 4 == 0 && aligned(p.state, p.slot_stride, 0, 16, 4) && aligned(p.a, 0, 0, 16, 1) &&
+                     aligned(p.b.p, p.b.bs, 0, 4 * esz, esz) && aligned(p.c.p, p.c.bs, 0, 4 * esz, esz);
     if (a->dtype == BF16) return vec ? launch_step<BF16, true>(p, st) : launch_step<BF16, false>(p, st);
     if (a->dtype == F16) return vec ? launch_step<F16, true>(p, st) : launch_step<F16, false>(p, st);
     return vec ? launch_step<F32, true>(p, st) : launch_step<F32, false>(p, st);

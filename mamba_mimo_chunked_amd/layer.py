@@ -77,13 +77,19 @@ def _data_dtype(name, x):
     return code
 
 
+_READY = set()   # devices that passed the checks
+
+
 def _device(what, name, x):
     """The device of the first tensor; every other one has to be there too."""
     dev = x.device
+    if dev in _READY:
+        return dev
     if dev.type != "cuda":
         raise ValueError(f"{what} requires GPU (HIP) tensors, got {name} on {dev}")
     if not _is_gfx950(dev.index if dev.index is not None else torch.cuda.current_device()):
         raise NotImplementedError(f"{what} supports gfx950 (MI355X) devices only")
+    _READY.add(dev)
     return dev
 
 
@@ -98,7 +104,8 @@ def _param(name, x, shape, dtype, device):
     keeps it until the call is queued."""
     if x is None:
         return None
-    _fits(name, x, shape, dtype, device)
+    if x.shape != shape or x.dtype != dtype or x.device != device:
+        _check_tensor(name, x, shape, dtype, device)
     return x if x.is_contiguous() else x.contiguous()
 
 
@@ -106,8 +113,9 @@ def _data(name, x, shape, dtype, device, inner=1):
     """A tensor whose last ``inner`` axes have to be dense: checked, a copy where they are not."""
     if x is None:
         return None
-    _fits(name, x, shape, dtype, device)
-    return _dense_inner(x, inner)
+    if x.shape != shape or x.dtype != dtype or x.device != device:
+        _check_tensor(name, x, shape, dtype, device)
+    return x if x.is_contiguous() else _dense_inner(x, inner)
 
 
 def _dense_inner(x, inner):
@@ -156,11 +164,6 @@ def _rows(x, packed):
     return (x.data_ptr(), 0, x.stride(0)) if packed else (x.data_ptr(), x.stride(0), x.stride(1))
 
 
-def _row(x):
-    """The same for the rows [n, ...] of a step."""
-    return _NO_ROWS if x is None else (x.data_ptr(), x.stride(0), 0)
-
-
 def _ptr(x):
     return 0 if x is None else x.data_ptr()
 
@@ -173,15 +176,16 @@ def _span(x):
     return lo, lo + (sum((s - 1) * st for s, st in zip(x.shape, x.stride())) + 1) * x.element_size()
 
 
-def _apart(name, x, others):
-    """A tensor that is written must not lie over one that is read."""
-    lo, hi = _span(x)
-    for other, y in others:
-        if y is None:
-            continue
-        p = y.data_ptr()
-        if p < hi and (p >= lo or _span(y)[1] > lo):
-            raise ValueError(f"{name} must not overlap {other}")
+def _apart(name, written, /, **others):
+    """A tensor that is written must not lie over one that is read. One that starts where its storage starts can only
+    be met by tensors that start inside it."""
+    lo, hi = _span(written)
+    first = written.untyped_storage().data_ptr() == lo
+    for other, x in others.items():
+        if x is not None:
+            p = x.data_ptr()
+            if p < hi and (p >= lo or (not first and _span(x)[1] > lo)):
+                raise ValueError(f"{name} must not overlap {other}")
 
 
 def _new_like(x):
@@ -189,12 +193,12 @@ def _new_like(x):
     return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
 
 
-def _out(out, x, inputs):
-    """The output: a new tensor like x, or the caller's."""
+def _out(out, like, /, **inputs):
+    """The output: a new tensor, or the caller's."""
     if out is None:
-        return _new_like(x)
-    _check_output("out", out, x.shape, x.dtype, x.device)
-    _apart("out", out, inputs)
+        return _new_like(like)
+    _check_output("out", out, like.shape, like.dtype, like.device)
+    _apart("out", out, **inputs)
     return out
 
 
@@ -262,7 +266,7 @@ def mamba_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, *,
     W, weight, bias = _check_filter(weight, bias, D, dev)
     initial_state = _param("initial_state", initial_state, (n, W - 1, D), x.dtype, dev)
     cu, x = _cu(cu_seqlens, dev), _dense_inner(x, 1)
-    res = _out(out, x, (("x", x), ("initial_state", initial_state)))
+    res = _out(out, x, x=x, initial_state=initial_state)
     state = x.new_empty((n, W - 1, D)) if return_state else None
     _call("mamba_conv_fwd", (n, S, D, W, code, silu, int(out is None), _ptr(cu), *_rows(x, cu is not None), _ptr(weight),
                              _ptr(bias), _ptr(initial_state), _ptr(res), _ptr(state)), dev)
@@ -330,8 +334,8 @@ def mamba_conv_step(x, state, weight, bias=None, state_indices=None, *, activati
     W, weight, bias = _check_filter(weight, bias, D, dev)
     slots, stride, idx = _check_pool(state, (W - 1, D), x.dtype, state_indices, n, dev)
     x = _dense_inner(x, 1)
-    _apart("state", state, (("x", x), ("weight", weight), ("bias", bias), ("state_indices", idx)))
-    res = _out(out, x, (("x", x), ("state", state)))
+    _apart("state", state, x=x, weight=weight, bias=bias, state_indices=idx)
+    res = _out(out, x, x=x, state=state)
     _call("mamba_conv_step", (n, D, slots, stride, x.stride(0), W, code, silu, 0, x.data_ptr(), state.data_ptr(), weight.data_ptr(),
                               _ptr(bias), _ptr(idx), res.data_ptr()), dev)
     return res
@@ -375,7 +379,7 @@ def mamba_scan_fwd(u, dt, a, b, c, d=None, z=None, dt_bias=None, initial_state=N
     n, S, lead = _sequences("u", u, cu_seqlens, 1)
     D, G, N, (u, dt, b, c, z), (a, d, dt_bias) = _check_scan(u, dt, a, b, c, d, z, dt_bias, lead, dev)
     cu, initial_state = _cu(cu_seqlens, dev), _param("initial_state", initial_state, (n, D, N), _F32, dev)
-    res = _out(out, u, (("u", u), ("dt", dt), ("b", b), ("c", c), ("z", z), ("initial_state", initial_state)))
+    res = _out(out, u, u=u, dt=dt, b=b, c=c, z=z, initial_state=initial_state)
     state = a.new_empty((n, D, N)) if return_state else None
     packed = cu is not None
     _call("mamba_scan_fwd", (n, S, D, G, N, code, int(bool(dt_softplus)), int(out is None), 0, _ptr(cu), *_rows(u, packed), *_rows(dt, packed),
@@ -418,10 +422,11 @@ def mamba_scan_step(u, dt, state, a, b, c, d=None, z=None, dt_bias=None, state_i
     n = u.shape[0]
     D, G, N, (u, dt, b, c, z), (a, d, dt_bias) = _check_scan(u, dt, a, b, c, d, z, dt_bias, (n,), dev)
     slots, stride, idx = _check_pool(state, (D, N), _F32, state_indices, n, dev)
-    inputs = (("u", u), ("dt", dt), ("b", b), ("c", c), ("z", z))
-    _apart("state", state, (*inputs, ("a", a), ("d", d), ("dt_bias", dt_bias), ("state_indices", idx)))
-    res = _out(out, u, (*inputs, ("state", state)))
-    _call("mamba_scan_step", (n, D, G, N, slots, stride, code, int(bool(dt_softplus)), *_row(u), *_row(dt), *_row(b), *_row(c), *_row(z),
+    _apart("state", state, u=u, dt=dt, b=b, c=c, z=z, a=a, d=d, dt_bias=dt_bias, state_indices=idx)
+    res = _out(out, u, u=u, dt=dt, b=b, c=c, z=z, state=state)
+    _call("mamba_scan_step", (n, D, G, N, slots, stride, code, int(bool(dt_softplus)), u.data_ptr(), u.stride(0), 0,
+                              dt.data_ptr(), dt.stride(0), 0, b.data_ptr(), b.stride(0), 0, c.data_ptr(), c.stride(0), 0,
+                              *(_NO_ROWS if z is None else (z.data_ptr(), z.stride(0), 0)),
                               a.data_ptr(), _ptr(d), _ptr(dt_bias), state.data_ptr(), _ptr(idx), res.data_ptr()), dev)
     return res
 
@@ -466,7 +471,7 @@ def mamba_norm_fwd(x, weight, bias=None, z=None, *, groups: int = 1, eps: float 
     and out = p * silu(z) (z given, gate "after"), silu(p) (activation "silu", without z), or p. x, z, out
     [..., D]; weight, bias [D] float32."""
     dev, code, silu, D, rows, zr, weight, bias = _check_norm("mamba_norm_fwd", x, weight, bias, z, groups, eps, gate, activation)
-    res = _out(out, x, (("x", rows), ("z", zr)))
+    res = _out(out, x, x=rows, z=zr)
     _call("mamba_norm_fwd", (rows.shape[0], D, groups, rows.stride(0), 0 if zr is None else zr.stride(0), code, int(bool(center)),
                              int(gate == "after"), silu, eps, 0, _ptr(rows), _ptr(zr), _ptr(weight), _ptr(bias), _ptr(res)), dev)
     return res
