@@ -24,8 +24,13 @@
  * Ownership, asynchrony and errors as in mimo_bwd_fwd.h: the caller owns every
  * buffer; nothing is allocated; the call returns once its kernels are queued on
  * `stream`; on error nothing has been queued. A workspace's contents do not
- * matter on entry; calls that may overlap need workspaces of their own. Sums
- * run in a fixed order: equal inputs give equal bits.
+ * matter on entry; calls that may overlap need workspaces of their own. Its size
+ * goes by the sizes, by which optional pointers are NULL and by the alignment of
+ * the tensors, so the query takes the arguments of the call (without workspace).
+ * For the backward scan it is mostly the states every sixteenth token, 4 D N / 16
+ * bytes a token, and the partial sums of db and dc, 8 D N / 64 bytes a token (N up
+ * to 16; 8 D N / 32 up to 64, 8 D N / 16 up to 128). Sums run in a fixed order:
+ * equal inputs give equal bits.
  */
 #ifndef MAMBA_LAYER_H
 #define MAMBA_LAYER_H

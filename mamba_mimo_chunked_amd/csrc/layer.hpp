@@ -216,6 +216,7 @@ inline mimo_status bad(const char* msg) { return set_error(MIMO_ERR_VALUE, msg);
 inline mimo_status unsupported(const char* msg) { return set_error(MIMO_ERR_UNSUPPORTED, msg); }
 
 template <class P> inline mimo_status launch(void (*f)(P), dim3 grid, int block, size_t lds, hipStream_t st, P p) {
+    if ((unsigned long)grid.x * block > 0xffffffffUL) return unsupported("the call needs more than 2^32 threads");
     if (lds > 64 * 1024 && hipFuncSetAttribute(reinterpret_cast<const void*>(f), hipFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)lds) != hipSuccess)
         return set_error(MIMO_ERR_HIP, "hipFuncSetAttribute(MaxDynamicSharedMemorySize) failed");

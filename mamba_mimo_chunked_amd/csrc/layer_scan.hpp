@@ -41,7 +41,7 @@ struct ScanParams {
 // first row of the flat token axis of a place
 __device__ __forceinline__ long flat_row(const Seqs& q, const Place& pl) { return q.cu ? (long)pl.row0 : (long)pl.i * q.S; }
 
-// the channel tile of blockIdx.y: CPB channels of one group
+// a channel tile: CPB channels of one group
 struct Tile {
     int g, c0, left;   // group, first channel, channels left in the group from there
 };
@@ -80,7 +80,11 @@ template <int K> __device__ __forceinline__ void store_states(float* row, int n0
     }
 }
 // the decay's base: exp(dt a) = exp2(dt * decay_base(a)); finite, so that a step of zero is no decay for a = -inf too
-__device__ __forceinline__ float decay_base(float a) { return __builtin_fmaxf(a * LOG2E, -3e38f); }
+// (NaN stays)
+__device__ __forceinline__ float decay_base(float a) {
+    const float x = a * LOG2E;
+    return x < -3e38f ? -3e38f : x;
+}
 
 // FWD: the outputs. AGG: a chunk's last state from zero. AGG2: also the adjoint that leaves it to the
 // left, sum_t exp(a sum_{s <= t} dt) c[t] dy[t], from the same exponentials.

@@ -12,9 +12,10 @@
 // of NS values over the 64 / Q others: each fold halves the values a lane keeps, two operations a
 // pair. A chunk is taken in units of 16 tokens from the last to the first, a unit in sub-tiles of ST
 // tokens likewise: forward with the states and decays of its ST tokens in registers (2 * NS * ST of
-// them: 128, or 64 for Q = 2, whose staging takes the rest), then backward through them. The state in front of a unit comes from the walk, which leaves it (from
-// zero, at the chunk's start) with the sum of dt to there: h = uh + exp(a udt) h(chunk). So an
-// exponential is computed twice (walk, sub-tile) and no state but every sixteenth goes to memory.
+// them: 128, or 64 for Q = 2, whose staging takes the rest), then backward through them. The state in
+// front of a unit comes from the walk, which leaves it (from zero, at the chunk's start) with the sum of
+// dt to there: h = uh + exp(a udt) h(chunk). So an exponential is computed twice (walk, sub-tile) and no
+// state but every sixteenth goes to memory.
 #include "layer_scan.hpp"
 
 namespace mimo {

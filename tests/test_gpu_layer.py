@@ -240,6 +240,106 @@ def test_scan_step(dtype, D, G, N, pad, idx):
     assert torch.equal(pool[idle], before[idle]) and torch.equal(pool[:, D:], before[:, D:])
 
 
+def test_optional_inputs_left_out():
+    """No initial state, no gradient of the last state, nothing but the recurrence."""
+    g = _gen(12)
+    for S in (9, 16, 90, 400):
+        x = _scan_inputs(g, (2, S), 2, 20, 2, 16, FF, sp=False, skip=False, gate=False, bias=False, init=False)
+        dout = torch.randn(2, S, 20, generator=g).cuda()
+        gr = m.mamba_scan_bwd(dout, **x)
+        o = m.mamba_scan_fwd(**x)
+        assert o.state is None and gr.dd is gr.dz is gr.ddt_bias is gr.dinitial_state is None
+        args = [x[k] for k in ("u", "dt", "a", "b", "c", "d", "z", "dt_bias", "initial_state")]
+        ref, mag = (R.scan(*args, None, False, dout, None, mag=k) for k in (False, True))
+        R.check({"out": o.out}, ref, mag, 8 * S + 56, S)
+        R.check(gr._asdict(), ref, mag, 16 * S + 96, S)
+        w = torch.randn(20, 3, generator=g).cuda()
+        gc = m.mamba_conv_bwd(dout, x["u"], w)
+        ref, mag = (R.conv(x["u"], w, None, None, None, False, dout, None, mag=k) for k in (False, True))
+        assert gc.dbias is gc.dinitial_state is None
+        R.check(gc._asdict(), ref, mag, 6 + 16 + 128, S)
+
+
+def test_special_values():
+    """a = -inf forgets at once, a = 0 and a step of zero keep everything, large steps and gates saturate; NaN in a
+    parameter of one channel stays in that channel."""
+    g = _gen(13)
+    x = _scan_inputs(g, (1, 50), 1, 70, 1, 16, FF)
+    x["a"][3] = float("-inf")
+    x["a"][4] = 0.0
+    x["dt"][0, :, 5] = -200.0
+    x["dt"][0, :, 6] = 90.0
+    x["z"][0, :, 7], x["z"][0, :, 8] = -300.0, 300.0
+    args = [x[k].clone() for k in ("u", "dt", "a", "b", "c", "d", "z", "dt_bias", "initial_state")]
+    o = m.mamba_scan_fwd(**x, dt_softplus=True, return_state=True)
+    ref, mag = (R.scan(*args, None, True, mag=k) for k in (False, True))
+    R.check({"out": o.out, "state": o.state}, ref, mag, 8 * 50 + 56)
+    y = m.mamba_scan_step(x["u"][:, 0], x["dt"][:, 0], x["initial_state"].clone(), x["a"],
+                          x["b"][:, 0], x["c"][:, 0], x["d"], x["z"][:, 0], x["dt_bias"], dt_softplus=True)
+    R.check({"out": y}, {"out": ref["out"][:, 0]}, {"out": mag["out"][:, 0]}, 64)
+    x["a"][9, 2] = float("nan")
+    p = m.mamba_scan_fwd(**x, dt_softplus=True, return_state=True)
+    assert p.out[0, :, 9].isnan().all() and p.state[0, 9, 2].isnan()
+    keep = [k for k in range(70) if k != 9]
+    assert _same(p.out[..., keep], o.out[..., keep])
+
+
+def test_far_offsets():
+    """Tensors of more than 2^31 elements: what lies behind that gives what it gives alone."""
+    T, D, n = (1 << 21) + 130, 1024, 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    tail = slice(T - n, T)
+    u, z = (torch.empty(T, D, dtype=BF, device="cuda") for _ in range(2))
+    for t in (u, z):
+        t.normal_(generator=g)
+    cu = torch.tensor([0, T - n, T], dtype=torch.int32).cuda()
+    w = torch.randn(D, 4, generator=g, device="cuda")
+    one = torch.tensor([0, n], dtype=torch.int32).cuda()
+    c = m.mamba_conv_fwd(u, w, cu_seqlens=cu, activation="silu", return_state=True)
+    c1 = m.mamba_conv_fwd(u[tail].clone(), w, cu_seqlens=one, activation="silu", return_state=True)
+    assert _same(c.out[tail], c1.out) and _same(c.state[1], c1.state[0])
+    gc, gc1 = m.mamba_conv_bwd(z, u, w, cu_seqlens=cu), m.mamba_conv_bwd(z[tail].clone(), u[tail].clone(), w, cu_seqlens=one)
+    assert _same(gc.dx[tail], gc1.dx)
+    y = m.mamba_norm_fwd(u, w[:, 0].contiguous(), None, z, groups=2)
+    assert _same(y[tail], m.mamba_norm_fwd(u[tail].clone(), w[:, 0].contiguous(), None, z[tail].clone(), groups=2))
+    gn = m.mamba_norm_bwd(z, u, w[:, 0].contiguous(), None, c.out, groups=2)
+    gn1 = m.mamba_norm_bwd(z[tail].clone(), u[tail].clone(), w[:, 0].contiguous(), None, c.out[tail].clone(), groups=2)
+    assert _same(gn.dx[tail], gn1.dx) and _same(gn.dz[tail], gn1.dz)
+    del c, gc, y, gn
+    a = -torch.rand(D, 16, generator=g, device="cuda") - 0.1
+    b = torch.randn(T, 1, 16, generator=g, device="cuda").to(BF)
+    bias = torch.full((D,), -2.0, device="cuda")
+    s = m.mamba_scan_fwd(u, z, a, b, b, None, u, bias, None, cu, dt_softplus=True, return_state=True)
+    ut, zt, bt = u[tail].clone(), z[tail].clone(), b[tail].clone()
+    s1 = m.mamba_scan_fwd(ut, zt, a, bt, bt, None, ut, bias, None, one, dt_softplus=True, return_state=True)
+    tol = dict(rtol=2 ** -7, atol=2 ** -7)      # other chunks: fp32 rounding, then at most a step of bf16 in values of about one
+    assert torch.allclose(s.out[tail].float(), s1.out.float(), **tol) and torch.allclose(s.state[1], s1.state[0], rtol=1e-4, atol=1e-4)
+    del s
+    gs = m.mamba_scan_bwd(u, u, z, a, b, b, None, z, bias, None, None, cu, dt_softplus=True)
+    g1 = m.mamba_scan_bwd(ut, ut, zt, a, bt, bt, None, zt, bias, None, None, one, dt_softplus=True)
+    for k in ("du", "ddt", "dz"):
+        p, q = getattr(gs, k)[tail].float(), getattr(g1, k).float()
+        assert float((p - q).norm() / q.norm()) < 2 ** -8, k
+    for k in ("db", "dc"):
+        p, q = getattr(gs, k)[tail].float(), getattr(g1, k).float()
+        assert float((p - q).norm() / q.norm()) < 2 ** -8, k
+    # a pool whose last slot starts behind 2^31 elements
+    del gs, u, z, b
+    slots = (1 << 31) // (3 * D) + 3
+    pool = torch.empty(slots, 3, D, dtype=BF, device="cuda")
+    pool[-1].normal_(generator=g)
+    alone, x = pool[-1:].clone(), ut[:1]
+    y = m.mamba_conv_step(x, pool, w, None, torch.tensor([slots - 1], dtype=torch.int32).cuda())
+    assert _same(y, m.mamba_conv_step(x, alone, w)) and _same(pool[-1], alone[0])
+    del pool
+    slots = (1 << 31) // (16 * D) + 3
+    pool = torch.empty(slots, D, 16, device="cuda")
+    pool[-1].normal_(generator=g)
+    alone = pool[-1:].clone()
+    y = m.mamba_scan_step(x, x, pool, a, bt[:1], bt[:1], state_indices=torch.tensor([slots - 1], dtype=torch.int32).cuda(), dt_softplus=True)
+    assert _same(y, m.mamba_scan_step(x, x, alone, a, bt[:1], bt[:1], dt_softplus=True)) and _same(pool[-1], alone[0])
+
+
 def test_scan_gradients_against_differences():
     """A central difference of the GPU forward pass in fp32 along random directions. With h = 2^-7 the truncation is h^2
     times third derivatives (about 1e-4 of the value), the rounding of an output sum 1e-6 / h."""
