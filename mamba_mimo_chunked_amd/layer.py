@@ -222,7 +222,7 @@ def _call(fn, values, device, workspace=None):
         workspace = _workspace(workspace, need.value, device)
         values = (*values, 0, 0) if workspace is None else (*values, workspace.data_ptr(), workspace.numel())
     args, stream = pack(*values), torch._C._cuda_getCurrentRawStream(device.index)
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == device.index:
         st = call(args, stream)
     else:
         with torch.cuda.device(device):
@@ -239,13 +239,15 @@ def _activation(activation):
 
 
 def _check_filter(weight, bias, D, device):
-    if weight.dim() != 2 or weight.shape[0] != D:
-        raise ValueError(f"weight must have shape [{D}, taps], got {list(weight.shape)}")
-    W = weight.shape[1]
-    weight, bias = _param("weight", weight, weight.shape, _F32, device), _param("bias", bias, (D,), _F32, device)
+    shape = weight.shape
+    if len(shape) != 2 or shape[0] != D:
+        raise ValueError(f"weight must have shape [{D}, taps], got {list(shape)}")
+    W = shape[1]
+    if weight.dtype != _F32 or weight.device != device:
+        _check_tensor("weight", weight, shape, _F32, device)
     if not 2 <= W <= 8:
         raise NotImplementedError(f"mamba_conv supports 2 to 8 taps, got {W}")
-    return W, weight, bias
+    return W, weight if weight.is_contiguous() else weight.contiguous(), _param("bias", bias, (D,), _F32, device)
 
 
 def mamba_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, *, activation: Optional[str] = None,
@@ -299,10 +301,12 @@ def mamba_conv_bwd(dout, x, weight, bias=None, initial_state=None, dstate=None, 
 
 def _check_pool(state, inner, dtype, indices, n, device):
     """A pool of states [slots, ...]: dense inside a slot, slots that do not overlap, updated in place."""
-    if state.dim() != 3 or state.shape[1:] != inner:
-        raise ValueError(f"state must have shape [slots, {', '.join(map(str, inner))}], got {list(state.shape)}")
-    slots, size = state.shape[0], inner[0] * inner[1]
-    _fits("state", state, (slots, *inner), dtype, device)
+    shape = state.shape
+    if len(shape) != 3 or shape[1] != inner[0] or shape[2] != inner[1]:
+        raise ValueError(f"state must have shape [slots, {', '.join(map(str, inner))}], got {list(shape)}")
+    slots, size = shape[0], inner[0] * inner[1]
+    if state.dtype != dtype or state.device != device:
+        _check_tensor("state", state, shape, dtype, device)
     if slots < 1:
         raise ValueError("state must have at least one slot")
     stride = size
@@ -328,9 +332,10 @@ def mamba_conv_step(x, state, weight, bias=None, state_indices=None, *, activati
     dev = _device("mamba_conv_step", "x", x)
     code = _data_dtype("x", x)
     silu = _activation(activation)
-    if x.dim() != 2 or x.numel() == 0:
-        raise ValueError(f"x must have shape [n, D] and not be empty, got {list(x.shape)}")
-    n, D = x.shape
+    shape = x.shape
+    if len(shape) != 2 or 0 in shape:
+        raise ValueError(f"x must have shape [n, D] and not be empty, got {list(shape)}")
+    n, D = shape
     W, weight, bias = _check_filter(weight, bias, D, dev)
     slots, stride, idx = _check_pool(state, (W - 1, D), x.dtype, state_indices, n, dev)
     x = _dense_inner(x, 1)
@@ -344,20 +349,21 @@ def mamba_conv_step(x, state, weight, bias=None, state_indices=None, *, activati
 # ---------------------------------------------------------------- selective scan
 def _check_scan(u, dt, a, b, c, d, z, dt_bias, lead, dev):
     """Sizes and the tensors with dense inner axes, parameters contiguous."""
-    D, dtype = u.shape[-1], u.dtype
-    if a.dim() != 2 or a.shape[0] != D:
-        raise ValueError(f"a must have shape [{D}, N], got {list(a.shape)}")
-    N, shape = a.shape[1], b.shape
-    if len(shape) != len(lead) + 2 or shape[:-2] != lead or shape[-1] != N:
+    rows, dtype, ashape, shape = u.shape, u.dtype, a.shape, b.shape
+    D = rows[-1]
+    if len(ashape) != 2 or ashape[0] != D:
+        raise ValueError(f"a must have shape [{D}, N], got {list(ashape)}")
+    N = ashape[1]
+    if shape[:-2] != lead or len(shape) < 2 or shape[-1] != N:
         raise ValueError(f"b must have shape {[*lead, 'G', N]}, got {list(shape)}")
     G = shape[-2]
     if G < 1 or N < 1 or D % G:
         raise ValueError(f"the {D} channels must be divisible by the {G} groups of b and c, and a must have states")
     if N > 128:
         raise NotImplementedError(f"mamba_scan supports at most 128 states, got {N}")
-    data = (_dense_inner(u, 1), _data("dt", dt, u.shape, dtype, dev), _data("b", b, shape, dtype, dev, 2), _data("c", c, shape, dtype, dev, 2),
-            _data("z", z, u.shape, dtype, dev))
-    return D, G, N, data, (_param("a", a, (D, N), _F32, dev), _param("d", d, (D,), _F32, dev), _param("dt_bias", dt_bias, (D,), _F32, dev))
+    data = (_dense_inner(u, 1), _data("dt", dt, rows, dtype, dev), _data("b", b, shape, dtype, dev, 2), _data("c", c, shape, dtype, dev, 2),
+            _data("z", z, rows, dtype, dev))
+    return D, G, N, data, (_param("a", a, ashape, _F32, dev), _param("d", d, (D,), _F32, dev), _param("dt_bias", dt_bias, (D,), _F32, dev))
 
 
 def mamba_scan_fwd(u, dt, a, b, c, d=None, z=None, dt_bias=None, initial_state=None, cu_seqlens=None, *, dt_softplus: bool = False,
@@ -417,9 +423,10 @@ def mamba_scan_step(u, dt, state, a, b, c, d=None, z=None, dt_bias=None, state_i
     D, N] float32 is updated in place. Slots and ``state_indices`` as for ``mamba_conv_step``."""
     dev = _device("mamba_scan_step", "u", u)
     code = _data_dtype("u", u)
-    if u.dim() != 2 or u.numel() == 0:
-        raise ValueError(f"u must have shape [n, D] and not be empty, got {list(u.shape)}")
-    n = u.shape[0]
+    shape = u.shape
+    if len(shape) != 2 or 0 in shape:
+        raise ValueError(f"u must have shape [n, D] and not be empty, got {list(shape)}")
+    n = shape[0]
     D, G, N, (u, dt, b, c, z), (a, d, dt_bias) = _check_scan(u, dt, a, b, c, d, z, dt_bias, (n,), dev)
     slots, stride, idx = _check_pool(state, (D, N), _F32, state_indices, n, dev)
     _apart("state", state, u=u, dt=dt, b=b, c=c, z=z, a=a, d=d, dt_bias=dt_bias, state_indices=idx)
