@@ -8,7 +8,7 @@
 // Two channels a thread and many threads beat wider accesses, whose windows cost the registers that
 // keep waves, and so loads, in flight: [8192, 2048] bf16 forward 18.5 us with eight channels, 17.1 with
 // four, 16.1 with two; [4, 4100, 2048] bf16 backward 156, 60 and 57 us. With scalar rows and the blocks' order
-// below, 15.1 us (4.4 TB/s) and 52 us; 8 x 8192 x 2048 forward 104 us (5.2 TB/s, as a copy).
+// below, 14.0 us (4.8 TB/s) and 52 us (3.9); 8 x 8192 x 2048 forward 104 us (5.2 TB/s, as a copy).
 #include "layer.hpp"
 
 namespace mimo {
@@ -309,15 +309,15 @@ template <int DT, int VEC, int W> __global__ __launch_bounds__(256) void k_conv_
 }
 
 // ---------------------------------------------------------------- host side
-// Tokens of a chunk: about 1024 threads a CU, 16 tokens at least. Longer chunks read fewer rows twice, and the
-// backward pass leaves fewer partial sums; 32 suffice forward (8 x 8192 x 2048 bf16: 107 us at 32, 115 at 128), where the
-// backward pass gains up to 128 (243 us at 64, 208 at 128).
-int chunk_tokens(int64_t n, int64_t S, bool packed, int64_t nvec, int most) {
-    const int64_t T = packed ? S : n * S;
-    const int64_t c = T * nvec / (256 * 1024) / 8 * 8;
+// Tokens of a chunk, 16 at least: longer chunks read fewer rows twice, and the backward pass leaves fewer partial
+// sums; shorter ones keep more threads, and so loads, in flight. Forward 2048 threads a CU and up to 32 tokens
+// ([8192, 2048] bf16: 14.0 us, 15.1 with 1024 threads; 8 x 8192 x 2048: 104 us at 32 tokens, 115 at 128); backward
+// 1024 threads a CU, whose registers allow no more, and up to 128 tokens ([4, 4100, 2048] bf16: 52 us, 55 with 2048;
+// 8 x 8192 x 2048: 243 us at 64 tokens, 208 at 128, before the scalar rows).
+int chunk_tokens(int64_t n, int64_t S, bool packed, int64_t nvec, bool backward) {
+    const int64_t T = packed ? S : n * S, c = T * nvec / (256 * (backward ? 1024 : 2048)) / 8 * 8, most = backward ? 128 : 32;
     return (int)(c < 16 ? 16 : c > most ? most : c);
 }
-constexpr int MOST_FWD = 32, MOST_BWD = 128;
 
 Seqs make_seqs(int64_t n, int64_t S, const int32_t* cu, int CH) {
     return Seqs{cu, (int)n, (int)S, CH, (int)((S + CH - 1) / CH)};
@@ -397,7 +397,7 @@ mimo_status plan_bwd(const mamba_conv_bwd_args* a, BwdPlan* pl) {
     for (const void* x : {a->initial_state, a->dstate, (const void*)a->dx, (const void*)a->dinitial_state}) even = even && aligned(x, 0, 0, 2 * esz, 1);
     pl->vec = vec_of(a->D, even);
     const bool packed = a->cu_seqlens != nullptr;
-    pl->CH = chunk_tokens(a->n, a->S, packed, a->D / pl->vec, MOST_BWD);
+    pl->CH = chunk_tokens(a->n, a->S, packed, a->D / pl->vec, true);
     const Seqs q = make_seqs(a->n, a->S, a->cu_seqlens, pl->CH);
     const long groups = (slots_of(q) + WS - 1) / WS;
     if (slots_of(q) > (long)1 << 30) return unsupported("too many tokens");
@@ -428,7 +428,7 @@ mimo_status mamba_conv_fwd(const mamba_conv_fwd_args* a, void* stream) {
     ConvParams p{};
     p.D = (int)a->D;
     p.nvec = p.D / vec;
-    p.q = make_seqs(a->n, a->S, a->cu_seqlens, chunk_tokens(a->n, a->S, packed, p.nvec, MOST_FWD));
+    p.q = make_seqs(a->n, a->S, a->cu_seqlens, chunk_tokens(a->n, a->S, packed, p.nvec, false));
     p.slots = slots_of(p.q);
     if (p.slots > (long)1 << 30) return unsupported("too many tokens");
     p.silu = a->silu;

@@ -19,7 +19,9 @@ struct StepParams {
 // reads and writes whole lines of the state [D, N], which is nearly all the traffic (8 bytes a state
 // against some twenty operations), and <c, h> is a sum over LPC lanes. A thread takes STEP_CH channels,
 // and everything it reads is asked for before the first use: the chain from a row's index to its store is
-// what a wave waits for. VEC: four states (and four of b, of c) in one access.
+// what a wave waits for. VEC: four states (and four of b, of c) in one
+// access. 128 rows, D = 2048, N = 64 from a pool: 28.6 us, 4.8 TB/s (40 with the inputs asked for behind the index
+// check; two channels 30.2, one 31.3, four 37.8 at that point).
 constexpr int STEP_CH = 2;
 template <int DT, int LPC, bool VEC> __global__ __launch_bounds__(256) void k_step(StepParams p) {
     typedef raw_t<DT> raw;
@@ -123,9 +125,10 @@ struct FwdPlan {
     size_t off_sdt, bytes;
 };
 
-// One wave per SIMD keeps the vector units busy (NS independent recurrences), two hide the loads: chunks
-// are cut until about 2048 waves walk, but not below 32 tokens. A second walk (the aggregates) nearly
-// doubles the work, so half the GPU's waves (512) without chunks are as good as chunks.
+// Chunks are cut until about 3072 waves walk (three a SIMD), but, as a chunk costs its loads and its aggregate, not
+// below 64 tokens while 2048 waves walk, nor below 32 at all ([8192, 1024], N = 16: 80 us at 64 tokens, 87 at 48;
+// [8 x 2048, 2048]: 257 us for 3072 waves, 268 for 2048). Half the GPU's waves (512) without chunks are as good as
+// chunks, whose second walk (the aggregates) nearly doubles the work.
 mimo_status plan_fwd(const mamba_scan_fwd_args* a, FwdPlan* pl) {
     if (a == nullptr) return bad("args must not be NULL");
     const mimo_status s = check_scan(a->n, a->S, a->D, a->G, a->N, a->dtype);
@@ -133,8 +136,9 @@ mimo_status plan_fwd(const mamba_scan_fwd_args* a, FwdPlan* pl) {
     const bool packed = a->cu_seqlens != nullptr;
     pl->tpg = (int)((a->D / a->G + 63) / 64);
     const int64_t waves = a->G * pl->tpg * waves_for(a->N), T = packed ? a->S : a->n * a->S;
-    int64_t CH = (T * waves / 3072 + 15) / 16 * 16;
-    if (CH < 64) CH = (T * waves / 2048 + 15) / 16 * 16 < 64 ? (T * waves / 2048 + 15) / 16 * 16 : 64;
+    auto tokens_for = [&](int64_t count) { return (T * waves / count + 15) / 16 * 16; };
+    int64_t CH = tokens_for(3072);
+    if (CH < 64) CH = tokens_for(2048) < 64 ? tokens_for(2048) : 64;
     CH = CH < 32 ? 32 : CH > 4096 ? 4096 : CH;
     if (a->S <= 64 || (!packed && a->n * waves >= 512)) CH = (a->S + 15) / 16 * 16;
     pl->q = Seqs{a->cu_seqlens, (int)a->n, (int)a->S, (int)CH, (int)((a->S + CH - 1) / CH)};

@@ -4,15 +4,20 @@
 //   h[t] = exp(dt[t] a) h[t-1] + dt[t] u[t] b[t],  y[t] = <c[t], h[t]> + d u[t],  out = y silu(z)
 //
 // The decay depends on token, channel and state, so there is no matrix form: a token costs a channel
-// N exponentials (a quarter of the rate of a multiply-add) and four multiplies or multiply-adds each.
-// A lane owns one channel with NS states in registers (no exchange between lanes: <c, h> is a sum
-// inside the lane), a block 64 channels with N split over KS waves; b and c of a tile of TT tokens
-// lie in LDS and are read as broadcasts. Loads of the next tile are in flight during a tile.
+// N exponentials (half the rate of a multiply-add on this GPU) and four multiplies or multiply-adds
+// each, which bind, not memory: 6 issue slots a state forward, against 0.5 bytes at N = 16. A lane owns
+// one channel with NS states in registers (no exchange between lanes: <c, h> is a sum inside the lane), a
+// block 64 channels with N split over KS waves; b and c of a tile of tokens lie in LDS and are read as
+// broadcasts. Loads of the next tile are in flight during a tile; rows are addressed by scalars; tokens
+// behind the chunk take a step of zero, so that nothing in a tile branches (120 vector instructions a
+// token and 16 states, 138 before).
 //
-// Where channels alone do not fill the GPU the time axis is cut into chunks: k_aggregate walks every
+// Where channels alone do not fill the GPU the time axis is cut into chunks: k_walk<AGG> walks every
 // chunk but a sequence's last from zero (its last state, and the sum of dt, which gives the chunk's
-// decay exp(a sum dt)), k_carry chains the states that enter the chunks, and k_scan_fwd walks the
-// chunks from them.
+// decay exp(a sum dt)), k_carry chains the states that enter the chunks, and k_walk<FWD> walks the
+// chunks from them. Measured, [8192, 1024] bf16, N = 16: 35 + 8 + 44 us (vector units busy 65 to 70 % of
+// the time at two waves a SIMD; three or four waves, with fewer registers or shorter chunks, were slower);
+// [8 x 2048, 2048]: 243 us in all, 77 % busy.
 #pragma once
 #include "layer.hpp"
 
@@ -89,13 +94,12 @@ __device__ __forceinline__ float decay_base(float a) {
 // FWD: the outputs. AGG: a chunk's last state from zero. AGG2: also the adjoint that leaves it to the
 // left, sum_t exp(a sum_{s <= t} dt) c[t] dy[t], from the same exponentials.
 enum { FWD, AGG, AGG2 };
-#ifndef WALK_WAVES
-#define WALK_WAVES 2
-#endif
+constexpr int WALK_WAVES = 2;   // waves a SIMD that the registers have to allow
 
 constexpr int UNIT = 16;   // tokens of a unit (backward)
 
 // tokens of a tile: what a lane keeps in registers, or the waves of a block share in LDS
+// ([8 x 2048, 2048], KS = 1: 243 us with 8, 281 with 4, 282 with 16; [4100, 2048], KS = 4: 242 with 16, 313 with 32)
 constexpr int tile_tokens(int KS) { return KS == 1 ? 8 : 16; }
 
 template <int DT, int NS, int KS, int MODE> __global__ __launch_bounds__(64 * KS, KS == 1 ? WALK_WAVES : 2) void k_walk(ScanParams p) {
