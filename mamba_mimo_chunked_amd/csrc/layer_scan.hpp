@@ -15,9 +15,9 @@
 // Where channels alone do not fill the GPU the time axis is cut into chunks: k_walk<AGG> walks every
 // chunk but a sequence's last from zero (its last state, and the sum of dt, which gives the chunk's
 // decay exp(a sum dt)), k_carry chains the states that enter the chunks, and k_walk<FWD> walks the
-// chunks from them. Measured, [8192, 1024] bf16, N = 16: 35 + 8 + 44 us (vector units busy 65 to 70 % of
-// the time at two waves a SIMD; three or four waves, with fewer registers or shorter chunks, were slower);
-// [8 x 2048, 2048]: 243 us in all, 77 % busy.
+// chunks from them. Measured, [8192, 1024] bf16, N = 16: 35 + 6 + 44 us; [8 x 2048, 2048]: 243 us in all.
+// From the two sizes: vector units 88 % busy behind a fixed 6 to 9 us a kernel (launch, first loads, drain).
+// More waves a SIMD, with fewer registers or shorter chunks, were slower.
 #pragma once
 #include "layer.hpp"
 
@@ -355,12 +355,14 @@ template <int DT, int MODE> mimo_status launch_walk(const ScanParams& p, hipStre
     if (p.N <= 64) return launch(&k_walk<DT, 16, 4, MODE>, grid, 256, 0, st, p);
     return launch(&k_walk<DT, 16, 8, MODE>, grid, 512, 0, st, p);
 }
-// at most `chunks` chunks in a sequence
+// At most `chunks` chunks in a sequence. Four states a thread where that still makes a block for each CU (7 x 2048 x 64
+// states: 13 us, 23 with one), else one ([1024, 16]: 6.3 us, 7.8 with four).
 template <bool ADJ> mimo_status launch_carry(const ScanParams& p, long chunks, hipStream_t st) {
-    const long waves = (chunks + SPAN - 1) / SPAN;
-    const int V = p.vec ? 4 : 1, block = 64 * (int)(waves < SPAN_WAVES ? waves : SPAN_WAVES);
-    const dim3 grid((unsigned)(((long)p.D * p.N / V + 63) / 64), ADJ ? 2 : 1, p.q.n);
-    return p.vec ? launch(&k_carry<ADJ, 4>, grid, block, 0, st, p) : launch(&k_carry<ADJ, 1>, grid, block, 0, st, p);
+    const long waves = (chunks + SPAN - 1) / SPAN, states = (long)p.D * p.N;
+    const int block = 64 * (int)(waves < SPAN_WAVES ? waves : SPAN_WAVES), dirs = ADJ ? 2 : 1;
+    if (p.vec && (states + 255) / 256 * dirs * p.q.n >= 256)
+        return launch(&k_carry<ADJ, 4>, dim3((unsigned)((states + 255) / 256), dirs, p.q.n), block, 0, st, p);
+    return launch(&k_carry<ADJ, 1>, dim3((unsigned)((states + 63) / 64), dirs, p.q.n), block, 0, st, p);
 }
 inline int waves_for(int64_t N) { return N <= 16 ? 1 : N <= 32 ? 2 : N <= 64 ? 4 : 8; }
 

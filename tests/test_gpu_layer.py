@@ -83,7 +83,7 @@ CONV = [  # dtype, taps, D, sequences, bias, initial state, silu, strided
     (BF, 4, 264, PACKED, True, True, True, False), (HF, 4, 33, PACKED, True, False, False, True), (FF, 5, 20, (2, 50), True, True, True, False),
     (BF, 6, 44, (1, 40), True, True, True, False), (HF, 7, 12, PACKED, False, True, True, False), (BF, 8, 36, (2, 29), True, True, True, False),
     (FF, 8, 7, ("packed", [3, 0, 0, 9], 0), True, True, True, False), (BF, 4, 2056, (1, 300), True, True, True, False),
-    (FF, 4, 4, ("packed", [200] + [1] * 70, 40), True, True, True, False),
+    (FF, 4, 4, ("packed", [200] + [1] * 70, 40), True, True, True, False), (BF, 3, 10, ("packed", [0, 0], 5), True, True, True, False),
 ]
 
 
@@ -175,6 +175,7 @@ SCAN = [  # dtype, D, G, N, sequences, options
     (BF, 130, 2, 16, ("packed", [300, 0, 1, 129], 50), {}), (HF, 12, 1, 7, ("packed", [1], 0), dict(sp=False, gate=False, skip=False, bias=False, init=False)),
     (FF, 36, 2, 33, PACKED, dict(gate=False, init=False)), (BF, 68, 1, 3, PACKED, dict(strided=True)), (FF, 5, 1, 6, ("packed", [0, 0, 3], 0), {}),
     (FF, 64, 1, 16, ("packed", [2] * 65, 3), {}), (BF, 16, 16, 8, (2, 35), {}), (FF, 260, 1, 9, (1, 66), {}),
+    (BF, 20, 1, 16, ("packed", [0, 0], 70), {}), (FF, 64, 1, 16, (40, 20), {}), (HF, 512, 1, 16, (70, 3), {}),
 ]
 
 
