@@ -125,10 +125,11 @@ struct FwdPlan {
     size_t off_sdt, bytes;
 };
 
-// Chunks are cut until about 3072 waves walk (three a SIMD), but, as a chunk costs its loads and its aggregate, not
-// below 64 tokens while 2048 waves walk, nor below 32 at all ([8192, 1024], N = 16: 80 us at 64 tokens, 87 at 48;
-// [8 x 2048, 2048]: 257 us for 3072 waves, 268 for 2048). Half the GPU's waves (512) without chunks are as good as
-// chunks, whose second walk (the aggregates) nearly doubles the work.
+// Chunks are cut until about 6144 units of work (waves_for) walk, but, as a chunk costs its loads and its aggregate, not
+// below 64 tokens while 2048 walk, nor below 32 at all ([8192, 1024], N = 16: 69 us at 64 tokens, 71 at 48, 75 at 96;
+// [8192, 1024], N = 32: 109 us, 119 with half as many units; packed prompts [4100, 2048], N = 64: 220 us, 236 with half,
+// 217 with a third more, which has a third more memory for the states). Half the GPU's waves (512 units) without chunks
+// are as good as chunks, whose second walk (the aggregates) nearly doubles the work.
 mimo_status plan_fwd(const mamba_scan_fwd_args* a, FwdPlan* pl) {
     if (a == nullptr) return bad("args must not be NULL");
     const mimo_status s = check_scan(a->n, a->S, a->D, a->G, a->N, a->dtype);
@@ -137,7 +138,7 @@ mimo_status plan_fwd(const mamba_scan_fwd_args* a, FwdPlan* pl) {
     pl->tpg = (int)((a->D / a->G + 63) / 64);
     const int64_t waves = a->G * pl->tpg * waves_for(a->N), T = packed ? a->S : a->n * a->S;
     auto tokens_for = [&](int64_t count) { return (T * waves / count + 15) / 16 * 16; };
-    int64_t CH = tokens_for(3072);
+    int64_t CH = tokens_for(6144);
     if (CH < 64) CH = tokens_for(2048) < 64 ? tokens_for(2048) : 64;
     CH = CH < 32 ? 32 : CH > 4096 ? 4096 : CH;
     if (a->S <= 64 || (!packed && a->n * waves >= 512)) CH = (a->S + 15) / 16 * 16;
@@ -154,7 +155,7 @@ template <int DT> mimo_status run_fwd(const ScanParams& p, hipStream_t st) {
     if (p.chunked) {
         mimo_status s = launch_walk<DT, AGG>(p, st);
         if (s != MIMO_OK) return s;
-        s = launch_carry<false>(p, p.q.nc, st);
+        s = launch_carry<false>(p, st);
         if (s != MIMO_OK) return s;
     }
     return launch_walk<DT, FWD>(p, st);

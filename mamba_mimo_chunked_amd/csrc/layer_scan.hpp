@@ -6,18 +6,15 @@
 // The decay depends on token, channel and state, so there is no matrix form: a token costs a channel
 // N exponentials (half the rate of a multiply-add on this GPU) and four multiplies or multiply-adds
 // each, which bind, not memory: 6 issue slots a state forward, against 0.5 bytes at N = 16. A lane owns
-// one channel with NS states in registers (no exchange between lanes: <c, h> is a sum inside the lane), a
-// block 64 channels with N split over KS waves; b and c of a tile of tokens lie in LDS and are read as
+// one channel with NS states in registers, a block 64 channels with N split over KS waves; the waves share
+// the steps of a tile of tokens and add up <c, h> in LDS, where b and c of the tile lie too and are read as
 // broadcasts. Loads of the next tile are in flight during a tile; rows are addressed by scalars; tokens
-// behind the chunk take a step of zero, so that nothing in a tile branches (120 vector instructions a
-// token and 16 states, 138 before).
+// behind the chunk take a step of zero, so that nothing in a tile branches.
 //
 // Where channels alone do not fill the GPU the time axis is cut into chunks: k_walk<AGG> walks every
 // chunk but a sequence's last from zero (its last state, and the sum of dt, which gives the chunk's
 // decay exp(a sum dt)), k_carry chains the states that enter the chunks, and k_walk<FWD> walks the
-// chunks from them. Measured, [8192, 1024] bf16, N = 16: 35 + 6 + 44 us; [8 x 2048, 2048]: 243 us in all.
-// From the two sizes: vector units 88 % busy behind a fixed 6 to 9 us a kernel (launch, first loads, drain).
-// More waves a SIMD, with fewer registers or shorter chunks, were slower.
+// chunks from them. Measured, [8192, 1024] bf16, N = 16: 69 us for the three; [8 x 2048, 2048]: 224 us.
 #pragma once
 #include "layer.hpp"
 
@@ -94,17 +91,20 @@ __device__ __forceinline__ float decay_base(float a) {
 // FWD: the outputs. AGG: a chunk's last state from zero. AGG2: also the adjoint that leaves it to the
 // left, sum_t exp(a sum_{s <= t} dt) c[t] dy[t], from the same exponentials.
 enum { FWD, AGG, AGG2 };
-constexpr int WALK_WAVES = 2;   // waves a SIMD that the registers have to allow
+// Waves a SIMD that the registers have to allow. Five for the narrow walks, whose few registers hold that many ([8192,
+// 1024], N = 16: 70.5 us without the bound, 69 with); six spill in the backward walk (N = 8: 91 us instead of 80).
+constexpr int walk_waves(int NS, int KS) { return KS == 1 ? 2 : NS == 4 ? 5 : KS == 16 ? 4 : 2; }
 
 constexpr int UNIT = 16;   // tokens of a unit (backward)
 
-// tokens of a tile: what a lane keeps in registers, or the waves of a block share in LDS
-// ([8 x 2048, 2048], KS = 1: 243 us with 8, 281 with 4, 282 with 16; [4100, 2048], KS = 4: 242 with 16, 313 with 32)
-constexpr int tile_tokens(int KS) { return KS == 1 ? 8 : 16; }
+// Tokens of a tile: what a lane keeps in registers, or the waves of a block share in LDS: 16, or 8 where one wave holds
+// all states and in the backward walk of few waves ([4 x 4096, 1024], N = 16, backward: 327 us with 8, 332 with 16; forward
+// [8 x 2048, 2048]: 224 us with 16, 231 with 8, 260 with 32).
+constexpr int tile_tokens(int KS, int MODE) { return KS == 1 || (KS <= 4 && MODE == AGG2) ? 8 : 16; }
 
-template <int DT, int NS, int KS, int MODE> __global__ __launch_bounds__(64 * KS, KS == 1 ? WALK_WAVES : 2) void k_walk(ScanParams p) {
+template <int DT, int NS, int KS, int MODE> __global__ __launch_bounds__(64 * KS, walk_waves(NS, KS)) void k_walk(ScanParams p) {
     typedef raw_t<DT> raw;
-    constexpr int TT = tile_tokens(KS), NP = NS * KS, TPW = TT / KS, NB = (TT * NP + 64 * KS - 1) / (64 * KS);
+    constexpr int TT = tile_tokens(KS, MODE), NP = NS * KS, TPW = TT / KS, NB = (TT * NP + 64 * KS - 1) / (64 * KS);
     constexpr bool C = MODE != AGG, OUT = MODE == FWD, ONE = KS == 1;
     __shared__ float s_dt[ONE ? 1 : TT][64], s_du[ONE ? 1 : TT][64], s_dy[!ONE && MODE == AGG2 ? TT : 1][64];
     __shared__ __attribute__((aligned(16))) float s_b[TT][NP], s_c[C ? TT : 1][NP];
@@ -281,8 +281,9 @@ template <int DT, int NS, int KS, int MODE> __global__ __launch_bounds__(64 * KS
 constexpr int SPAN = 8, SPAN_WAVES = 16;
 template <bool ADJ, int V> __global__ __launch_bounds__(64 * SPAN_WAVES) void k_carry(ScanParams p) {
     typedef float vec __attribute__((ext_vector_type(V)));
-    __shared__ vec s_h[SPAN_WAVES][64], s_p[SPAN_WAVES][64];
+    extern __shared__ __attribute__((aligned(16))) float lds[];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    vec *s_h = reinterpret_cast<vec*>(lds), *s_p = s_h + waves * 64;   // [waves][64] each
     const int i = blockIdx.z;
     const unsigned step = (unsigned)p.D * p.N, s = min((blockIdx.x * 64 + lane) * V, step - V), d = s / (unsigned)p.N;
     const bool rev = ADJ && blockIdx.y, act = (blockIdx.x * 64 + lane) * V < step;
@@ -319,12 +320,12 @@ template <bool ADJ, int V> __global__ __launch_bounds__(64 * SPAN_WAVES) void k_
             }
         vec g = h;
         if (waves > 1) {
-            s_h[w][lane] = fold;
-            s_p[w][lane] = prod;
+            s_h[w * 64 + lane] = fold;
+            s_p[w * 64 + lane] = prod;
             __syncthreads();
             for (int o = 0; o < waves; ++o) {
                 if (o == w) g = h;
-                const vec f = s_h[o][lane], q = s_p[o][lane];
+                const vec f = s_h[o * 64 + lane], q = s_p[o * 64 + lane];
 #pragma unroll
                 for (int v = 0; v < V; ++v) h[v] = __builtin_fmaf(q[v], h[v], f[v]);
             }
@@ -345,27 +346,39 @@ template <bool ADJ, int V> __global__ __launch_bounds__(64 * SPAN_WAVES) void k_
 }
 
 // ---------------------------------------------------------------- host side
-// (states of a lane, waves) of the walk: the smallest that hold N
-template <int DT, int MODE> mimo_status launch_walk(const ScanParams& p, hipStream_t st) {
-    const dim3 grid((unsigned)p.slots, (unsigned)(p.G * p.tpg));
-    if (p.N <= 4) return launch(&k_walk<DT, 4, 1, MODE>, grid, 64, 0, st, p);
-    if (p.N <= 8) return launch(&k_walk<DT, 8, 1, MODE>, grid, 64, 0, st, p);
-    if (p.N <= 16) return launch(&k_walk<DT, 16, 1, MODE>, grid, 64, 0, st, p);
-    if (p.N <= 32) return launch(&k_walk<DT, 16, 2, MODE>, grid, 128, 0, st, p);
-    if (p.N <= 64) return launch(&k_walk<DT, 16, 4, MODE>, grid, 256, 0, st, p);
-    return launch(&k_walk<DT, 16, 8, MODE>, grid, 512, 0, st, p);
-}
-// At most `chunks` chunks in a sequence. Four states a thread where that still makes a block for each CU (7 x 2048 x 64
-// states: 13 us, 23 with one), else one ([1024, 16]: 6.3 us, 7.8 with four).
-template <bool ADJ> mimo_status launch_carry(const ScanParams& p, long chunks, hipStream_t st) {
-    const long waves = (chunks + SPAN - 1) / SPAN, states = (long)p.D * p.N;
-    const int block = 64 * (int)(waves < SPAN_WAVES ? waves : SPAN_WAVES), dirs = ADJ ? 2 : 1;
-    if (p.vec && (states + 255) / 256 * dirs * p.q.n >= 256)
-        return launch(&k_carry<ADJ, 4>, dim3((unsigned)((states + 255) / 256), dirs, p.q.n), block, 0, st, p);
-    return launch(&k_carry<ADJ, 1>, dim3((unsigned)((states + 63) / 64), dirs, p.q.n), block, 0, st, p);
-}
+// 64 channels by sixteen states: the unit in which the work of a walk is counted
 inline int waves_for(int64_t N) { return N <= 16 ? 1 : N <= 32 ? 2 : N <= 64 ? 4 : 8; }
 
+// States of a lane by waves of a block. Four states a lane leave the registers for five waves a SIMD and more: [8192,
+// 1024], N = 16 forward 78 us with 16 states a lane, 69 with four (8 x 2048 x 2048: 245 and 224; N = 32: 146 and 109).
+// What it costs, <c, h> joined in LDS over more waves, weighs more from N = 64 on: packed prompts [4100, 2048] 220 us with
+// 16 by 4, 275 with 8 by 8; and for N <= 8 one wave needs no joining (97 us for [8192, 2048], 103 with 4 by 2). So those
+// are split further only where the GPU is not full (N = 64, 300 tokens: 32 us with 16 by 4, 26 with 8 by 8), and in the
+// backward walk, which joins nothing (N = 64: 346 us with 16 by 4, 331 with 8 by 8).
+constexpr long FEW = 1024;
+template <int DT, int MODE> mimo_status launch_walk(const ScanParams& p, hipStream_t st) {
+    const dim3 grid((unsigned)p.slots, (unsigned)(p.G * p.tpg));
+    const bool narrow = MODE == AGG2 || p.slots * p.G * p.tpg * waves_for(p.N) <= FEW;
+    if (p.N <= 4) return launch(&k_walk<DT, 4, 1, MODE>, grid, 64, 0, st, p);
+    if (p.N <= 8) return narrow ? launch(&k_walk<DT, 4, 2, MODE>, grid, 128, 0, st, p) : launch(&k_walk<DT, 8, 1, MODE>, grid, 64, 0, st, p);
+    if (p.N <= 16) return launch(&k_walk<DT, 4, 4, MODE>, grid, 256, 0, st, p);
+    if (p.N <= 32) return launch(&k_walk<DT, 4, 8, MODE>, grid, 512, 0, st, p);
+    if (p.N <= 64) return narrow ? launch(&k_walk<DT, 8, 8, MODE>, grid, 512, 0, st, p) : launch(&k_walk<DT, 16, 4, MODE>, grid, 256, 0, st, p);
+    return narrow ? launch(&k_walk<DT, 8, 16, MODE>, grid, 1024, 0, st, p) : launch(&k_walk<DT, 16, 8, MODE>, grid, 512, 0, st, p);
+}
+// Four states a thread where that still makes a block for each CU (7 x 2048 x 64 states: 13 us, 23 with one), else one
+// ([1024, 16]: 6.3 us, 7.8 with four). Waves for the chunks of a sequence, of a packed one for twice the average: longer
+// ones take more rounds, but blocks for the longest that could be leave most waves idle.
+template <bool ADJ> mimo_status launch_carry(const ScanParams& p, hipStream_t st) {
+    long chunks = p.q.nc;
+    if (p.q.cu && 2 * p.slots / p.q.n < chunks) chunks = 2 * p.slots / p.q.n;
+    const long states = (long)p.D * p.N;
+    const int waves = (int)(chunks <= SPAN ? 1 : chunks < SPAN * SPAN_WAVES ? (chunks + SPAN - 1) / SPAN : SPAN_WAVES), dirs = ADJ ? 2 : 1;
+    const size_t lds = waves > 1 ? sizeof(float) * 2 * 64 * waves : 0;
+    if (p.vec && (states + 255) / 256 * dirs * p.q.n >= 256)
+        return launch(&k_carry<ADJ, 4>, dim3((unsigned)((states + 255) / 256), dirs, p.q.n), 64 * waves, 4 * lds, st, p);
+    return launch(&k_carry<ADJ, 1>, dim3((unsigned)((states + 63) / 64), dirs, p.q.n), 64 * waves, lds, st, p);
+}
 inline mimo_status check_scan(int64_t n, int64_t S, int64_t D, int64_t G, int64_t N, int dtype) {
     const mimo_status s = check_sequences(n, S, D, dtype);
     if (s != MIMO_OK) return s;

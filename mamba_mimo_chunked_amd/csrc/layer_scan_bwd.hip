@@ -15,8 +15,8 @@
 // them: 128, or 64 for Q = 2, whose staging takes the rest), then backward through them. The state in
 // front of a unit comes from the walk, which leaves it (from zero, at the chunk's start) with the sum of
 // dt to there: h = uh + exp(a udt) h(chunk). So an exponential is computed twice (walk, sub-tile) and no
-// state but every sixteenth goes to memory. 4 x 4096 tokens, D = 1024, N = 16, bf16: 347 us, of them the
-// walk 102, this kernel 245 (its vector units busy 75 % of the time: 97 vector instructions a token and
+// state but every sixteenth goes to memory. 4 x 4096 tokens, D = 1024, N = 16, bf16: 327 us, of them the
+// walk 80, this kernel 245 (its vector units busy 75 % of the time: 97 vector instructions a token and
 // 64 states), sums 12; walking the chunk a third time for its states, with 64-bit row addresses, took
 // 415 us. Vector instructions bind; two waves a SIMD fill 256 registers each (with 168 and three waves:
 // 436 us).
@@ -446,7 +446,7 @@ template <int DT> struct Run {
             if ((s = launch_walk<DT, AGG2>(w, st)) != MIMO_OK) return s;
         }
         if (p.chunked) {
-            if ((s = launch_carry<true>(p, p.q.nc, st)) != MIMO_OK) return s;
+            if ((s = launch_carry<true>(p, st)) != MIMO_OK) return s;
         }
         s = launch(&k_scan_bwd<DT, NS, Q>, dim3((unsigned)p.slots, p.G * p.tpg), 256, Shape<NS, Q>::lds, st, p);
         if (s != MIMO_OK) return s;
