@@ -8,7 +8,7 @@
 // Two channels a thread and many threads beat wider accesses, whose windows cost the registers that
 // keep waves, and so loads, in flight: [8192, 2048] bf16 forward 18.5 us with eight channels, 17.1 with
 // four, 16.1 with two; [4, 4100, 2048] bf16 backward 156, 60 and 57 us. With scalar rows and the blocks' order
-// below, 14.0 us (4.8 TB/s) and 52 us (3.9); 8 x 8192 x 2048 forward 104 us (5.2 TB/s, as a copy).
+// below, 14.0 us (4.8 TB/s) and 49 us (4.1); 8 x 8192 x 2048 forward 104 us (5.2 TB/s, as a copy).
 #include "layer.hpp"
 
 namespace mimo {
@@ -312,7 +312,8 @@ template <int DT, int VEC, int W> __global__ __launch_bounds__(256) void k_conv_
 // Tokens of a chunk, 16 at least: longer chunks read fewer rows twice, and the backward pass leaves fewer partial
 // sums; shorter ones keep more threads, and so loads, in flight. Forward 2048 threads a CU and up to 32 tokens
 // ([8192, 2048] bf16: 14.0 us, 15.1 with 1024 threads; 8 x 8192 x 2048: 104 us at 32 tokens, 115 at 128); backward
-// 1024 threads a CU, whose registers allow no more, and up to 128 tokens ([4, 4100, 2048] bf16: 52 us, 55 with 2048;
+// 1024 threads a CU, whose registers allow no more, and up to 128 tokens ([4, 4100, 2048] bf16: 52 us before chunks were
+// equal, 55 with 2048;
 // 8 x 8192 x 2048: 243 us at 64 tokens, 208 at 128, before the scalar rows).
 int chunk_tokens(int64_t n, int64_t S, bool packed, int64_t nvec, bool backward) {
     const int64_t T = packed ? S : n * S, c = T * nvec / (256 * (backward ? 1024 : 2048)) / 8 * 8, most = backward ? 128 : 32;
@@ -398,6 +399,13 @@ mimo_status plan_bwd(const mamba_conv_bwd_args* a, BwdPlan* pl) {
     pl->vec = vec_of(a->D, even);
     const bool packed = a->cu_seqlens != nullptr;
     pl->CH = chunk_tokens(a->n, a->S, packed, a->D / pl->vec, true);
+    if (packed) {   // a wave walks W - 1 tokens past its chunk: whole unrolled steps ([5003, 517] fp32, W = 3: 14.7 us, 16.7 with 16 tokens)
+        const int U = UNROLL_B * (3 - pl->vec), over = (int)a->W - 1;
+        pl->CH = (pl->CH + over + U / 2) / U * U - over;
+    } else if (a->S > pl->CH) {   // equal chunks (4100 tokens: 48.5 us with 32 chunks of 129 tokens, 52.5 with 33, the last of 4)
+        const int64_t count = (a->S + pl->CH / 2) / pl->CH;
+        pl->CH = (int)((a->S + count - 1) / count);
+    }
     const Seqs q = make_seqs(a->n, a->S, a->cu_seqlens, pl->CH);
     const long groups = (slots_of(q) + WS - 1) / WS;
     if (slots_of(q) > (long)1 << 30) return unsupported("too many tokens");
