@@ -268,7 +268,7 @@ def mamba_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, *,
     W, weight, bias = _check_filter(weight, bias, D, dev)
     initial_state = _param("initial_state", initial_state, (n, W - 1, D), x.dtype, dev)
     cu, x = _cu(cu_seqlens, dev), _dense_inner(x, 1)
-    res = _out(out, x, x=x, initial_state=initial_state)
+    res = _out(out, x, x=x, weight=weight, bias=bias, initial_state=initial_state)
     state = x.new_empty((n, W - 1, D)) if return_state else None
     _call("mamba_conv_fwd", (n, S, D, W, code, silu, int(out is None), _ptr(cu), *_rows(x, cu is not None), _ptr(weight),
                              _ptr(bias), _ptr(initial_state), _ptr(res), _ptr(state)), dev)
@@ -340,7 +340,7 @@ def mamba_conv_step(x, state, weight, bias=None, state_indices=None, *, activati
     slots, stride, idx = _check_pool(state, (W - 1, D), x.dtype, state_indices, n, dev)
     x = _dense_inner(x, 1)
     _apart("state", state, x=x, weight=weight, bias=bias, state_indices=idx)
-    res = _out(out, x, x=x, state=state)
+    res = _out(out, x, x=x, state=state, weight=weight, bias=bias)
     _call("mamba_conv_step", (n, D, slots, stride, x.stride(0), W, code, silu, 0, x.data_ptr(), state.data_ptr(), weight.data_ptr(),
                               _ptr(bias), _ptr(idx), res.data_ptr()), dev)
     return res
@@ -385,7 +385,7 @@ def mamba_scan_fwd(u, dt, a, b, c, d=None, z=None, dt_bias=None, initial_state=N
     n, S, lead = _sequences("u", u, cu_seqlens, 1)
     D, G, N, (u, dt, b, c, z), (a, d, dt_bias) = _check_scan(u, dt, a, b, c, d, z, dt_bias, lead, dev)
     cu, initial_state = _cu(cu_seqlens, dev), _param("initial_state", initial_state, (n, D, N), _F32, dev)
-    res = _out(out, u, u=u, dt=dt, b=b, c=c, z=z, initial_state=initial_state)
+    res = _out(out, u, u=u, dt=dt, a=a, b=b, c=c, d=d, z=z, dt_bias=dt_bias, initial_state=initial_state)
     state = a.new_empty((n, D, N)) if return_state else None
     packed = cu is not None
     _call("mamba_scan_fwd", (n, S, D, G, N, code, int(bool(dt_softplus)), int(out is None), 0, _ptr(cu), *_rows(u, packed), *_rows(dt, packed),
@@ -430,7 +430,7 @@ def mamba_scan_step(u, dt, state, a, b, c, d=None, z=None, dt_bias=None, state_i
     D, G, N, (u, dt, b, c, z), (a, d, dt_bias) = _check_scan(u, dt, a, b, c, d, z, dt_bias, (n,), dev)
     slots, stride, idx = _check_pool(state, (D, N), _F32, state_indices, n, dev)
     _apart("state", state, u=u, dt=dt, b=b, c=c, z=z, a=a, d=d, dt_bias=dt_bias, state_indices=idx)
-    res = _out(out, u, u=u, dt=dt, b=b, c=c, z=z, state=state)
+    res = _out(out, u, u=u, dt=dt, a=a, b=b, c=c, d=d, z=z, dt_bias=dt_bias, state=state)
     _call("mamba_scan_step", (n, D, G, N, slots, stride, code, int(bool(dt_softplus)), u.data_ptr(), u.stride(0), 0,
                               dt.data_ptr(), dt.stride(0), 0, b.data_ptr(), b.stride(0), 0, c.data_ptr(), c.stride(0), 0,
                               *(_NO_ROWS if z is None else (z.data_ptr(), z.stride(0), 0)),
@@ -478,7 +478,7 @@ def mamba_norm_fwd(x, weight, bias=None, z=None, *, groups: int = 1, eps: float 
     and out = p * silu(z) (z given, gate "after"), silu(p) (activation "silu", without z), or p. x, z, out
     [..., D]; weight, bias [D] float32."""
     dev, code, silu, D, rows, zr, weight, bias = _check_norm("mamba_norm_fwd", x, weight, bias, z, groups, eps, gate, activation)
-    res = _out(out, x, x=rows, z=zr)
+    res = _out(out, x, x=rows, z=zr, weight=weight, bias=bias)
     _call("mamba_norm_fwd", (rows.shape[0], D, groups, rows.stride(0), 0 if zr is None else zr.stride(0), code, int(bool(center)),
                              int(gate == "after"), silu, eps, 0, _ptr(rows), _ptr(zr), _ptr(weight), _ptr(bias), _ptr(res)), dev)
     return res

@@ -179,6 +179,11 @@ def test_outputs_may_not_overlap_inputs(on_cpu):
     with pytest.raises(ValueError, match="overlap u"):
         a = _scan(u=out)
         m.mamba_scan_fwd(**a, out=out)
+    bias = Z(48)
+    with pytest.raises(ValueError, match="overlap bias"):
+        m.mamba_conv_fwd(Z(1, 1, 48), Z(48, 4), bias, out=bias.view(1, 1, 48))
+    with pytest.raises(ValueError, match="overlap weight"):
+        m.mamba_norm_fwd(Z(1, 48), bias, out=bias.view(1, 48))
     pool = Z(3, 8, 4)
     with pytest.raises(ValueError, match="overlap"):
         m.mamba_scan_step(pool.view(-1)[:16].view(2, 8), Z(2, 8), pool, Z(8, 4), Z(2, 2, 4), Z(2, 2, 4))
