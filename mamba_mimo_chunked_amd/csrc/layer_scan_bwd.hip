@@ -16,7 +16,7 @@
 // front of a unit comes from the walk, which leaves it (from zero, at the chunk's start) with the sum of
 // dt to there: h = uh + exp(a udt) h(chunk). So an exponential is computed twice (walk, sub-tile) and no
 // state but every sixteenth goes to memory. 4 x 4096 tokens, D = 1024, N = 16, bf16: 327 us, of them the
-// walk 80, this kernel 245 (its vector units busy 75 % of the time: 97 vector instructions a token and
+// walk 86, this kernel 245 (its vector units busy 77 % of the time: 97 vector instructions a token and
 // 64 states), sums 12; walking the chunk a third time for its states, with 64-bit row addresses, took
 // 415 us. Vector instructions bind; two waves a SIMD fill 256 registers each (with 168 and three waves:
 // 436 us).
