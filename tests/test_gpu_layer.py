@@ -84,6 +84,9 @@ CONV = [  # dtype, taps, D, sequences, bias, initial state, silu, strided
     (BF, 6, 44, (1, 40), True, True, True, False), (HF, 7, 12, PACKED, False, True, True, False), (BF, 8, 36, (2, 29), True, True, True, False),
     (FF, 8, 7, ("packed", [3, 0, 0, 9], 0), True, True, True, False), (BF, 4, 2056, (1, 300), True, True, True, False),
     (FF, 4, 4, ("packed", [200] + [1] * 70, 40), True, True, True, False), (BF, 3, 10, ("packed", [0, 0], 5), True, True, True, False),
+    # around the backward pass's chunks: whole unrolled steps in packed sequences, equal chunks in dense ones
+    (FF, 3, 9, ("packed", [13, 14, 15, 28, 1], 1), True, True, True, False), (HF, 8, 6, ("packed", [16, 17, 18, 34], 0), True, True, True, False),
+    (BF, 4, 64, (1, 25), True, True, True, False), (FF, 5, 33, (2, 24), True, True, True, False), (BF, 2, 16, (3, 23), True, True, True, False),
 ]
 
 
@@ -176,6 +179,9 @@ SCAN = [  # dtype, D, G, N, sequences, options
     (FF, 36, 2, 33, PACKED, dict(gate=False, init=False)), (BF, 68, 1, 3, PACKED, dict(strided=True)), (FF, 5, 1, 6, ("packed", [0, 0, 3], 0), {}),
     (FF, 64, 1, 16, ("packed", [2] * 65, 3), {}), (BF, 16, 16, 8, (2, 35), {}), (FF, 260, 1, 9, (1, 66), {}),
     (BF, 20, 1, 16, ("packed", [0, 0], 70), {}), (FF, 64, 1, 16, (40, 20), {}), (HF, 512, 1, 16, (70, 3), {}),
+    # enough tiles that the states are split over few waves; a sequence much longer than the average of its batch
+    (FF, 1024, 1024, 7, (2, 20), {}), (BF, 300, 300, 40, ("packed", [100, 3, 0, 70], 4), {}), (HF, 150, 150, 100, (1, 40), {}),
+    (FF, 16, 1, 16, ("packed", [1] * 30 + [1500] + [0] * 5, 2), {}),
 ]
 
 
