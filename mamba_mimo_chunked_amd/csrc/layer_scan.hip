@@ -126,10 +126,10 @@ struct FwdPlan {
 };
 
 // Chunks are cut until about 6144 units of work (waves_for) walk, but, as a chunk costs its loads and its aggregate, not
-// below 64 tokens while 2048 walk, nor below 32 at all ([8192, 1024], N = 16: 69 us at 64 tokens, 71 at 48, 75 at 96;
-// [8192, 1024], N = 32: 109 us, 119 with half as many units; packed prompts [4100, 2048], N = 64: 220 us, 236 with half,
-// 217 with a third more, which has a third more memory for the states). Half the GPU's waves (512 units) without chunks
-// are as good as chunks, whose second walk (the aggregates) nearly doubles the work.
+// below 64 tokens while 2048 walk, nor below 32 at all ([8192, 1024], N = 16: 67 us at 64 tokens, 70 at 48, 74 at 96;
+// [8192, 1024], N = 32: 107 us, 116 with half as many units; packed prompts [4100, 2048], N = 64: 206 us, 216 with half,
+// 214 with a third more). Half the GPU's waves (512 units) without chunks are as good as chunks, whose second walk (the
+// aggregates) nearly doubles the work.
 mimo_status plan_fwd(const mamba_scan_fwd_args* a, FwdPlan* pl) {
     if (a == nullptr) return bad("args must not be NULL");
     const mimo_status s = check_scan(a->n, a->S, a->D, a->G, a->N, a->dtype);

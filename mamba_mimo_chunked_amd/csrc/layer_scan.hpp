@@ -14,7 +14,7 @@
 // Where channels alone do not fill the GPU the time axis is cut into chunks: k_walk<AGG> walks every
 // chunk but a sequence's last from zero (its last state, and the sum of dt, which gives the chunk's
 // decay exp(a sum dt)), k_carry chains the states that enter the chunks, and k_walk<FWD> walks the
-// chunks from them. Measured, [8192, 1024] bf16, N = 16: 69 us for the three; [8 x 2048, 2048]: 224 us.
+// chunks from them. Measured, [8192, 1024] bf16, N = 16: 67 us for the three; [8 x 2048, 2048]: 224 us.
 #pragma once
 #include "layer.hpp"
 
@@ -91,9 +91,10 @@ __device__ __forceinline__ float decay_base(float a) {
 // FWD: the outputs. AGG: a chunk's last state from zero. AGG2: also the adjoint that leaves it to the
 // left, sum_t exp(a sum_{s <= t} dt) c[t] dy[t], from the same exponentials.
 enum { FWD, AGG, AGG2 };
-// Waves a SIMD that the registers have to allow. Five for the narrow walks, whose few registers hold that many ([8192,
-// 1024], N = 16: 70.5 us without the bound, 69 with); six spill in the backward walk (N = 8: 91 us instead of 80).
-constexpr int walk_waves(int NS, int KS) { return KS == 1 ? 2 : NS == 4 ? 5 : KS == 16 ? 4 : 2; }
+// Waves a SIMD that the registers have to allow, five where the states are split, whose few registers hold that many
+// ([8192, 1024], N = 16: 70.5 us without the bound, 69 with; [16 x 1024, 4096], N = 64: 741 and 734); six spill in the
+// backward walk (N = 8: 91 us instead of 80). 16 waves a block are four a SIMD.
+constexpr int walk_waves(int KS) { return KS == 1 ? 2 : KS == 16 ? 4 : 5; }
 
 constexpr int UNIT = 16;   // tokens of a unit (backward)
 
@@ -102,7 +103,7 @@ constexpr int UNIT = 16;   // tokens of a unit (backward)
 // [8 x 2048, 2048]: 224 us with 16, 231 with 8, 260 with 32).
 constexpr int tile_tokens(int KS, int MODE) { return KS == 1 || (KS <= 4 && MODE == AGG2) ? 8 : 16; }
 
-template <int DT, int NS, int KS, int MODE> __global__ __launch_bounds__(64 * KS, walk_waves(NS, KS)) void k_walk(ScanParams p) {
+template <int DT, int NS, int KS, int MODE> __global__ __launch_bounds__(64 * KS, walk_waves(KS)) void k_walk(ScanParams p) {
     typedef raw_t<DT> raw;
     constexpr int TT = tile_tokens(KS, MODE), NP = NS * KS, TPW = TT / KS, NB = (TT * NP + 64 * KS - 1) / (64 * KS);
     constexpr bool C = MODE != AGG, OUT = MODE == FWD, ONE = KS == 1;
@@ -245,7 +246,9 @@ template <int DT, int NS, int KS, int MODE> __global__ __launch_bounds__(64 * KS
                 if (OUT && act && tt + t < t1) (out + (tt + t) * D)[off] = to_raw<DT>(__builtin_fmaf(skip, f_u[t], y) * f_z[t]);
             }
         } else {
-#pragma unroll 4
+            // the reads of a whole tile ahead of their use (packed prompts [4100, 2048], N = 64: 221 us with four tokens, 207 with 16;
+            // backward 327 with four, 329)
+#pragma unroll (MODE == AGG2 ? 4 : TT)
             for (int t = 0; t < TT; ++t) {
                 const float y = token(t, s_dt[t][lane], s_du[t][lane], MODE == AGG2 ? s_dy[t][lane] : 0.f);
                 if (OUT) s_y[w][t][lane] = y;
@@ -349,22 +352,24 @@ template <bool ADJ, int V> __global__ __launch_bounds__(64 * SPAN_WAVES) void k_
 // 64 channels by sixteen states: the unit in which the work of a walk is counted
 inline int waves_for(int64_t N) { return N <= 16 ? 1 : N <= 32 ? 2 : N <= 64 ? 4 : 8; }
 
-// States of a lane by waves of a block. Four states a lane leave the registers for five waves a SIMD and more: [8192,
+// States of a lane by waves of a block. Few states a lane leave the registers for five waves a SIMD and more: [8192,
 // 1024], N = 16 forward 78 us with 16 states a lane, 69 with four (8 x 2048 x 2048: 245 and 224; N = 32: 146 and 109).
-// What it costs, <c, h> joined in LDS over more waves, weighs more from N = 64 on: packed prompts [4100, 2048] 220 us with
-// 16 by 4, 275 with 8 by 8; and for N <= 8 one wave needs no joining (97 us for [8192, 2048], 103 with 4 by 2). So those
-// are split further only where the GPU is not full (N = 64, 300 tokens: 32 us with 16 by 4, 26 with 8 by 8), and in the
-// backward walk, which joins nothing (N = 64: 346 us with 16 by 4, 331 with 8 by 8).
+// What it costs, <c, h> joined in LDS over more waves, weighs more from N = 64 on, where eight are as fast as 16 or
+// faster ([16 x 1024, 4096] 783 us with 16 by 4, 741 with 8 by 8; [1024, 1024] 48 and 43; four, packed prompts: 270, 207 with
+// eight). For N <= 8 one wave needs no joining ([8192, 2048]: 85 us, 92 with 4 by 2), so those are split only where the GPU
+// is not full (D = 512: 37 us, 36 split) and in the backward walk, which joins nothing.
 constexpr long FEW = 1024;
 template <int DT, int MODE> mimo_status launch_walk(const ScanParams& p, hipStream_t st) {
     const dim3 grid((unsigned)p.slots, (unsigned)(p.G * p.tpg));
-    const bool narrow = MODE == AGG2 || p.slots * p.G * p.tpg * waves_for(p.N) <= FEW;
     if (p.N <= 4) return launch(&k_walk<DT, 4, 1, MODE>, grid, 64, 0, st, p);
-    if (p.N <= 8) return narrow ? launch(&k_walk<DT, 4, 2, MODE>, grid, 128, 0, st, p) : launch(&k_walk<DT, 8, 1, MODE>, grid, 64, 0, st, p);
+    if (p.N <= 8) {
+        if (MODE == AGG2 || p.slots * p.G * p.tpg <= FEW) return launch(&k_walk<DT, 4, 2, MODE>, grid, 128, 0, st, p);
+        return launch(&k_walk<DT, 8, 1, MODE>, grid, 64, 0, st, p);
+    }
     if (p.N <= 16) return launch(&k_walk<DT, 4, 4, MODE>, grid, 256, 0, st, p);
     if (p.N <= 32) return launch(&k_walk<DT, 4, 8, MODE>, grid, 512, 0, st, p);
-    if (p.N <= 64) return narrow ? launch(&k_walk<DT, 8, 8, MODE>, grid, 512, 0, st, p) : launch(&k_walk<DT, 16, 4, MODE>, grid, 256, 0, st, p);
-    return narrow ? launch(&k_walk<DT, 8, 16, MODE>, grid, 1024, 0, st, p) : launch(&k_walk<DT, 16, 8, MODE>, grid, 512, 0, st, p);
+    if (p.N <= 64) return launch(&k_walk<DT, 8, 8, MODE>, grid, 512, 0, st, p);
+    return launch(&k_walk<DT, 8, 16, MODE>, grid, 1024, 0, st, p);
 }
 // Four states a thread where that still makes a block for each CU (7 x 2048 x 64 states: 13 us, 23 with one), else one
 // ([1024, 16]: 6.3 us, 7.8 with four). Waves for the chunks of a sequence, of a packed one for twice the average: longer
