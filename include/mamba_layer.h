@@ -27,10 +27,18 @@
  * matter on entry; calls that may overlap need workspaces of their own. Its size
  * goes by the sizes, by which optional pointers are NULL and by the alignment of
  * the tensors, so the query takes the arguments of the call (without workspace).
- * For the backward scan it is mostly the states every sixteenth token, 4 D N / 16
- * bytes a token, and the partial sums of db and dc, 8 D N / 64 bytes a token (N up
- * to 16; 8 D N / 32 up to 64, 8 D N / 16 up to 128). Sums run in a fixed order:
- * equal inputs give equal bits.
+ * Sums run in a fixed order: equal inputs give equal bits.
+ *
+ * The backward scan's workspace, in bytes, with channel tiles of B = 128 channels
+ * for N <= 8, 64 up to 32, 32 up to 64 and 16 up to 128, t = ceil(D / G / B) of
+ * them in a group, and chunks of C = 16 to 128 tokens (fewer where there is less
+ * to do; a whole sequence of up to 128 tokens where two chunks would hold it):
+ *   partial sums of db and dc: 8 N G t a token;
+ *   sums of a chunk: 4 D (N + 2), and where chunks follow each other in a sequence
+ *     4 D (N + 1) more; n ceil(S / C) chunks, packed S / C + n + 1;
+ *   states at every sixteenth token but a chunk's first: 4 D (N + 1) each;
+ *     n (ceil(S / 16) - ceil(S / C)) of them, packed S (C / 16 - 1) / C + n.
+ * Each packed sequence thus costs about 3 states [D, N] beside its tokens.
  */
 #ifndef MAMBA_LAYER_H
 #define MAMBA_LAYER_H

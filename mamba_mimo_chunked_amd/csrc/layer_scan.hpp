@@ -35,13 +35,23 @@ struct ScanParams {
     void *du, *ddt, *db, *dc, *dz;
     float *da, *dd, *dbias, *dinit;
     float *pbc, *pdd;               // [tpg][tokens][G][2][N], [slots][2][D]
-    float *uh, *udt;                // units of a chunk: state from zero and sum of dt in front, [slots * units][D][N] and [..][D]
-    int units;                      // of a chunk: CH / UNIT
+    float *uh, *udt;                // units of a chunk behind its first: state from zero and sum of dt in front, [..][D][N], [..][D]
+    int units, seq_units;           // of those: a full chunk's, a dense sequence's
     long slots, tokens;
 };
 
 // first row of the flat token axis of a place
 __device__ __forceinline__ long flat_row(const Seqs& q, const Place& pl) { return q.cu ? (long)pl.row0 : (long)pl.i * q.S; }
+
+// Where a chunk's units behind its first lie (backward): in the order of the tokens, CH / UNIT - 1 = p.units a full chunk.
+// Packed, sequence i starts at floor(start(i) * units / CH) + i: as many units as its length needs lie in front of where the
+// next one starts, and the room goes by the tokens, not by the chunks that the sequences start.
+__device__ __forceinline__ long first_unit(const ScanParams& p, const Place& pl) {
+    const long in = (long)pl.j * p.units;
+    if (p.q.cu == nullptr) return (long)pl.i * p.seq_units + in;
+    const int whole = pl.row0 / p.q.CH;
+    return whole * p.units + (pl.row0 - whole * p.q.CH) * p.units / p.q.CH + pl.i + in;
+}
 
 // a channel tile: CPB channels of one group
 struct Tile {
@@ -189,6 +199,7 @@ template <int DT, int NS, int KS, int MODE> __global__ __launch_bounds__(64 * KS
         }
         return y[0] + y[1];
     };
+    const long unit0 = MODE == AGG2 ? first_unit(p, pl) - 1 : 0;
     if (t0 < t1) fetch(t0);
     for (int tt = t0; tt < t1; tt += TT) {
         float f_v[TPW], f_u[TPW], f_z[TPW], f_g[TPW];   // step, input, gate, dy of this wave's tokens
@@ -234,7 +245,7 @@ template <int DT, int NS, int KS, int MODE> __global__ __launch_bounds__(64 * KS
         if constexpr (MODE == AGG2) {   // the backward pass starts again from every unit
             const int k = (tt - t0) / UNIT;
             if (k > 0 && (tt - t0) % UNIT == 0 && act) {
-                const long at = (long)blockIdx.x * p.units + k;
+                const long at = unit0 + k;
                 store_states(p.uh + (at * D + d) * p.N, w * NS, p.N, p.vec, h);
                 if (w == 0) p.udt[at * D + d] = total;
             }
@@ -268,7 +279,7 @@ template <int DT, int NS, int KS, int MODE> __global__ __launch_bounds__(64 * KS
             }
         }
     }
-    if (!act) return;
+    if (!act || (MODE == AGG2 && !p.chunked)) return;
     float* to = !OUT ? p.agg + blockIdx.x * D * p.N : p.state && t1 == pl.len ? p.state + pl.i * D * p.N : nullptr;
     if (to) store_states(to + d * (long)p.N, w * NS, p.N, p.vec, h);
     if constexpr (MODE == AGG2) store_states(p.gagg + (blockIdx.x * D + d) * p.N, w * NS, p.N, p.vec, gr);

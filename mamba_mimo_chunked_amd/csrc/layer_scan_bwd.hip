@@ -191,8 +191,9 @@ template <int DT, int NS, int Q> __global__ __launch_bounds__(256, 2) void k_sca
             }
     };
     float uh[NS], ut = 0.f;
+    const long unit0 = first_unit(p, pl) - 1;
     auto fetch_unit = [&](int k) {
-        const long at = (long)blockIdx.x * p.units + k;
+        const long at = unit0 + k;
         load_states(p.uh + at * D * N + dn, q * NS, p.N, p.vec, 0.f, uh);
         ut = p.udt[at * D + d];
     };
@@ -384,6 +385,7 @@ struct BwdPlan {
     long slots, tokens;
     bool chunked;
     bool walked;                    // chunks of more than a unit, or more than one chunk
+    int units, seq_units;           // as in ScanParams
     size_t off_gagg, off_sdt, off_pdd, off_uh, off_udt, off_pbc, bytes;
 };
 
@@ -423,12 +425,14 @@ mimo_status plan_bwd(const mamba_scan_bwd_args* a, BwdPlan* pl) {
     pl->walked = a->S > UNIT;
     const long per = pl->tokens * a->G * 2 * a->N;
     if (pl->slots > 0x7fffffffL || per / 256 > 0x70000000L || a->G * pl->tpg > 65535) return unsupported("too many tokens or channels");
+    pl->units = CH / UNIT - 1;
+    pl->seq_units = (int)((a->S + UNIT - 1) / UNIT) - pl->q.nc;
     const size_t agg = up256((size_t)pl->slots * a->N * a->D * sizeof(float));
     pl->off_gagg = agg;
-    pl->off_sdt = pl->off_gagg + (pl->walked ? agg : 0);
-    pl->off_pdd = pl->off_sdt + up256((size_t)pl->slots * a->D * sizeof(float));
+    pl->off_sdt = pl->off_gagg + (pl->chunked ? agg : 0);
+    pl->off_pdd = pl->off_sdt + (pl->chunked ? up256((size_t)pl->slots * a->D * sizeof(float)) : 0);
     pl->off_uh = pl->off_pdd + up256((size_t)pl->slots * 2 * a->D * sizeof(float));
-    const size_t units = a->S > UNIT ? (size_t)pl->slots * (CH / UNIT) * a->D : 0;
+    const size_t units = !pl->walked || pl->units == 0 ? 0 : (size_t)(packed ? a->S * pl->units / CH + a->n : a->n * pl->seq_units) * a->D;
     pl->off_udt = pl->off_uh + up256(units * a->N * sizeof(float));
     pl->off_pbc = pl->off_udt + up256(units * sizeof(float));
     pl->bytes = pl->off_pbc + up256((size_t)pl->tpg * per * sizeof(float));
@@ -501,7 +505,7 @@ mimo_status mamba_scan_bwd(const mamba_scan_bwd_args* a, void* stream) {
     p.pbc = reinterpret_cast<float*>(ws + pl.off_pbc);
     p.uh = pl.walked ? reinterpret_cast<float*>(ws + pl.off_uh) : nullptr;
     p.udt = reinterpret_cast<float*>(ws + pl.off_udt);
-    p.units = pl.q.CH / UNIT;
+    p.units = pl.units, p.seq_units = pl.seq_units;
     p.slots = pl.slots, p.tokens = pl.tokens;
     p.vec = p.N % 4 == 0;
     for (const void* x : {(const void*)p.a, (const void*)p.init, (const void*)p.dstate, (const void*)p.dinit}) p.vec = p.vec && aligned(x, 0, 0, 16, 1);
