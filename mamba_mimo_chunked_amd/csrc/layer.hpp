@@ -215,8 +215,10 @@ template <class F> __device__ __forceinline__ void column_sums(const float* part
 inline mimo_status bad(const char* msg) { return set_error(MIMO_ERR_VALUE, msg); }
 inline mimo_status unsupported(const char* msg) { return set_error(MIMO_ERR_UNSUPPORTED, msg); }
 
+// the most threads along a grid's first axis. A call of several kernels checks them all before it queues the first.
+inline bool grid_fits(long blocks, int block) { return (unsigned long)blocks * block <= 0xffffffffUL; }
 template <class P> inline mimo_status launch(void (*f)(P), dim3 grid, int block, size_t lds, hipStream_t st, P p) {
-    if ((unsigned long)grid.x * block > 0xffffffffUL) return unsupported("the call needs more than 2^32 threads");
+    if (!grid_fits(grid.x, block)) return unsupported("the call needs more than 2^32 threads");
     if (lds > 64 * 1024 && hipFuncSetAttribute(reinterpret_cast<const void*>(f), hipFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)lds) != hipSuccess)
         return set_error(MIMO_ERR_HIP, "hipFuncSetAttribute(MaxDynamicSharedMemorySize) failed");

@@ -370,6 +370,7 @@ inline int waves_for(int64_t N) { return N <= 16 ? 1 : N <= 32 ? 2 : N <= 64 ? 4
 // eight). For N <= 8 one wave needs no joining ([8192, 2048]: 85 us, 92 with 4 by 2), so those are split only where the GPU
 // is not full (D = 512: 37 us, 36 split) and in the backward walk, which joins nothing.
 constexpr long FEW = 1024;
+inline int walk_threads(int64_t N) { return N <= 4 ? 64 : N <= 8 ? 128 : N <= 16 ? 256 : N <= 64 ? 512 : 1024; }   // at most
 template <int DT, int MODE> mimo_status launch_walk(const ScanParams& p, hipStream_t st) {
     const dim3 grid((unsigned)p.slots, (unsigned)(p.G * p.tpg));
     if (p.N <= 4) return launch(&k_walk<DT, 4, 1, MODE>, grid, 64, 0, st, p);

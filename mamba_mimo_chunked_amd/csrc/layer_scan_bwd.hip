@@ -350,8 +350,9 @@ template <int DT, int NS, int Q> __global__ __launch_bounds__(256, 2) void k_sca
 
 __host__ __device__ inline int blocks_of(long n, int per) { return (int)((n + per - 1) / per); }
 
-// blocks [0, na): da over the slots; [na, na + nd): dd and d(dt_bias); the rest: db and dc over the
-// channel tiles of a group
+// blocks [0, na): da over the slots; [na, na + nd): dd and d(dt_bias); the rest, up to SUM_BLOCKS: db and dc over the
+// channel tiles of a group, an element a thread and, where there are more, others behind
+constexpr long SUM_BLOCKS = 1 << 22;
 template <int DT> __global__ __launch_bounds__(256) void k_sums(ScanParams p) {
     const long D = p.D, N = p.N;
     const int na = blocks_of(N * D, SUM_COLS), nd = blocks_of(2 * D, SUM_COLS);
@@ -370,12 +371,13 @@ template <int DT> __global__ __launch_bounds__(256) void k_sums(ScanParams p) {
         return;
     }
     blk -= nd;
-    const long per = p.tokens * p.G * 2 * N, e = (long)blk * 256 + threadIdx.x;
-    if (e >= per) return;
-    float s = 0.f;
-    for (int k = 0; k < p.tpg; ++k) s += p.pbc[k * per + e];
-    const long n = e % N, m = e / N % 2, row = e / (2 * N);   // row: token and group
-    static_cast<raw_t<DT>*>(m ? p.dc : p.db)[row * N + n] = to_raw<DT>(s);
+    const long per = p.tokens * p.G * 2 * N;
+    for (long e = (long)blk * 256 + threadIdx.x; e < per; e += SUM_BLOCKS * 256) {
+        float s = 0.f;
+        for (int k = 0; k < p.tpg; ++k) s += p.pbc[k * per + e];
+        const long n = e % N, m = e / N % 2, row = e / (2 * N);   // row: token and group
+        static_cast<raw_t<DT>*>(m ? p.dc : p.db)[row * N + n] = to_raw<DT>(s);
+    }
 }
 
 // ---------------------------------------------------------------- host side
@@ -424,7 +426,8 @@ mimo_status plan_bwd(const mamba_scan_bwd_args* a, BwdPlan* pl) {
     pl->chunked = a->S > CH;
     pl->walked = a->S > UNIT;
     const long per = pl->tokens * a->G * 2 * a->N;
-    if (pl->slots > 0x7fffffffL || per / 256 > 0x70000000L || a->G * pl->tpg > 65535) return unsupported("too many tokens or channels");
+    const int threads = walk_threads(a->N) > 256 ? walk_threads(a->N) : 256;   // the sums' blocks are at most 2^24
+    if (pl->slots > 0x7fffffffL || !grid_fits(pl->slots, threads) || a->G * pl->tpg > 65535) return unsupported("too many tokens or channels");
     pl->units = CH / UNIT - 1;
     pl->seq_units = (int)((a->S + UNIT - 1) / UNIT) - pl->q.nc;
     const size_t agg = up256((size_t)pl->slots * a->N * a->D * sizeof(float));
@@ -455,7 +458,8 @@ template <int DT> struct Run {
         s = launch(&k_scan_bwd<DT, NS, Q>, dim3((unsigned)p.slots, p.G * p.tpg), 256, Shape<NS, Q>::lds, st, p);
         if (s != MIMO_OK) return s;
         const long per = p.tokens * p.G * 2 * p.N;
-        const long blocks = (long)blocks_of((long)p.N * p.D, SUM_COLS) + blocks_of(2L * p.D, SUM_COLS) + (per + 255) / 256;
+        const long rest = (per + 255) / 256 < SUM_BLOCKS ? (per + 255) / 256 : SUM_BLOCKS;
+        const long blocks = (long)blocks_of((long)p.N * p.D, SUM_COLS) + blocks_of(2L * p.D, SUM_COLS) + rest;
         return launch(&k_sums<DT>, dim3((unsigned)blocks), 256, 0, st, p);
     }
 };

@@ -67,3 +67,22 @@ def test_within_the_bound(dtype, D, G, N, seqs):
 def test_steps_of_both_signs(dtype, D, G, N, seqs):
     """Without softplus, steps between -0.15 and 0.5: states shrink and grow, and stay in fp32's range."""
     assert compare(dtype, D, G, N, seqs, sp=False, bias=0.03) < 2e-2
+
+
+def test_more_than_2_32_partial_sums():
+    """256 times the same sequence, whose gradients of b and c have 2^32 elements: every one as the first's, and that
+    within the bound. The inputs of all sequences lie in one place (a batch stride of zero)."""
+    n, S, D, N = 256, 1024, 64, 128
+    g = _gen(77)
+    x = _scan_inputs(g, (1, S), 1, D, D, N, BF)
+    dout, ds = _rows(g, (1, S), D, BF, False), torch.randn(1, D, N, generator=g).cuda()
+    wide = {k: v if k in ("a", "d", "dt_bias") else v.expand(n, *v.shape[1:]) for k, v in x.items()}
+    gr = m.mamba_scan_bwd(dout.expand(n, S, D), **wide, dstate=ds.expand(n, D, N), dt_softplus=True)
+    for k in ("db", "dc", "du", "ddt", "dz", "dinitial_state"):
+        t = getattr(gr, k)
+        for i in range(1, n):
+            assert torch.equal(t[i], t[0]), (k, i)
+    x["initial"] = x.pop("initial_state")
+    ref, bound = Bd.scan(**x, cu=None, sp=True, dout=dout, dstate=ds, chunk=128)
+    got = {k: getattr(gr, k)[:1] for k in ("db", "dc", "du", "ddt", "dz", "dinitial_state")}
+    log(f"[scan bound] 2^32 sums: worst {Bd.check(got, ref, bound, tuple(got))[0]:.3f}")
