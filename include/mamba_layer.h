@@ -120,6 +120,11 @@ mimo_status mamba_conv_step(const mamba_conv_step_args *args, void *stream);
  *   h[t]  = exp(dt'[t] a[d,n]) h[t-1] + dt'[t] u[t] b[t,g,n]
  *   y[t]  = sum_n c[t,g,n] h[t] + d[d] u[t];   out = y * silu(z), or y without z
  * from h = initial_state (zeros where NULL); state (optional) receives the last h.
+ * Infinities come out as the formulas give them, with two exceptions: where the time
+ * axis is cut, a state that is infinite at a cut may be NaN behind it if the decay
+ * over a whole chunk is below fp32's range; and da may be NaN where a state is
+ * infinite. Steps that let the state grow (dt' a > 0) must keep the product of the
+ * factors exp(dt' a) of 128 tokens in fp32's range.
  *   u, dt, z, out [.., D]; a [D, N]; b, c [.., G, N]; d, dt_bias [D] or NULL;
  *   states [n, D, N] fp32. N <= MAMBA_SCAN_MAX_STATE, D a multiple of G.
  */

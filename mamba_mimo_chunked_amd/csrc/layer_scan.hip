@@ -87,7 +87,8 @@ template <int DT, int LPC, bool VEC> __global__ __launch_bounds__(256) void k_st
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 h[j][k] = __builtin_fmaf(exp2_hw(dt * decay_base(a[j][k])), h[j][k], du * to_f<DT>(r_b[j][k]));
-                y = __builtin_fmaf(h[j][k], to_f<DT>(r_c[j][k]), y);
+                // places behind the last state take no part: an infinite input times their zero b is NaN
+                if (n0 + (VEC ? 0 : k) < p.N) y = __builtin_fmaf(h[j][k], to_f<DT>(r_c[j][k]), y);
             }
             y = sum_lanes<LPC < 16 ? LPC : 16>(y);
             if (LPC == 32) y += __shfl_xor(y, 16);

@@ -16,6 +16,8 @@
 // decay exp(a sum dt)), k_carry chains the states that enter the chunks, and k_walk<FWD> walks the
 // chunks from them. Measured, [8192, 1024] bf16, N = 16: 67 us for the three; [8 x 2048, 2048]: 224 us.
 #pragma once
+#include <type_traits>
+
 #include "layer.hpp"
 
 namespace mimo {
@@ -104,7 +106,8 @@ enum { FWD, AGG, AGG2 };
 // Waves a SIMD that the registers have to allow, five where the states are split, whose few registers hold that many
 // ([8192, 1024], N = 16: 70.5 us without the bound, 69 with; [16 x 1024, 4096], N = 64: 741 and 734); six spill in the
 // backward walk (N = 8: 91 us instead of 80). 16 waves a block are four a SIMD.
-constexpr int walk_waves(int KS) { return KS == 1 ? 2 : KS == 16 ? 4 : 5; }
+// Six for four states by eight waves, of which LDS lets three blocks in (N = 24: 113 us with the 82 registers that five allow).
+constexpr int walk_waves(int NS, int KS, int MODE) { return KS == 1 ? 2 : KS == 16 ? 4 : NS == 4 && KS == 8 && MODE == FWD ? 6 : 5; }
 
 constexpr int UNIT = 16;   // tokens of a unit (backward)
 
@@ -113,7 +116,19 @@ constexpr int UNIT = 16;   // tokens of a unit (backward)
 // [8 x 2048, 2048]: 224 us with 16, 231 with 8, 260 with 32).
 constexpr int tile_tokens(int KS, int MODE) { return KS == 1 || (KS <= 4 && MODE == AGG2) ? 8 : 16; }
 
-template <int DT, int NS, int KS, int MODE> __global__ __launch_bounds__(64 * KS, walk_waves(KS)) void k_walk(ScanParams p) {
+// f(n) with n = `states` as a constant: 0 (or less) to NS (or more)
+template <int NS, class F> __device__ __forceinline__ void with_states(int states, F f) {
+    if constexpr (NS > 0) {
+        if (states >= NS) f(std::integral_constant<int, NS>{});
+        else with_states<NS - 1>(states, f);
+    } else f(std::integral_constant<int, 0>{});
+}
+
+// PAD: the waves hold more than N states. A place behind the last one reads zeros for b and c, but an infinite input times
+// zero is NaN, and so would <c, h> be: the outputs' walk leaves those places out, by a loop for each number of states
+// that a wave may hold ([8192, 1024] bf16, N = 7: 54 us, 63 with a condition in each step; [8192, 512], N = 100: 207 and 248;
+// with the places in the sum 55 and 223).
+template <int DT, int NS, int KS, int MODE, bool PAD> __global__ __launch_bounds__(64 * KS, walk_waves(NS, KS, MODE)) void k_walk(ScanParams p) {
     typedef raw_t<DT> raw;
     constexpr int TT = tile_tokens(KS, MODE), NP = NS * KS, TPW = TT / KS, NB = (TT * NP + 64 * KS - 1) / (64 * KS);
     constexpr bool C = MODE != AGG, OUT = MODE == FWD, ONE = KS == 1;
@@ -182,13 +197,13 @@ template <int DT, int NS, int KS, int MODE> __global__ __launch_bounds__(64 * KS
         pb += (long)TT * p.b.ts;
         if (C) pc += (long)TT * p.c.ts;
     };
-    // one token of step v: the states, and <c, h> (or, with dy = g, the adjoint). A step of zero changes nothing: so
-    // pass the tokens of a tile behind the chunk.
-    auto token = [&](int t, float v, float vu, float g) {
+    // one token of step v: the wave's first `real` states, and <c, h> (or, with dy = g, the adjoint). A step of zero changes
+    // nothing: so pass the tokens of a tile behind the chunk.
+    auto token = [&](auto real, int t, float v, float vu, float g) {
         float y[2] = {0.f, 0.f};
         if (MODE != FWD) total += v;
 #pragma unroll
-        for (int k = 0; k < NS; ++k) {
+        for (int k = 0; k < real; ++k) {
             const float e = exp2_hw(v * a[k]);
             h[k] = __builtin_fmaf(e, h[k], vu * s_b[t][w * NS + k]);
             if (OUT) y[k & 1] = __builtin_fmaf(h[k], s_c[t][w * NS + k], y[k & 1]);
@@ -250,21 +265,25 @@ template <int DT, int NS, int KS, int MODE> __global__ __launch_bounds__(64 * KS
                 if (w == 0) p.udt[at * D + d] = total;
             }
         }
-        if (ONE) {
+        auto tokens = [&](auto real) {
+            if constexpr (ONE) {
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                const float y = token(t, f_v[t], f_v[t] * f_u[t], f_g[t]);
-                if (OUT && act && tt + t < t1) (out + (tt + t) * D)[off] = to_raw<DT>(__builtin_fmaf(skip, f_u[t], y) * f_z[t]);
-            }
-        } else {
-            // the reads of a whole tile ahead of their use (packed prompts [4100, 2048], N = 64: 221 us with four tokens, 207 with 16;
-            // backward 327 with four, 329)
+                for (int t = 0; t < TT; ++t) {
+                    const float y = token(real, t, f_v[t], f_v[t] * f_u[t], f_g[t]);
+                    if (OUT && act && tt + t < t1) (out + (tt + t) * D)[off] = to_raw<DT>(__builtin_fmaf(skip, f_u[t], y) * f_z[t]);
+                }
+            } else {
+                // the reads of a whole tile ahead of their use (packed prompts [4100, 2048], N = 64: 221 us with four tokens,
+                // 207 with 16; backward 327 with four, 329)
 #pragma unroll (MODE == AGG2 ? 4 : TT)
-            for (int t = 0; t < TT; ++t) {
-                const float y = token(t, s_dt[t][lane], s_du[t][lane], MODE == AGG2 ? s_dy[t][lane] : 0.f);
-                if (OUT) s_y[w][t][lane] = y;
+                for (int t = 0; t < TT; ++t) {
+                    const float y = token(real, t, s_dt[t][lane], s_du[t][lane], MODE == AGG2 ? s_dy[t][lane] : 0.f);
+                    if (OUT) s_y[w][t][lane] = y;
+                }
             }
-        }
+        };
+        if constexpr (PAD) with_states<NS>(p.N - w * NS, tokens);
+        else tokens(std::integral_constant<int, NS>{});
         __syncthreads();
         if (OUT && !ONE && act) {
 #pragma unroll
@@ -371,17 +390,21 @@ inline int waves_for(int64_t N) { return N <= 16 ? 1 : N <= 32 ? 2 : N <= 64 ? 4
 // is not full (D = 512: 37 us, 36 split) and in the backward walk, which joins nothing.
 constexpr long FEW = 1024;
 inline int walk_threads(int64_t N) { return N <= 4 ? 64 : N <= 8 ? 128 : N <= 16 ? 256 : N <= 64 ? 512 : 1024; }   // at most
-template <int DT, int MODE> mimo_status launch_walk(const ScanParams& p, hipStream_t st) {
+inline int walk_places(int64_t N) { return N <= 4 ? 4 : N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : N <= 64 ? 64 : 128; }
+template <int DT, int MODE, bool PAD> mimo_status launch_shape(const ScanParams& p, hipStream_t st) {
     const dim3 grid((unsigned)p.slots, (unsigned)(p.G * p.tpg));
-    if (p.N <= 4) return launch(&k_walk<DT, 4, 1, MODE>, grid, 64, 0, st, p);
+    if (p.N <= 4) return launch(&k_walk<DT, 4, 1, MODE, PAD>, grid, 64, 0, st, p);
     if (p.N <= 8) {
-        if (MODE == AGG2 || p.slots * p.G * p.tpg <= FEW) return launch(&k_walk<DT, 4, 2, MODE>, grid, 128, 0, st, p);
-        return launch(&k_walk<DT, 8, 1, MODE>, grid, 64, 0, st, p);
+        if (MODE == AGG2 || p.slots * p.G * p.tpg <= FEW) return launch(&k_walk<DT, 4, 2, MODE, PAD>, grid, 128, 0, st, p);
+        return launch(&k_walk<DT, 8, 1, MODE, PAD>, grid, 64, 0, st, p);
     }
-    if (p.N <= 16) return launch(&k_walk<DT, 4, 4, MODE>, grid, 256, 0, st, p);
-    if (p.N <= 32) return launch(&k_walk<DT, 4, 8, MODE>, grid, 512, 0, st, p);
-    if (p.N <= 64) return launch(&k_walk<DT, 8, 8, MODE>, grid, 512, 0, st, p);
-    return launch(&k_walk<DT, 8, 16, MODE>, grid, 1024, 0, st, p);
+    if (p.N <= 16) return launch(&k_walk<DT, 4, 4, MODE, PAD>, grid, 256, 0, st, p);
+    if (p.N <= 32) return launch(&k_walk<DT, 4, 8, MODE, PAD>, grid, 512, 0, st, p);
+    if (p.N <= 64) return launch(&k_walk<DT, 8, 8, MODE, PAD>, grid, 512, 0, st, p);
+    return launch(&k_walk<DT, 8, 16, MODE, PAD>, grid, 1024, 0, st, p);
+}
+template <int DT, int MODE> mimo_status launch_walk(const ScanParams& p, hipStream_t st) {
+    return p.N < walk_places(p.N) && MODE == FWD ? launch_shape<DT, MODE, MODE == FWD>(p, st) : launch_shape<DT, MODE, false>(p, st);
 }
 // Four states a thread where that still makes a block for each CU (7 x 2048 x 64 states: 13 us, 23 with one), else one
 // ([1024, 16]: 6.3 us, 7.8 with four). Waves for the chunks of a sequence, of a packed one for twice the average: longer

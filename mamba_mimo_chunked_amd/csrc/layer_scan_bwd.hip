@@ -51,7 +51,12 @@ template <int NS, int Q> __device__ __forceinline__ void fold_channels(float (&v
     if constexpr (CPW >= 32) v[0] = add_dpp<DPP_XOR2>(v[0]);
 }
 
-template <int DT, int NS, int Q> __global__ __launch_bounds__(256, 2) void k_scan_bwd(ScanParams p) {
+//
+// The places of a channel's states behind the last one read zeros for b and c, but an infinite input times zero is NaN, and
+// so would the sums over the states be. PAD = 1, whole lanes of them: left out of the three sums; 2, some of a lane: its h
+// and g are set to zero there in each step, and a is so small that no finite step makes more than 2^34 of its decay, an
+// infinite one zero ([2 x 2048, 1024] bf16, N = 24: 192 us, 190 without; N = 13: 110 and 108; [2 x 2048, 512], N = 100: 398 and 384).
+template <int DT, int NS, int Q, int PAD> __global__ __launch_bounds__(256, 2) void k_scan_bwd(ScanParams p) {
     typedef raw_t<DT> raw;
     typedef Shape<NS, Q> H;
     constexpr int ST = H::ST, NP = H::NP, CPB = H::CPB, SUBS = H::SUBS, NT = (ST * CPB + 255) / 256, NB = (H::BC + 255) / 256;
@@ -122,6 +127,13 @@ template <int DT, int NS, int Q> __global__ __launch_bounds__(256, 2) void k_sca
         hc[k] = h0 && act ? hc[k] : 0.f;
         g[k] = g0 && act ? g[k] : 0.f;
     }
+    bool on[NS];
+#pragma unroll
+    for (int k = 0; k < NS; ++k) {
+        on[k] = PAD != 2 || q * NS + k < p.N;
+        if (!on[k]) a[k] = -1e-37f;
+    }
+    const bool lane_on = PAD != 1 || q * NS < p.N;
     const int nunit = (t1 - t0 + UNIT - 1) / UNIT;
 
     raw r_dt[NT], r_u[NT], r_z[NT], r_g[NT], r_b[NB], r_c[NB];
@@ -226,7 +238,10 @@ template <int DT, int NS, int Q> __global__ __launch_bounds__(256, 2) void k_sca
                 for (int t = 0; t < ST; ++t) {
                     const float v = s_dt[t * CPB + cb], vu = s_du[t * CPB + cb];
 #pragma unroll
-                    for (int k = 0; k < NS; ++k) h[k] = __builtin_fmaf(exp2_hw(v * a[k]), h[k], vu * s_b[t * NP + q * NS + k]);
+                    for (int k = 0; k < NS; ++k) {
+                        h[k] = __builtin_fmaf(exp2_hw(v * a[k]), h[k], vu * s_b[t * NP + q * NS + k]);
+                        if (PAD == 2) h[k] = on[k] ? h[k] : 0.f;
+                    }
                 }
 #pragma unroll
                 for (int k = 0; k < NS; k += 4)
@@ -261,6 +276,7 @@ template <int DT, int NS, int Q> __global__ __launch_bounds__(256, 2) void k_sca
                     hp[t][k] = h[k];
                     e[t][k] = exp2_hw(v * a[k]);
                     h[k] = __builtin_fmaf(e[t][k], h[k], vu * s_b[t * NP + q * NS + k]);
+                    if (PAD == 2) h[k] = on[k] ? h[k] : 0.f;
                 }
             }
 #pragma unroll
@@ -272,6 +288,7 @@ template <int DT, int NS, int Q> __global__ __launch_bounds__(256, 2) void k_sca
                     const float b = s_b[t * NP + q * NS + k], c = s_c[t * NP + q * NS + k];
                     const float ht = t == ST - 1 ? h[k] : hp[t + 1 < ST ? t + 1 : 0][k];
                     g[k] = __builtin_fmaf(c, dy, g[k]);
+                    if (PAD == 2) g[k] = on[k] ? g[k] : 0.f;
                     y = __builtin_fmaf(c, ht, y);
                     sgb = __builtin_fmaf(g[k], b, sgb);
                     vc[k] = dy * ht;
@@ -280,6 +297,11 @@ template <int DT, int NS, int Q> __global__ __launch_bounds__(256, 2) void k_sca
                     const float x = g[k] * hp[t][k];
                     sxa = __builtin_fmaf(x, a[k], sxa);
                     da[k] = __builtin_fmaf(x, v, da[k]);
+                }
+                if (PAD == 1) {
+                    y = lane_on ? y : 0.f;
+                    sgb = lane_on ? sgb : 0.f;
+                    sxa = lane_on ? sxa : 0.f;
                 }
                 y = sum_lanes<Q>(y);
                 sgb = sum_lanes<Q>(sgb);
@@ -455,7 +477,8 @@ template <int DT> struct Run {
         if (p.chunked) {
             if ((s = launch_carry<true>(p, st)) != MIMO_OK) return s;
         }
-        s = launch(&k_scan_bwd<DT, NS, Q>, dim3((unsigned)p.slots, p.G * p.tpg), 256, Shape<NS, Q>::lds, st, p);
+        const auto grad = p.N == NS * Q ? &k_scan_bwd<DT, NS, Q, 0> : p.N % NS == 0 ? &k_scan_bwd<DT, NS, Q, 1> : &k_scan_bwd<DT, NS, Q, 2>;
+        s = launch(grad, dim3((unsigned)p.slots, p.G * p.tpg), 256, Shape<NS, Q>::lds, st, p);
         if (s != MIMO_OK) return s;
         const long per = p.tokens * p.G * 2 * p.N;
         const long rest = (per + 255) / 256 < SUM_BLOCKS ? (per + 255) / 256 : SUM_BLOCKS;
