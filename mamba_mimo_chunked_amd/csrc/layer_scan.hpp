@@ -395,8 +395,10 @@ template <int DT, int MODE, bool PAD> mimo_status launch_shape(const ScanParams&
     const dim3 grid((unsigned)p.slots, (unsigned)(p.G * p.tpg));
     if (p.N <= 4) return launch(&k_walk<DT, 4, 1, MODE, PAD>, grid, 64, 0, st, p);
     if (p.N <= 8) {
-        if (MODE == AGG2 || p.slots * p.G * p.tpg <= FEW) return launch(&k_walk<DT, 4, 2, MODE, PAD>, grid, 128, 0, st, p);
-        return launch(&k_walk<DT, 8, 1, MODE, PAD>, grid, 64, 0, st, p);
+        if constexpr (MODE != AGG2) {
+            if (p.slots * p.G * p.tpg > FEW) return launch(&k_walk<DT, 8, 1, MODE, PAD>, grid, 64, 0, st, p);
+        }
+        return launch(&k_walk<DT, 4, 2, MODE, PAD>, grid, 128, 0, st, p);
     }
     if (p.N <= 16) return launch(&k_walk<DT, 4, 4, MODE, PAD>, grid, 256, 0, st, p);
     if (p.N <= 32) return launch(&k_walk<DT, 4, 8, MODE, PAD>, grid, 512, 0, st, p);
