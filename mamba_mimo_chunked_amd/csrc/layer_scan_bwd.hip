@@ -26,13 +26,14 @@ namespace mimo {
 namespace layer {
 namespace {
 
-// channels of a block, LDS floats: staging of dt, dt u, dy, three sums; b, c; fold results of four
-// waves; the states in front of a unit's later sub-tiles
+// channels of a block, LDS floats: staging of dt, dt u, dy, three sums; b, c, and zeros in their place for lanes without a
+// channel (zero times an infinite b or c would be NaN in the folds); fold results of four waves; the states in front of
+// a unit's later sub-tiles
 template <int NS, int Q> struct Shape {
     static constexpr int ST = NS == 4 && Q == 4 ? 16 : 8, NP = NS * Q, CPW = 64 / Q, CPB = 4 * CPW;
     static constexpr int ROWS = ST * CPB, BC = ST * NP, FOLD = 4 * 2 * BC;
     static constexpr int SUBS = UNIT / ST, CKPT = SUBS > 1 ? (SUBS - 1) * 256 * NS : 0;
-    static constexpr size_t lds = sizeof(float) * (6 * ROWS + 2 * BC + FOLD + CKPT);
+    static constexpr size_t lds = sizeof(float) * (6 * ROWS + 4 * BC + FOLD + CKPT);
 };
 
 // the NS values of the lanes that hold other channels of the same states, summed: NS / 4 (CPW = 4),
@@ -67,7 +68,7 @@ template <int DT, int NS, int Q, int PAD> __global__ __launch_bounds__(256, 2) v
     float *s_dt = lds, *s_du = s_dt + H::ROWS, *s_dy = s_du + H::ROWS;   // [ST][CPB]
     float* s_sum = s_dy + H::ROWS;                                       // y, s, <X, a>: [3][ST][CPB]
     float *s_b = s_sum + 3 * H::ROWS, *s_c = s_b + H::BC;                // [ST][NP]
-    float* s_fold = s_c + H::BC;                                         // [4][2][ST][NP]
+    float* s_fold = s_c + 3 * H::BC;                                     // behind 2 * BC zeros; [4][2][ST][NP]
     float* s_ck = s_fold + H::FOLD;                                      // [SUBS - 1][NS/4][256][4]
     const Place pl = place(p.q, blockIdx.x);
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), q = lane % Q, cb = w * H::CPW + lane / Q;
@@ -113,6 +114,9 @@ template <int DT, int NS, int Q, int PAD> __global__ __launch_bounds__(256, 2) v
     const raw *gb = at<DT>(p.b, pl) + (long)br * p.b.ts + tile.g * p.N + bn, *gc = at<DT>(p.c, pl) + (long)br * p.c.ts + tile.g * p.N + bn;
 
     const bool act = cb < tile.left;
+    const int bq = act ? q * NS : 2 * H::BC + q * NS;
+    if (tile.left < CPB)
+        for (int e = tid; e < 2 * H::BC; e += 256) s_c[H::BC + e] = 0.f;
     const int d = tile.c0 + (act ? cb : 0);
     float a[NS], hc[NS], h[NS], g[NS], da[NS] = {};   // hc: the chunk's first state
     const long dn = d * N;
@@ -239,7 +243,7 @@ template <int DT, int NS, int Q, int PAD> __global__ __launch_bounds__(256, 2) v
                     const float v = s_dt[t * CPB + cb], vu = s_du[t * CPB + cb];
 #pragma unroll
                     for (int k = 0; k < NS; ++k) {
-                        h[k] = __builtin_fmaf(exp2_hw(v * a[k]), h[k], vu * s_b[t * NP + q * NS + k]);
+                        h[k] = __builtin_fmaf(exp2_hw(v * a[k]), h[k], vu * s_b[t * NP + bq + k]);
                         if (PAD == 2) h[k] = on[k] ? h[k] : 0.f;
                     }
                 }
@@ -275,7 +279,7 @@ template <int DT, int NS, int Q, int PAD> __global__ __launch_bounds__(256, 2) v
                 for (int k = 0; k < NS; ++k) {
                     hp[t][k] = h[k];
                     e[t][k] = exp2_hw(v * a[k]);
-                    h[k] = __builtin_fmaf(e[t][k], h[k], vu * s_b[t * NP + q * NS + k]);
+                    h[k] = __builtin_fmaf(e[t][k], h[k], vu * s_b[t * NP + bq + k]);
                     if (PAD == 2) h[k] = on[k] ? h[k] : 0.f;
                 }
             }
@@ -285,7 +289,7 @@ template <int DT, int NS, int Q, int PAD> __global__ __launch_bounds__(256, 2) v
                 float y = 0.f, sgb = 0.f, sxa = 0.f, vb[NS], vc[NS];
 #pragma unroll
                 for (int k = 0; k < NS; ++k) {
-                    const float b = s_b[t * NP + q * NS + k], c = s_c[t * NP + q * NS + k];
+                    const float b = s_b[t * NP + bq + k], c = s_c[t * NP + bq + k];
                     const float ht = t == ST - 1 ? h[k] : hp[t + 1 < ST ? t + 1 : 0][k];
                     g[k] = __builtin_fmaf(c, dy, g[k]);
                     if (PAD == 2) g[k] = on[k] ? g[k] : 0.f;

@@ -127,3 +127,25 @@ def test_infinite_inputs(dtype, D, S, what, N):
     one = {k: (v[:, t:t + 1] if k in ("u", "dt", "b", "c", "z") else v) for k, v in names.items()}
     ref = R.scan(**one, cu=None, sp=True)
     assert torch.equal(_kind(y), _kind(ref["out"][:, 0])) and torch.equal(_kind(state), _kind(ref["state"])) and bool((_kind(y) != 0).any())
+
+
+@pytest.mark.parametrize("dtype,D,G,S,N,what,at", [
+    # channels that do not fill a tile: an infinite b or c beside lanes without a channel
+    (FF, 70, 1, 64, 16, "b", 20), (BF, 70, 1, 160, 8, "c", 20), (HF, 12, 2, 32, 40, "b", 5), (FF, 5, 1, 16, 5, "c", 15), (FF, 3, 1, 32, 100, "b", 31)])
+def test_infinite_input_at_the_edge_of_a_tile(dtype, D, G, S, N, what, at):
+    """What lies behind the channels or the tokens of a tile stays out of the gradients."""
+    g = _gen(N + S)
+    pos = lambda *s: (torch.rand(*s, generator=g) + 0.5)  # noqa: E731
+    x = {k: pos(1, S, D).to(dtype).cuda() for k in ("u", "dt", "z")}
+    x["dt"] = x["dt"] * -2
+    x.update({k: pos(1, S, G, N).to(dtype).cuda() for k in ("b", "c")})
+    x.update(a=-pos(D, N).cuda() * 0.2, d=pos(D).cuda(), dt_bias=torch.zeros(D).cuda(), initial_state=pos(1, D, N).cuda())
+    dout, ds = pos(1, S, D).to(dtype).cuda(), pos(1, D, N).cuda()
+    t = dout if what == "dout" else x[what]
+    t[(0, at, 2) if what == "dout" else (0, at, 0, N // 2)] = float("inf")
+    gr = m.mamba_scan_bwd(dout, **x, dstate=ds, dt_softplus=True)
+    x["initial"] = x.pop("initial_state")
+    ref = R.scan(**x, cu=None, sp=True, dout=dout, dstate=ds)
+    for k, v in gr._asdict().items():
+        assert torch.equal(_kind(v), _kind(ref[k])), k
+    assert bool((_kind(ref["dinitial_state" if what in ("c", "dout") else "dc"]) == 1).any())
