@@ -238,7 +238,10 @@ template <int DT, int NS, int KS, int MODE, bool PAD> __global__ __launch_bounds
         if (tt + TT > t1) {
 #pragma unroll
             for (int k = 0; k < TPW; ++k)
-                if (tt + w * TPW + k >= t1) f_v[k] = f_u[k] = f_z[k] = 0.f;
+                if (tt + w * TPW + k >= t1) {
+                    f_v[k] = f_u[k] = f_z[k] = 0.f;
+                    if (MODE == AGG2) r_g[k] = raw(0);
+                }
         }
 #pragma unroll
         for (int k = 0; k < TPW; ++k) {

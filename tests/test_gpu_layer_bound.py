@@ -131,7 +131,9 @@ def test_infinite_inputs(dtype, D, S, what, N):
 
 @pytest.mark.parametrize("dtype,D,G,S,N,what,at", [
     # channels that do not fill a tile: an infinite b or c beside lanes without a channel
-    (FF, 70, 1, 64, 16, "b", 20), (BF, 70, 1, 160, 8, "c", 20), (HF, 12, 2, 32, 40, "b", 5), (FF, 5, 1, 16, 5, "c", 15), (FF, 3, 1, 32, 100, "b", 31)])
+    (FF, 70, 1, 64, 16, "b", 20), (BF, 70, 1, 160, 8, "c", 20), (HF, 12, 2, 32, 40, "b", 5), (FF, 5, 1, 16, 5, "c", 15), (FF, 3, 1, 32, 100, "b", 31),
+    # the last token of a sequence that ends inside a tile
+    (FF, 8, 1, 197, 16, "dout", 196), (BF, 20, 1, 203, 6, "dout", 202), (FF, 6, 1, 205, 3, "dout", 204)])
 def test_infinite_input_at_the_edge_of_a_tile(dtype, D, G, S, N, what, at):
     """What lies behind the channels or the tokens of a tile stays out of the gradients."""
     g = _gen(N + S)
