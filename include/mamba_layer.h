@@ -18,8 +18,8 @@
  * elements; the batch stride is not used when packed) whose inner axes are
  * dense. Everything else is dense, row-major. Data tensors share one dtype
  * (MIMO_DTYPE_BF16, _FP16 or _FP32); parameters, the scan's state and their
- * gradients are fp32. All arithmetic is fp32, rounded once when stored. Outputs
- * and gradients must not overlap any input.
+ * gradients are fp32. All arithmetic is fp32, rounded once when stored. Outputs,
+ * gradients and the workspace must not overlap any input or each other.
  *
  * Ownership, asynchrony and errors as in mimo_bwd_fwd.h: the caller owns every
  * buffer; nothing is allocated; the call returns once its kernels are queued on

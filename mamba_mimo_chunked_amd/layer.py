@@ -268,7 +268,7 @@ def mamba_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, *,
     W, weight, bias = _check_filter(weight, bias, D, dev)
     initial_state = _param("initial_state", initial_state, (n, W - 1, D), x.dtype, dev)
     cu, x = _cu(cu_seqlens, dev), _dense_inner(x, 1)
-    res = _out(out, x, x=x, weight=weight, bias=bias, initial_state=initial_state)
+    res = _out(out, x, x=x, weight=weight, bias=bias, initial_state=initial_state, cu_seqlens=cu)
     state = x.new_empty((n, W - 1, D)) if return_state else None
     _call("mamba_conv_fwd", (n, S, D, W, code, silu, int(out is None), _ptr(cu), *_rows(x, cu is not None), _ptr(weight),
                              _ptr(bias), _ptr(initial_state), _ptr(res), _ptr(state)), dev)
@@ -293,6 +293,8 @@ def mamba_conv_bwd(dout, x, weight, bias=None, initial_state=None, dstate=None, 
     dx, dweight = _new_like(x), torch.empty_like(weight)
     dbias = None if bias is None else torch.empty_like(bias)
     dinit = None if initial_state is None else torch.empty_like(initial_state)
+    if workspace is not None:
+        _apart("workspace", workspace, dout=dout, x=x, weight=weight, bias=bias, initial_state=initial_state, dstate=dstate, cu_seqlens=cu)
     packed = cu is not None
     _call("mamba_conv_bwd", (n, S, D, W, code, silu, 0, _ptr(cu), *_rows(dout, packed), *_rows(x, packed), _ptr(weight), _ptr(bias),
                              _ptr(initial_state), _ptr(dstate), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(dinit)), dev, workspace)
@@ -340,7 +342,7 @@ def mamba_conv_step(x, state, weight, bias=None, state_indices=None, *, activati
     slots, stride, idx = _check_pool(state, (W - 1, D), x.dtype, state_indices, n, dev)
     x = _dense_inner(x, 1)
     _apart("state", state, x=x, weight=weight, bias=bias, state_indices=idx)
-    res = _out(out, x, x=x, state=state, weight=weight, bias=bias)
+    res = _out(out, x, x=x, state=state, weight=weight, bias=bias, state_indices=idx)
     _call("mamba_conv_step", (n, D, slots, stride, x.stride(0), W, code, silu, 0, x.data_ptr(), state.data_ptr(), weight.data_ptr(),
                               _ptr(bias), _ptr(idx), res.data_ptr()), dev)
     return res
@@ -385,7 +387,9 @@ def mamba_scan_fwd(u, dt, a, b, c, d=None, z=None, dt_bias=None, initial_state=N
     n, S, lead = _sequences("u", u, cu_seqlens, 1)
     D, G, N, (u, dt, b, c, z), (a, d, dt_bias) = _check_scan(u, dt, a, b, c, d, z, dt_bias, lead, dev)
     cu, initial_state = _cu(cu_seqlens, dev), _param("initial_state", initial_state, (n, D, N), _F32, dev)
-    res = _out(out, u, u=u, dt=dt, a=a, b=b, c=c, d=d, z=z, dt_bias=dt_bias, initial_state=initial_state)
+    res = _out(out, u, u=u, dt=dt, a=a, b=b, c=c, d=d, z=z, dt_bias=dt_bias, initial_state=initial_state, cu_seqlens=cu)
+    if workspace is not None:
+        _apart("workspace", workspace, u=u, dt=dt, a=a, b=b, c=c, d=d, z=z, dt_bias=dt_bias, initial_state=initial_state, cu_seqlens=cu, out=out)
     state = a.new_empty((n, D, N)) if return_state else None
     packed = cu is not None
     _call("mamba_scan_fwd", (n, S, D, G, N, code, int(bool(dt_softplus)), int(out is None), 0, _ptr(cu), *_rows(u, packed), *_rows(dt, packed),
@@ -407,8 +411,10 @@ def mamba_scan_bwd(dout, u, dt, a, b, c, d=None, z=None, dt_bias=None, initial_s
     dout = _data("dout", dout, u.shape, u.dtype, dev)
     initial_state = _param("initial_state", initial_state, (n, D, N), _F32, dev)
     cu, dstate = _cu(cu_seqlens, dev), _param("dstate", dstate, (n, D, N), _F32, dev)
+    if workspace is not None:
+        _apart("workspace", workspace, dout=dout, u=u, dt=dt, a=a, b=b, c=c, d=d, z=z, dt_bias=dt_bias, initial_state=initial_state,
+               dstate=dstate, cu_seqlens=cu)
     packed = cu is not None
-
     g = MambaScanGrads(*(None if t is None else _new_like(t) for t in (u, dt, a, b, c, d, z, dt_bias, initial_state)))
     _call("mamba_scan_bwd", (n, S, D, G, N, code, int(bool(dt_softplus)), 0, 0, _ptr(cu), *_rows(dout, packed), *_rows(u, packed),
                              *_rows(dt, packed), *_rows(b, packed), *_rows(c, packed), *_rows(z, packed), _ptr(a), _ptr(d), _ptr(dt_bias),
@@ -430,7 +436,7 @@ def mamba_scan_step(u, dt, state, a, b, c, d=None, z=None, dt_bias=None, state_i
     D, G, N, (u, dt, b, c, z), (a, d, dt_bias) = _check_scan(u, dt, a, b, c, d, z, dt_bias, (n,), dev)
     slots, stride, idx = _check_pool(state, (D, N), _F32, state_indices, n, dev)
     _apart("state", state, u=u, dt=dt, b=b, c=c, z=z, a=a, d=d, dt_bias=dt_bias, state_indices=idx)
-    res = _out(out, u, u=u, dt=dt, a=a, b=b, c=c, d=d, z=z, dt_bias=dt_bias, state=state)
+    res = _out(out, u, u=u, dt=dt, a=a, b=b, c=c, d=d, z=z, dt_bias=dt_bias, state=state, state_indices=idx)
     _call("mamba_scan_step", (n, D, G, N, slots, stride, code, int(bool(dt_softplus)), u.data_ptr(), u.stride(0), 0,
                               dt.data_ptr(), dt.stride(0), 0, b.data_ptr(), b.stride(0), 0, c.data_ptr(), c.stride(0), 0,
                               *(_NO_ROWS if z is None else (z.data_ptr(), z.stride(0), 0)),
@@ -491,6 +497,8 @@ def mamba_norm_bwd(dout, x, weight, bias=None, z=None, *, groups: int = 1, eps: 
     dev, code, silu, D, rows, zr, weight, bias = _check_norm("mamba_norm_bwd", x, weight, bias, z, groups, eps, gate, activation)
     _fits("dout", dout, x.shape, x.dtype, dev)
     dr = _row_view(dout, D)
+    if workspace is not None:
+        _apart("workspace", workspace, dout=dr, x=rows, z=zr, weight=weight, bias=bias)
     dx, dweight = _new_like(x), torch.empty_like(weight)
     dz, dbias = None if z is None else _new_like(z), None if bias is None else torch.empty_like(bias)
     _call("mamba_norm_bwd", (rows.shape[0], D, groups, dr.stride(0), rows.stride(0), 0 if zr is None else zr.stride(0), code,
