@@ -82,6 +82,8 @@ _READY = set()   # devices that passed the checks
 
 def _device(what, name, x):
     """The device of the first tensor; every other one has to be there too."""
+    if x is None:
+        raise ValueError(f"{name} is required")
     dev = x.device
     if dev in _READY:
         return dev
@@ -91,6 +93,12 @@ def _device(what, name, x):
         raise NotImplementedError(f"{what} supports gfx950 (MI355X) devices only")
     _READY.add(dev)
     return dev
+
+
+def _required(**tensors):
+    for name, x in tensors.items():
+        if x is None:
+            raise ValueError(f"{name} is required")
 
 
 def _fits(name, x, shape, dtype, device):
@@ -239,6 +247,8 @@ def _activation(activation):
 
 
 def _check_filter(weight, bias, D, device):
+    if weight is None:
+        _required(weight=weight)
     shape = weight.shape
     if len(shape) != 2 or shape[0] != D:
         raise ValueError(f"weight must have shape [{D}, taps], got {list(shape)}")
@@ -286,6 +296,8 @@ def mamba_conv_bwd(dout, x, weight, bias=None, initial_state=None, dstate=None, 
     n, S, lead = _sequences("x", x, cu_seqlens, 1)
     D = x.shape[-1]
     W, weight, bias = _check_filter(weight, bias, D, dev)
+    if dout is None:
+        _required(dout=dout)
     dout = _data("dout", dout, x.shape, x.dtype, dev)
     initial_state = _param("initial_state", initial_state, (n, W - 1, D), x.dtype, dev)
     dstate = _param("dstate", dstate, (n, W - 1, D), x.dtype, dev)
@@ -303,6 +315,8 @@ def mamba_conv_bwd(dout, x, weight, bias=None, initial_state=None, dstate=None, 
 
 def _check_pool(state, inner, dtype, indices, n, device):
     """A pool of states [slots, ...]: dense inside a slot, slots that do not overlap, updated in place."""
+    if state is None:
+        _required(state=state)
     shape = state.shape
     if len(shape) != 3 or shape[1] != inner[0] or shape[2] != inner[1]:
         raise ValueError(f"state must have shape [slots, {', '.join(map(str, inner))}], got {list(shape)}")
@@ -351,6 +365,8 @@ def mamba_conv_step(x, state, weight, bias=None, state_indices=None, *, activati
 # ---------------------------------------------------------------- selective scan
 def _check_scan(u, dt, a, b, c, d, z, dt_bias, lead, dev):
     """Sizes and the tensors with dense inner axes, parameters contiguous."""
+    if dt is None or a is None or b is None or c is None:
+        _required(dt=dt, a=a, b=b, c=c)
     rows, dtype, ashape, shape = u.shape, u.dtype, a.shape, b.shape
     D = rows[-1]
     if len(ashape) != 2 or ashape[0] != D:
@@ -408,6 +424,8 @@ def mamba_scan_bwd(dout, u, dt, a, b, c, d=None, z=None, dt_bias=None, initial_s
     code = _data_dtype("u", u)
     n, S, lead = _sequences("u", u, cu_seqlens, 1)
     D, G, N, (u, dt, b, c, z), (a, d, dt_bias) = _check_scan(u, dt, a, b, c, d, z, dt_bias, lead, dev)
+    if dout is None:
+        _required(dout=dout)
     dout = _data("dout", dout, u.shape, u.dtype, dev)
     initial_state = _param("initial_state", initial_state, (n, D, N), _F32, dev)
     cu, dstate = _cu(cu_seqlens, dev), _param("dstate", dstate, (n, D, N), _F32, dev)
@@ -459,6 +477,8 @@ def _check_norm(what, x, weight, bias, z, groups, eps, gate, activation):
         raise ValueError("gate must be 'before' or 'after'")
     if silu and z is not None:
         raise ValueError("activation and a gate z exclude each other")
+    if weight is None:
+        _required(weight=weight)
     if x.dim() < 1 or x.numel() == 0:
         raise ValueError(f"x must have shape [..., D] and not be empty, got {list(x.shape)}")
     D = x.shape[-1]
@@ -495,6 +515,8 @@ def mamba_norm_bwd(dout, x, weight, bias=None, z=None, *, groups: int = 1, eps: 
     """Gradients of ``sum(out * dout)`` for the arguments of ``mamba_norm_fwd``: dx and dz in x's dtype, dweight and
     dbias float32; dbias and dz are None without the input. The statistics are recomputed from x and z."""
     dev, code, silu, D, rows, zr, weight, bias = _check_norm("mamba_norm_bwd", x, weight, bias, z, groups, eps, gate, activation)
+    if dout is None:
+        _required(dout=dout)
     _fits("dout", dout, x.shape, x.dtype, dev)
     dr = _row_view(dout, D)
     if workspace is not None:
