@@ -103,11 +103,15 @@ __device__ __forceinline__ float decay_base(float a) {
 // FWD: the outputs. AGG: a chunk's last state from zero. AGG2: also the adjoint that leaves it to the
 // left, sum_t exp(a sum_{s <= t} dt) c[t] dy[t], from the same exponentials.
 enum { FWD, AGG, AGG2 };
-// Waves a SIMD that the registers have to allow, five where the states are split, whose few registers hold that many
-// ([8192, 1024], N = 16: 70.5 us without the bound, 69 with; [16 x 1024, 4096], N = 64: 741 and 734); six spill in the
-// backward walk (N = 8: 91 us instead of 80). 16 waves a block are four a SIMD.
-// Six for four states by eight waves, of which LDS lets three blocks in (N = 24: 113 us with the 82 registers that five allow).
-constexpr int walk_waves(int NS, int KS, int MODE) { return KS == 1 ? 2 : KS == 16 ? 4 : NS == 4 && KS == 8 && MODE == FWD ? 6 : 5; }
+// Waves a SIMD that the registers have to allow: five where the states are split over many waves, whose registers hold that
+// many without scratch memory ([8192, 1024], N = 16: 70.5 us without the bound, 69 with; [16 x 1024, 4096], N = 64: 741 and 734);
+// six spill in the backward walk (N = 8: 91 us instead of 80). Four in the outputs' walk by two waves, which five left with 2 to
+// 9 registers in scratch memory ([2048, 512], N = 8: 23.1 us, 24.1 with five; [4096, 512], N = 7: 25.4 and 27.2). Six for four
+// states by eight waves, of which LDS lets three blocks in (N = 24: 103 us, 113 with the 82 registers that five allow). 16 waves
+// a block are four a SIMD.
+constexpr int walk_waves(int NS, int KS, int MODE) {
+    return KS == 1 ? 2 : KS == 16 || (KS == 2 && MODE == FWD) ? 4 : NS == 4 && KS == 8 && MODE == FWD ? 6 : 5;
+}
 
 constexpr int UNIT = 16;   // tokens of a unit (backward)
 
