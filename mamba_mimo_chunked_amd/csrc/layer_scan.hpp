@@ -393,9 +393,11 @@ inline int waves_for(int64_t N) { return N <= 16 ? 1 : N <= 32 ? 2 : N <= 64 ? 4
 // 1024], N = 16 forward 78 us with 16 states a lane, 69 with four (8 x 2048 x 2048: 245 and 224; N = 32: 146 and 109).
 // What it costs, <c, h> joined in LDS over more waves, weighs more from N = 64 on, where eight are as fast as 16 or
 // faster ([16 x 1024, 4096] 783 us with 16 by 4, 741 with 8 by 8; [1024, 1024] 48 and 43; four, packed prompts: 270, 207 with
-// eight). For N <= 8 one wave needs no joining ([8192, 2048]: 85 us, 92 with 4 by 2), so those are split only where the GPU
-// is not full (D = 512: 37 us, 36 split) and in the backward walk, which joins nothing.
-constexpr long FEW = 1024;
+// eight). For N <= 8 one wave needs no joining, so those are split only where the blocks do not fill the GPU, up to ten a CU, and
+// in the backward walk, which joins nothing (N = 8, split and not: [2048, 512] 24.7 us and 26.6, [8192, 512], 2048 blocks, 35.0 and
+// 37.0, [8192, 1024], as many, 52.5 and 54.4, [2 x 4096, 768], 2064 blocks, 47.6 and 53.7; [8192, 2048], 4096 blocks, 90.7 and 86.6;
+// N = 6, [2 x 8192, 1024], as many, 87.0 and 80.4; fp32 [4096, 1024], 2048 blocks, 37.5 and 36.7).
+constexpr long FEW = 2560;
 inline int walk_threads(int64_t N) { return N <= 4 ? 64 : N <= 8 ? 128 : N <= 16 ? 256 : N <= 64 ? 512 : 1024; }   // at most
 inline int walk_places(int64_t N) { return N <= 4 ? 4 : N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : N <= 64 ? 64 : 128; }
 template <int DT, int MODE, bool PAD> mimo_status launch_shape(const ScanParams& p, hipStream_t st) {
