@@ -21,6 +21,12 @@
  * gradients are fp32. All arithmetic is fp32, rounded once when stored. Outputs,
  * gradients and the workspace must not overlap any input or each other.
  *
+ * Limits, MIMO_ERR_UNSUPPORTED beyond them: 65535 sequences or rows of a step, S up to
+ * 2^30, 2^20 channels, 1024 groups of the scan, 65535 groups and 2^31 groups of rows of
+ * the norm; 2^32 threads in a kernel, which only the norm comes near (a group of a row
+ * takes a thread for every 16 bytes, or element where rows are not aligned to that, in
+ * powers of two from 8 to 1024).
+ *
  * Ownership, asynchrony and errors as in mimo_bwd_fwd.h: the caller owns every
  * buffer; nothing is allocated; the call returns once its kernels are queued on
  * `stream`; on error nothing has been queued. A workspace's contents do not
@@ -120,11 +126,11 @@ mimo_status mamba_conv_step(const mamba_conv_step_args *args, void *stream);
  *   h[t]  = exp(dt'[t] a[d,n]) h[t-1] + dt'[t] u[t] b[t,g,n]
  *   y[t]  = sum_n c[t,g,n] h[t] + d[d] u[t];   out = y * silu(z), or y without z
  * from h = initial_state (zeros where NULL); state (optional) receives the last h.
- * Infinities come out as the formulas give them, with two exceptions: where the time
- * axis is cut, a state that is infinite at a cut may be NaN behind it if the decay
- * over a whole chunk is below fp32's range; and da may be NaN where a state is
- * infinite. Steps that let the state grow (dt' a > 0) must keep the product of the
- * factors exp(dt' a) of 128 tokens in fp32's range.
+ * Infinities come out as the formulas give them, but da may be NaN where a state is
+ * infinite. Long sequences are cut into chunks whose factors exp(dt' a) are multiplied
+ * over up to 32768 tokens before they meet a state: a product below fp32's range turns
+ * an infinite state into NaN, and one above it (steps that let the state grow, dt' a > 0)
+ * a state or an adjoint of zero.
  *   u, dt, z, out [.., D]; a [D, N]; b, c [.., G, N]; d, dt_bias [D] or NULL;
  *   states [n, D, N] fp32. N <= MAMBA_SCAN_MAX_STATE, D a multiple of G.
  */

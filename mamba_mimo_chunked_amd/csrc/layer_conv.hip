@@ -8,7 +8,7 @@
 // Two channels a thread and many threads beat wider accesses, whose windows cost the registers that
 // keep waves, and so loads, in flight: [8192, 2048] bf16 forward 18.5 us with eight channels, 17.1 with
 // four, 16.1 with two; [4, 4100, 2048] bf16 backward 156, 60 and 57 us. With scalar rows and the blocks' order
-// below, 14.0 us (4.8 TB/s) and 49 us (4.1); 8 x 8192 x 2048 forward 104 us (5.2 TB/s, as a copy).
+// below, 15.4 us (4.4 TB/s; 14.3 of them the kernel) and 50 us (4.0); 8 x 8192 x 2048 forward 104 us (5.2 TB/s, as a copy).
 #include "layer.hpp"
 
 namespace mimo {
@@ -311,7 +311,7 @@ template <int DT, int VEC, int W> __global__ __launch_bounds__(256) void k_conv_
 // ---------------------------------------------------------------- host side
 // Tokens of a chunk, 16 at least: longer chunks read fewer rows twice, and the backward pass leaves fewer partial
 // sums; shorter ones keep more threads, and so loads, in flight. Forward 2048 threads a CU and up to 32 tokens
-// ([8192, 2048] bf16: 14.0 us, 15.1 with 1024 threads; 8 x 8192 x 2048: 104 us at 32 tokens, 115 at 128); backward
+// ([8192, 2048] bf16, the same inputs: 14.5 us, 15.9 with 1024 threads; 8 x 8192 x 2048: 104 us at 32 tokens, 115 at 128); backward
 // 1024 threads a CU, whose registers allow no more, and up to 128 tokens ([4, 4100, 2048] bf16: 52 us before chunks were
 // equal, 55 with 2048;
 // 8 x 8192 x 2048: 243 us at 64 tokens, 208 at 128, before the scalar rows).

@@ -6,8 +6,8 @@
 //             dv = r (q - [mean(q)] - hat mean(q hat)), then through the gate
 //
 // TPR threads share a group of a row and keep it in registers (IT accesses of VEC elements each, up to
-// 16 bytes), so every input is read once: memory binds ([8192, 2048] bf16 in 8 groups with z: forward 18.4 us, 5.5 TB/s;
-// backward 37 us, 4.5 TB/s). Parameters are loaded before the sums, and nothing in an element's loop
+// 16 bytes), so every input is read once: memory binds ([8192, 2048] bf16 with z: in 8 groups forward 18.3 us, 5.5 TB/s, backward
+// 36.4 us, 4.6 TB/s, in one group backward 42.7 us). Parameters are loaded before the sums, and nothing in an element's loop
 // branches: with one load a parameter and branches inside, the forward pass took 39 us. Sums run over
 // lanes; groups that need more than a wave join the waves' sums in LDS. The variance is taken from the
 // centred values, not from a difference of sums.
@@ -183,8 +183,8 @@ template <int DT, int VEC, int TPR, int IT> __global__ __launch_bounds__(threads
     float w[IT][VEC], b[IT][VEC], dw[IT][VEC] = {}, db[IT][VEC] = {};
     Grp::param(p.w + c0, p.W, w);
     Grp::param(p.b ? p.b + c0 : nullptr, p.W, b);
-    // the next row's loads are in flight during a row, with 16-bit types: [8192, 2048] bf16 44 us instead of 48, but
-    // [4100, 2048] fp32 38 us instead of 34
+    // the next row's loads are in flight during a row, with 16-bit types: [8192, 2048] bf16, one group, 42.7 us instead of 43.4,
+    // [4100, 4096] fp16 46.8 instead of 48.0, but [4100, 2048] fp32 39.3 instead of 36.7
     constexpr bool AHEAD = DT != F32;
     typename Grp::Raw rx, rz, rd;
     auto fetch = [&](long row) {
@@ -300,7 +300,9 @@ __global__ __launch_bounds__(256) void k_norm_sums(NormParams p) {
 
 // ---------------------------------------------------------------- host side
 // Threads of a group: one access each where 1024 threads allow it (a group's values cost a thread about
-// a hundred registers an access in the backward pass), in whole waves beyond 32.
+// a hundred registers an access in the backward pass), in whole waves beyond 32. 1024 threads leave a thread 128 registers: the
+// backward pass in 16-bit types keeps 8 of its values in scratch memory with one access (fp16, groups over 4096 wide), 19 to
+// 23 with eight of one element each (groups over 2048 wide that are odd or not aligned).
 template <int DT, int VEC, class F> mimo_status with_shape(int W, F f) {
     const int nv = (W + VEC - 1) / VEC;
     if (nv <= 8) return f.template operator()<DT, VEC, 8, 1>();

@@ -129,8 +129,11 @@ struct FwdPlan {
 // Chunks are cut until about 6144 units of work (waves_for) walk, but, as a chunk costs its loads and its aggregate, not
 // below 64 tokens while 2048 walk, nor below 32 at all ([8192, 1024], N = 16: 67 us at 64 tokens, 70 at 48, 74 at 96;
 // [8192, 1024], N = 32: 107 us, 116 with half as many units; packed prompts [4100, 2048], N = 64: 206 us, 216 with half,
-// 214 with a third more). Half the GPU's waves (512 units) without chunks are as good as chunks, whose second walk (the
-// aggregates) nearly doubles the work.
+// 214 with a third more). A dense batch of 512 units is not cut, as the second walk (the aggregates) nearly doubles the work: bf16
+// [4 x 4096, 8192], N = 16, 677 us, 862 cut; [4 x 4096, 4096], N = 32, 583 and 731; [16 x 1024, 4096], N = 64, 744 and 1700. But
+// that counts units, and a tile is one block whatever N is: with few sequences of a wide state, or a narrow one, the blocks
+// leave CUs idle, and cut it would be faster ([8192, 4096], N = 128, 64 blocks: 2961 us, 1401 cut; [2 x 8192, 4096], N = 64: 1829
+// and 1310; [8 x 2048, 1024], N = 64: 460 and 361; [8 x 2048, 4096], N = 8: 504 and 313, N = 4: 516 and 242).
 mimo_status plan_fwd(const mamba_scan_fwd_args* a, FwdPlan* pl) {
     if (a == nullptr) return bad("args must not be NULL");
     const mimo_status s = check_scan(a->n, a->S, a->D, a->G, a->N, a->dtype);

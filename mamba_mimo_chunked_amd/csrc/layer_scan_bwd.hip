@@ -15,11 +15,15 @@
 // them: 128, or 64 for Q = 2, whose staging takes the rest), then backward through them. The state in
 // front of a unit comes from the walk, which leaves it (from zero, at the chunk's start) with the sum of
 // dt to there: h = uh + exp(a udt) h(chunk). So an exponential is computed twice (walk, sub-tile) and no
-// state but every sixteenth goes to memory. 4 x 4096 tokens, D = 1024, N = 16, bf16: 327 us, of them the
-// walk 86, this kernel 245 (its vector units busy 77 % of the time: 97 vector instructions a token and
-// 64 states), sums 12; walking the chunk a third time for its states, with 64-bit row addresses, took
+// state but every sixteenth goes to memory. 4 x 4096 tokens, D = 1024, N = 16, bf16: 330 us, of them the
+// walk 86, this kernel 250 (its vector units busy 77 % of the time: 97 vector instructions a token and
+// 64 states), sums 12 (times under a profiler); walking the chunk a third time for its states, with 64-bit row addresses, took
 // 415 us. Vector instructions bind; two waves a SIMD fill 256 registers each (with 168 and three waves:
-// 436 us).
+// 436 us) and more: what lives across a sub-tile (the states of the chunk and the unit, the next unit's, da) stays in scratch
+// memory in part, 4 registers at N = 9 to 16, 28 to 30 to N = 32, 19 to 24 to N = 64, 31 to 33 to N = 128, none to N = 8.
+// 2 x 2048 tokens, D = 1024, bf16: N = 8 79 us, 32 (fp32) 208, 64 335; 2 x 1024, N = 128 396.
+// Lanes work on nothing where N is less than the shape's states (8, 16, 32, 64, 128: at N = 1 seven eighths of them) and where
+// the channels of a group do not fill its tile (128 channels to N = 8, 64 to 32, 32 to 64, 16 to 128).
 #include "layer_scan.hpp"
 
 namespace mimo {
