@@ -23,9 +23,7 @@
  *
  * Limits, MIMO_ERR_UNSUPPORTED beyond them: 65535 sequences or rows of a step, S up to
  * 2^30, 2^20 channels, 1024 groups of the scan, 65535 groups and 2^31 groups of rows of
- * the norm; 2^32 threads in a kernel, which only the norm comes near (a group of a row
- * takes a thread for every 16 bytes, or element where rows are not aligned to that, in
- * powers of two from 8 to 1024).
+ * the norm, 2^32 threads along an axis of a kernel's grid.
  *
  * Ownership, asynchrony and errors as in mimo_bwd_fwd.h: the caller owns every
  * buffer; nothing is allocated; the call returns once its kernels are queued on

@@ -137,7 +137,7 @@ template <int DT, int VEC, int TPR, int IT> __global__ __launch_bounds__(threads
     typedef raw_t<DT> raw;
     typedef Group<DT, VEC, TPR, IT> Grp;
     __shared__ float s[2][16];
-    const unsigned item = blockIdx.x * (threads_of(TPR) / TPR) + threadIdx.x / TPR;
+    const unsigned item = (blockIdx.y * gridDim.x + blockIdx.x) * (threads_of(TPR) / TPR) + threadIdx.x / TPR;
     const bool act = item < (unsigned)p.rows * (unsigned)p.G;
     const unsigned in = act ? item / (unsigned)p.G : 0;
     const long row = in;
@@ -348,8 +348,10 @@ struct FwdRun {
     NormParams p;
     hipStream_t st;
     template <int DT, int VEC, int TPR, int IT> mimo_status operator()() {
-        const long per = threads_of(TPR) / TPR, blocks = (p.rows * p.G + per - 1) / per;
-        return launch(&k_norm_fwd<DT, VEC, TPR, IT>, dim3((unsigned)blocks), threads_of(TPR), 0, st, p);
+        // in more than one row of blocks where they are too many for one; rows * G + a row of blocks is below 2^32
+        const long per = threads_of(TPR) / TPR, blocks = (p.rows * p.G + per - 1) / per, most = 0xffffffffL / threads_of(TPR);
+        const long along = blocks < most ? blocks : most;
+        return launch(&k_norm_fwd<DT, VEC, TPR, IT>, dim3((unsigned)along, (unsigned)((blocks + along - 1) / along)), threads_of(TPR), 0, st, p);
     }
 };
 struct BwdRun {

@@ -151,3 +151,15 @@ def test_infinite_input_at_the_edge_of_a_tile(dtype, D, G, S, N, what, at):
     for k, v in gr._asdict().items():
         assert torch.equal(_kind(v), _kind(ref[k])), k
     assert bool((_kind(ref["dinitial_state" if what in ("c", "dout") else "dc"]) == 1).any())
+
+
+def test_norm_of_more_rows_than_one_axis_of_blocks():
+    """Eight threads a row and 2^29 rows: 2^32 threads and more. The last rows as by themselves, the first as well."""
+    rows, D, n = (1 << 29) + 1000, 2, 3000
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.empty(rows, D, dtype=BF, device="cuda").normal_(generator=g)
+    w = torch.tensor([0.7, -1.3], device="cuda")
+    y = m.mamba_norm_fwd(x, w, activation="silu", out=torch.full_like(x, float("nan")))
+    assert not bool(y.isnan().any())        # every row was written
+    for part in (slice(0, n), slice(rows // 2, rows // 2 + n), slice(rows - n, rows)):
+        assert _same(y[part], m.mamba_norm_fwd(x[part].clone(), w, activation="silu"))
