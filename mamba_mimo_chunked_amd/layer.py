@@ -8,8 +8,10 @@ gradients are float32; so is all arithmetic, rounded once when stored. Sequences
 [B, S, ...] or packed along one token axis [T, ...] with ``cu_seqlens`` [n + 1] (int32, on the device:
 0, then each sequence's end, not decreasing, at most T; its values are not checked, and sequences may
 be empty). Token and batch strides are free as long as the inner axes are dense; other layouts are
-copied. Calls are asynchronous on the current HIP stream of the tensors' device. Sums run in a fixed
-order: equal inputs give equal bits.
+copied. What a call writes (a given output or workspace, a pool of states) must not overlap what it
+reads. Calls are asynchronous on the current HIP stream of the tensors' device. Sums run in a fixed
+order: equal inputs give equal bits. Limits, infinite inputs and the size of workspaces:
+``include/mamba_layer.h``.
 """
 
 from __future__ import annotations
