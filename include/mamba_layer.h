@@ -1,9 +1,10 @@
 /*
  * mamba_layer.h -- C ABI of the layer operators around the scan on MI355X
  * (gfx950): the short causal convolution in front of it, the selective scan
- * whose decay differs for each channel and state, and the gated group norm
- * behind it. Each has a forward and a backward pass; the two with a state also
- * have a step of one token. They live in the library of mimo_bwd_fwd.h, with
+ * whose decay differs for each channel and state, the gated linear recurrence, and
+ * the gated group norm behind it; and what lies between blocks, the addition to
+ * the residual stream with its norm. Each has a forward and a backward pass;
+ * those with a state also have a step of one token. They live in the library of mimo_bwd_fwd.h, with
  * its status codes, mimo_last_error() and MIMO_DTYPE_* codes.
  *
  * Sequences. n sequences are given dense, [n, S, ...], or packed along one
@@ -23,7 +24,7 @@
  *
  * Limits, MIMO_ERR_UNSUPPORTED beyond them: 65535 sequences or rows of a step, S up to
  * 2^30, 2^20 channels, 1024 groups of the scan, 65535 groups and 2^31 groups of rows of
- * the norm, 2^32 threads along an axis of a kernel's grid.
+ * the norms, 2^32 threads along an axis of a kernel's grid.
  *
  * Ownership, asynchrony and errors as in mimo_bwd_fwd.h: the caller owns every
  * buffer; nothing is allocated; the call returns once its kernels are queued on
@@ -220,6 +221,140 @@ typedef struct mamba_norm_bwd_args {
 } mamba_norm_bwd_args;
 mimo_status mamba_norm_bwd_workspace_size(const mamba_norm_bwd_args *args, size_t *bytes);
 mimo_status mamba_norm_bwd(const mamba_norm_bwd_args *args, void *stream);
+
+/*
+ * Gated linear recurrence, one state a channel:
+ *   l[t]  = -rate * softplus(decay[d]) * sigmoid(r[t] + r_bias[d])
+ *   h[t]  = exp(l[t]) h[t-1] + sqrt(1 - exp(2 l[t])) * sigmoid(i[t] + i_bias[d]) * x[t]
+ *   out   = h * silu(z), or h without z
+ * from h = initial_state (zeros where NULL); state (optional) receives the last h.
+ * Long sequences are cut into chunks whose factors exp(l) are multiplied before they
+ * meet a state: a product below fp32's range turns an infinite state into NaN. A decay
+ * below -87 counts as none (its softplus is below fp32's range): nothing is forgotten or
+ * enters.
+ *   x, r, i, z, out [.., D]; decay, r_bias, i_bias [D] (the biases optional); states
+ *   [n, D] fp32. rate is not negative.
+ */
+typedef struct mamba_recur_fwd_args {
+    int64_t n, S, D;
+    int32_t dtype, zero_tail;
+    float rate;
+    int32_t reserved;
+    const int32_t *cu_seqlens;
+    mamba_rows x, r, i;
+    mamba_rows z;                 /* data NULL: no gate */
+    const float *decay, *r_bias, *i_bias;
+    const float *initial_state;   /* optional */
+    void *out;
+    float *state;                 /* optional */
+    void *workspace;              /* mamba_recur_fwd_workspace_size() bytes, 256-byte aligned */
+    size_t workspace_bytes;
+} mamba_recur_fwd_args;
+mimo_status mamba_recur_fwd_workspace_size(const mamba_recur_fwd_args *args, size_t *bytes);
+mimo_status mamba_recur_fwd(const mamba_recur_fwd_args *args, void *stream);
+
+/* Gradients of sum(out * dout) + sum(state * dstate). dx, dr, di, dz [.., D] in the
+ * data dtype; ddecay, dr_bias, di_bias [D] and dinitial_state fp32. dz is required iff
+ * z is given, dr_bias iff r_bias is, di_bias iff i_bias is; dinitial_state and dstate
+ * are optional. Where exp(l) = 1 nothing of x enters, and the gradients are those of the
+ * limit (no part of r, decay or their biases). Tokens behind the last sequence get zero
+ * gradients. */
+typedef struct mamba_recur_bwd_args {
+    int64_t n, S, D;
+    int32_t dtype, reserved0;
+    float rate;
+    int32_t reserved1;
+    const int32_t *cu_seqlens;
+    mamba_rows dout, x, r, i;
+    mamba_rows z;                 /* data NULL: no gate */
+    const float *decay, *r_bias, *i_bias;
+    const float *initial_state, *dstate;
+    void *dx, *dr, *di, *dz;
+    float *ddecay, *dr_bias, *di_bias, *dinitial_state;
+    void *workspace;              /* mamba_recur_bwd_workspace_size() bytes, 256-byte aligned */
+    size_t workspace_bytes;
+} mamba_recur_bwd_args;
+mimo_status mamba_recur_bwd_workspace_size(const mamba_recur_bwd_args *args, size_t *bytes);
+mimo_status mamba_recur_bwd(const mamba_recur_bwd_args *args, void *stream);
+
+/* One token for each of n rows: x, r, i, z, out [n, D]; state [slots, D] fp32
+ * (slot_stride elements from slot to slot), updated in place. Slots and indices as for
+ * mamba_conv_step. Here batch_stride is the row stride. */
+typedef struct mamba_recur_step_args {
+    int64_t n, D, slots, slot_stride;
+    int32_t dtype, reserved;
+    float rate;
+    int32_t reserved1;
+    mamba_rows x, r, i;
+    mamba_rows z;                 /* data NULL: no gate */
+    const float *decay, *r_bias, *i_bias;
+    float *state;
+    const int32_t *indices;       /* optional */
+    void *out;
+} mamba_recur_step_args;
+mimo_status mamba_recur_step(const mamba_recur_step_args *args, void *stream);
+
+/*
+ * Addition to the residual stream and root-mean-square norm of the sum, by rows:
+ *   v = dropout(x) + residual (or dropout(x));  y = v / sqrt(mean(v^2) + eps) * weight
+ * The norm takes v before it is rounded to `sum`. The stream (residual, sum, and their
+ * gradients) has the data dtype, or fp32 where wide is set. A square of v beyond fp32's
+ * range (|v| > 1.8e19) makes the row's norm infinite.
+ *
+ * Dropout: an element is dropped, whatever its value, where its 16 bits are below
+ * `drop`, and multiplied by 65536 / (65536 - drop) elsewhere. The bits of the columns
+ * 8 c .. 8 c + 7 of row k are the four words of Philox4x32 with ten rounds (J. Salmon
+ * et al., "Parallel random numbers: as easy as 1, 2, 3", 2011), low halves first, for
+ * the counter (c, k, low word, high word of seed[1]) and the key (low word, high word
+ * of seed[0]); seed lies on the device, so that a captured call takes new numbers. No
+ * mask is stored: the backward pass draws the bits again.
+ *
+ * out: y in the data dtype (MAMBA_OUT_SAME), or in 8 bits with scales, y = q * scale:
+ * q in e4m3 (no infinities, largest 448) or whole numbers from -127 to 127, rounded to
+ * nearest even; a scale for every `block` columns (32, 64, 128 or 256; the last block may
+ * be short), or for the row (0). scale = max(largest |y|, 2^-100) / (448 or 127); where a
+ * block holds a value that is not finite its scale is NaN, and q NaN (e4m3) or 0.
+ *   x [rows, D] (row stride in elements), residual likewise; sum, out [rows, D] dense;
+ *   weight [D]; scale [rows, ceil(D / block)] or [rows]. D <= MAMBA_ADD_NORM_MAX_WIDTH.
+ *   sum is optional where nothing is added or dropped and the stream has the data dtype.
+ */
+#define MAMBA_ADD_NORM_MAX_WIDTH 16384
+#define MAMBA_OUT_SAME 0
+#define MAMBA_OUT_E4M3 1
+#define MAMBA_OUT_INT8 2
+typedef struct mamba_add_norm_fwd_args {
+    int64_t rows, D;
+    int64_t x_stride, residual_stride;
+    int32_t dtype, wide, out_kind, block;
+    int32_t drop;                 /* of 65536; 0: none */
+    float eps;
+    const void *x, *residual;     /* residual optional */
+    const int64_t *seed;          /* [2], required where drop is not 0 */
+    const float *weight;
+    void *sum, *out;
+    float *scale;                 /* required unless MAMBA_OUT_SAME */
+} mamba_add_norm_fwd_args;
+mimo_status mamba_add_norm_fwd(const mamba_add_norm_fwd_args *args, void *stream);
+
+/* Gradients of sum(y * dout) + sum(sum * dsum), from the sum: with dv the gradient of v,
+ * dx = dropout's factor * dv in the data dtype (that of dout), dresidual = dv in the
+ * stream's, dweight [D] fp32. dsum and dresidual are optional. */
+typedef struct mamba_add_norm_bwd_args {
+    int64_t rows, D;
+    int64_t dout_stride, sum_stride, dsum_stride;
+    int32_t dtype, wide;
+    int32_t drop;
+    float eps;
+    const void *dout, *sum, *dsum;
+    const int64_t *seed;
+    const float *weight;
+    void *dx, *dresidual;
+    float *dweight;
+    void *workspace;              /* mamba_add_norm_bwd_workspace_size() bytes, 256-byte aligned */
+    size_t workspace_bytes;
+} mamba_add_norm_bwd_args;
+mimo_status mamba_add_norm_bwd_workspace_size(const mamba_add_norm_bwd_args *args, size_t *bytes);
+mimo_status mamba_add_norm_bwd(const mamba_add_norm_bwd_args *args, void *stream);
 
 #ifdef __cplusplus
 }

@@ -231,6 +231,71 @@ class MambaNormBwdArgs(ctypes.Structure):
     ]
 
 
+class MambaRecurFwdArgs(ctypes.Structure):
+    """Mirror of ``mamba_recur_fwd_args``."""
+
+    _fields_ = [
+        ("n", ctypes.c_int64), ("S", ctypes.c_int64), ("D", ctypes.c_int64), ("dtype", ctypes.c_int32),
+        ("zero_tail", ctypes.c_int32), ("rate", ctypes.c_float), ("reserved", ctypes.c_int32),
+        ("cu_seqlens", ctypes.c_void_p), ("x", MambaRows), ("r", MambaRows), ("i", MambaRows), ("z", MambaRows),
+        ("decay", ctypes.c_void_p), ("r_bias", ctypes.c_void_p), ("i_bias", ctypes.c_void_p),
+        ("initial_state", ctypes.c_void_p), ("out", ctypes.c_void_p), ("state", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class MambaRecurBwdArgs(ctypes.Structure):
+    """Mirror of ``mamba_recur_bwd_args``."""
+
+    _fields_ = [
+        ("n", ctypes.c_int64), ("S", ctypes.c_int64), ("D", ctypes.c_int64), ("dtype", ctypes.c_int32),
+        ("reserved0", ctypes.c_int32), ("rate", ctypes.c_float), ("reserved1", ctypes.c_int32),
+        ("cu_seqlens", ctypes.c_void_p), ("dout", MambaRows), ("x", MambaRows), ("r", MambaRows), ("i", MambaRows),
+        ("z", MambaRows), ("decay", ctypes.c_void_p), ("r_bias", ctypes.c_void_p), ("i_bias", ctypes.c_void_p),
+        ("initial_state", ctypes.c_void_p), ("dstate", ctypes.c_void_p), ("dx", ctypes.c_void_p),
+        ("dr", ctypes.c_void_p), ("di", ctypes.c_void_p), ("dz", ctypes.c_void_p), ("ddecay", ctypes.c_void_p),
+        ("dr_bias", ctypes.c_void_p), ("di_bias", ctypes.c_void_p), ("dinitial_state", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class MambaRecurStepArgs(ctypes.Structure):
+    """Mirror of ``mamba_recur_step_args``."""
+
+    _fields_ = [
+        ("n", ctypes.c_int64), ("D", ctypes.c_int64), ("slots", ctypes.c_int64), ("slot_stride", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32), ("rate", ctypes.c_float),
+        ("reserved1", ctypes.c_int32), ("x", MambaRows), ("r", MambaRows), ("i", MambaRows), ("z", MambaRows),
+        ("decay", ctypes.c_void_p), ("r_bias", ctypes.c_void_p), ("i_bias", ctypes.c_void_p),
+        ("state", ctypes.c_void_p), ("indices", ctypes.c_void_p), ("out", ctypes.c_void_p),
+    ]
+
+
+class MambaAddNormFwdArgs(ctypes.Structure):
+    """Mirror of ``mamba_add_norm_fwd_args``."""
+
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("D", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+        ("residual_stride", ctypes.c_int64), ("dtype", ctypes.c_int32), ("wide", ctypes.c_int32),
+        ("out_kind", ctypes.c_int32), ("block", ctypes.c_int32), ("drop", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("seed", ctypes.c_void_p),
+        ("weight", ctypes.c_void_p), ("sum", ctypes.c_void_p), ("out", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+    ]
+
+
+class MambaAddNormBwdArgs(ctypes.Structure):
+    """Mirror of ``mamba_add_norm_bwd_args``."""
+
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("D", ctypes.c_int64), ("dout_stride", ctypes.c_int64),
+        ("sum_stride", ctypes.c_int64), ("dsum_stride", ctypes.c_int64), ("dtype", ctypes.c_int32),
+        ("wide", ctypes.c_int32), ("drop", ctypes.c_int32), ("eps", ctypes.c_float), ("dout", ctypes.c_void_p),
+        ("sum", ctypes.c_void_p), ("dsum", ctypes.c_void_p), ("seed", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+        ("dx", ctypes.c_void_p), ("dresidual", ctypes.c_void_p), ("dweight", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 DTYPE_BF16, DTYPE_FP16, DTYPE_FP32 = 0, 1, 2
 
 EXPORTED = ("mimo_bwd_fwd", "mimo_bwd_fwd_timed", "mimo_bwd_fwd_workspace_size", "mimo_fwd",
@@ -245,6 +310,9 @@ LAYER_CALLS = {
     "mamba_conv_step": (MambaConvStepArgs, False), "mamba_scan_fwd": (MambaScanFwdArgs, True),
     "mamba_scan_bwd": (MambaScanBwdArgs, True), "mamba_scan_step": (MambaScanStepArgs, False),
     "mamba_norm_fwd": (MambaNormFwdArgs, False), "mamba_norm_bwd": (MambaNormBwdArgs, True),
+    "mamba_recur_fwd": (MambaRecurFwdArgs, True), "mamba_recur_bwd": (MambaRecurBwdArgs, True),
+    "mamba_recur_step": (MambaRecurStepArgs, False), "mamba_add_norm_fwd": (MambaAddNormFwdArgs, False),
+    "mamba_add_norm_bwd": (MambaAddNormBwdArgs, True),
 }
 NOALLOC_SCRATCH_BYTES = 64 << 20
 TIMED_EVENTS = 5

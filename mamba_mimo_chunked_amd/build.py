@@ -16,7 +16,8 @@ PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
 CSRC = PKG / "csrc"
 SOURCES = (["mimo_bwd_fwd.hip"] + [f"b2_{t}.hip" for t in ("bf16", "f16", "f32")]
-           + ["layer_conv.hip", "layer_scan.hip", "layer_scan_bwd.hip", "layer_norm.hip"]
+           + ["layer_conv.hip", "layer_scan.hip", "layer_scan_bwd.hip", "layer_norm.hip",
+              "layer_add_norm.hip", "layer_add_norm_bwd.hip", "layer_recur.hip", "layer_recur_bwd.hip"]
            + [f"tiles_f32_mt{m}.hip" for m in (32, 64, 128)]
            + [f"tiles_rp{r}_ct{c}.hip" for r, c in
               ((1, 1), (1, 2), (1, 4), (2, 1), (2, 2), (2, 4), (4, 1), (4, 2), (8, 1))])

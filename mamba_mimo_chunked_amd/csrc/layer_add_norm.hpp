@@ -1,0 +1,142 @@
+// Addition to the residual stream and root-mean-square norm of the sum: what the forward and the backward pass share.
+//
+//   v = dropout(x) + residual;  r = 1 / sqrt(mean(v^2) + eps);  y = v r w
+//   backward: q = dout w;  hat = v r;  dv = r (q - hat mean(q hat)) + dsum;  dw = sum dout hat;  dx = dropout(dv)
+//
+// TPR threads share a row; thread t takes the eight columns from 8 t on (and 8 TPR further on, where a row needs more
+// than 1024 threads), whatever the types: 16 bytes of a 16-bit type, twice 16 of fp32, 8 of an 8-bit output, and the
+// eight elements that one counter of the generator covers. Rows that allow no 16-byte access take elements of their own.
+#pragma once
+#include "layer.hpp"
+
+namespace mimo {
+namespace layer {
+
+constexpr int NV = 8;   // columns of a thread's access
+
+// the sum over the TPR threads of a row, in all of them; `s`: LDS of a float a wave, safe to use again after the
+// next call on another one
+template <int TPR> __device__ __forceinline__ float sum_row(float x, float* s) {
+    if constexpr (TPR <= 64) return sum_wave<TPR>(x);
+    else {
+        x = sum_wave<64>(x);
+        if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = x;
+        __syncthreads();
+        const int first = threadIdx.x / TPR * (TPR / 64);
+        x = 0.f;
+#pragma unroll
+        for (int k = 0; k < TPR / 64; ++k) x += s[first + k];
+        return x;
+    }
+}
+constexpr int block_of(int TPR) { return TPR < 256 ? 256 : TPR; }
+
+// eight neighbouring elements from column c of a row of D on, zeros behind the row
+template <int DT, bool WIDE> struct Eight {
+    Pack<DT, WIDE ? (DT == F32 ? 4 : 8) : 1> t[WIDE ? (DT == F32 ? 2 : 1) : 8];
+    __device__ __forceinline__ void fetch(const raw_t<DT>* p, int c, int D) {
+        if constexpr (WIDE) {
+            if (c < D) {
+#pragma unroll
+                for (int k = 0; k < (DT == F32 ? 2 : 1); ++k) t[k] = load<DT, DT == F32 ? 4 : 8>(p + c + 4 * k);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                t[k].v[0] = raw_t<DT>(0);
+                if (c + k < D) t[k].v[0] = p[c + k];
+            }
+        }
+    }
+    __device__ __forceinline__ void read(int c, int D, float (&x)[NV]) const {
+        if constexpr (WIDE) {
+            constexpr int V = DT == F32 ? 4 : 8;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) x[k] = c < D ? to_f<DT>(t[k / V].v[k % V]) : 0.f;
+        } else {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) x[k] = to_f<DT>(t[k].v[0]);
+        }
+    }
+};
+template <int DT, bool WIDE> __device__ __forceinline__ void put8(raw_t<DT>* p, int c, int D, const float (&x)[NV]) {
+    if constexpr (WIDE) {
+        if (c >= D) return;
+        if constexpr (DT == F32) {
+            const float lo[4] = {x[0], x[1], x[2], x[3]}, hi[4] = {x[4], x[5], x[6], x[7]};
+            store<DT, 4>(p + c, lo);
+            store<DT, 4>(p + c + 4, hi);
+        } else store<DT, 8>(p + c, x);
+    } else {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (c + k < D) p[c + k] = to_raw<DT>(x[k]);
+    }
+}
+
+// Which of the eight elements of (row, columns 8 c ..) are kept: bit k of the result. Philox4x32, ten rounds (J. Salmon
+// et al., "Parallel random numbers: as easy as 1, 2, 3", 2011): four multiplications of 32 to 64 bits in the round, for
+// eight elements of 16 bits.
+__device__ __forceinline__ unsigned kept8(const long* seed, unsigned c, unsigned row, unsigned drop) {
+    const unsigned long key = seed[0], off = seed[1];
+    unsigned c0 = c, c1 = row, c2 = (unsigned)off, c3 = (unsigned)(off >> 32), k0 = (unsigned)key, k1 = (unsigned)(key >> 32);
+#pragma unroll
+    for (int k = 0; k < 10; ++k) {
+        const unsigned long a = (unsigned long)c0 * 0xD2511F53u, b = (unsigned long)c2 * 0xCD9E8D57u;
+        c0 = (unsigned)(b >> 32) ^ c1 ^ k0;
+        c1 = (unsigned)b;
+        c2 = (unsigned)(a >> 32) ^ c3 ^ k1;
+        c3 = (unsigned)a;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    const unsigned w[4] = {c0, c1, c2, c3};
+    unsigned m = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        m |= ((w[k] & 0xffffu) >= drop ? 1u : 0u) << (2 * k);
+        m |= ((w[k] >> 16) >= drop ? 1u : 0u) << (2 * k + 1);
+    }
+    return m;
+}
+
+// ---------------------------------------------------------------- host side
+// Threads of a row: one access each where 1024 threads allow it, 16 or whole waves.
+template <class F> mimo_status with_row(int64_t D, F f) {
+    const int64_t nv = (D + NV - 1) / NV;
+    if (nv <= 16) return f.template operator()<16, 1>();
+    if (nv <= 64) return f.template operator()<64, 1>();
+    if (nv <= 128) return f.template operator()<128, 1>();
+    if (nv <= 256) return f.template operator()<256, 1>();
+    if (nv <= 512) return f.template operator()<512, 1>();
+    if (nv <= 1024) return f.template operator()<1024, 1>();
+    return f.template operator()<1024, 2>();
+}
+inline int row_threads(int64_t D) {
+    const int64_t nv = (D + NV - 1) / NV;
+    return nv <= 16 ? 16 : nv <= 64 ? 64 : nv <= 128 ? 128 : nv <= 256 ? 256 : nv <= 512 ? 512 : 1024;
+}
+// f<type of the data, type of the stream, wide accesses>
+template <class F> mimo_status with_types(int dtype, int wide_stream, bool even, F f) {
+    if (dtype == F32) return even ? f.template operator()<F32, F32, true>() : f.template operator()<F32, F32, false>();
+    if (dtype == BF16) {
+        if (wide_stream) return even ? f.template operator()<BF16, F32, true>() : f.template operator()<BF16, F32, false>();
+        return even ? f.template operator()<BF16, BF16, true>() : f.template operator()<BF16, BF16, false>();
+    }
+    if (wide_stream) return even ? f.template operator()<F16, F32, true>() : f.template operator()<F16, F32, false>();
+    return even ? f.template operator()<F16, F16, true>() : f.template operator()<F16, F16, false>();
+}
+inline mimo_status check_add_norm(int64_t rows, int64_t D, int dtype, float eps, int drop, const void* seed) {
+    if (rows < 1 || D < 1) return bad("rows and channels must be positive");
+    if (dtype < BF16 || dtype > F32) return set_error(MIMO_ERR_TYPE, "dtype must be a MIMO_DTYPE_* code");
+    if (!(eps >= 0.f)) return bad("eps must not be negative");
+    if (drop < 0 || drop > 65535) return bad("drop must be in [0, 65535]");
+    if (drop && !seed) return bad("dropout needs a seed");
+    if (D > MAMBA_ADD_NORM_MAX_WIDTH) return unsupported("more than 16384 channels");
+    if (rows > (int64_t)1 << 31) return unsupported("more than 2^31 rows");
+    return MIMO_OK;
+}
+inline float drop_factor(int drop) { return 65536.f / (float)(65536 - drop); }
+
+}  // namespace layer
+}  // namespace mimo

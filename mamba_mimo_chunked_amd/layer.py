@@ -1,7 +1,8 @@
 """The layer operators around the scan: the short causal convolution ``mamba_conv_*``, the selective
-scan ``mamba_scan_*`` with a decay for each channel and state, and the gated group norm
-``mamba_norm_*``, each as a forward call, a backward call that returns the gradients, and (where there
-is a state) a step of one token.
+scan ``mamba_scan_*`` with a decay for each channel and state, the gated linear recurrence
+``mamba_recur_*``, the gated group norm ``mamba_norm_*``, and between blocks the addition to the residual
+stream with its norm ``mamba_add_norm_*``, each as a forward call, a backward call that returns the
+gradients, and (where there is a state) a step of one token.
 
 Data tensors share one dtype: bfloat16, float16 or float32. Parameters, the scan's state and their
 gradients are float32; so is all arithmetic, rounded once when stored. Sequences are a dense batch
@@ -25,9 +26,10 @@ from . import _lib
 from .api import _BWD2_DTYPES as _DTYPES
 from .api import _check_output, _check_tensor, _is_gfx950, _raise, _workspace
 
-__all__ = ["MambaConvOutputs", "MambaConvGrads", "MambaScanOutputs", "MambaScanGrads", "MambaNormGrads", "mamba_conv_fwd",
+__all__ = ["MambaConvOutputs", "MambaConvGrads", "MambaScanOutputs", "MambaScanGrads", "MambaNormGrads", "MambaRecurOutputs",
+           "MambaRecurGrads", "MambaAddNormOutputs", "MambaAddNormGrads", "mamba_conv_fwd",
            "mamba_conv_bwd", "mamba_conv_step", "mamba_scan_fwd", "mamba_scan_bwd", "mamba_scan_step", "mamba_norm_fwd",
-           "mamba_norm_bwd"]
+           "mamba_norm_bwd", "mamba_recur_fwd", "mamba_recur_bwd", "mamba_recur_step", "mamba_add_norm_fwd", "mamba_add_norm_bwd"]
 
 Tensor = torch.Tensor
 _F32 = torch.float32
@@ -67,6 +69,34 @@ class MambaNormGrads(NamedTuple):
     dweight: Tensor
     dbias: Optional[Tensor]
     dz: Optional[Tensor]
+
+
+class MambaRecurOutputs(NamedTuple):
+    out: Tensor
+    state: Optional[Tensor]
+
+
+class MambaRecurGrads(NamedTuple):
+    dx: Tensor
+    dr: Tensor
+    di: Tensor
+    ddecay: Tensor
+    dr_bias: Optional[Tensor]
+    di_bias: Optional[Tensor]
+    dz: Optional[Tensor]
+    dinitial_state: Optional[Tensor]
+
+
+class MambaAddNormOutputs(NamedTuple):
+    out: Tensor
+    sum: Tensor
+    scale: Optional[Tensor]
+
+
+class MambaAddNormGrads(NamedTuple):
+    dx: Tensor
+    dresidual: Optional[Tensor]
+    dweight: Tensor
 
 
 # ---------------------------------------------------------------- checks
@@ -316,20 +346,21 @@ def mamba_conv_bwd(dout, x, weight, bias=None, initial_state=None, dstate=None, 
 
 
 def _check_pool(state, inner, dtype, indices, n, device):
-    """A pool of states [slots, ...]: dense inside a slot, slots that do not overlap, updated in place."""
+    """A pool of states [slots, *inner], one or two inner axes: dense inside a slot, slots that do not overlap, updated in
+    place."""
     if state is None:
         _required(state=state)
     shape = state.shape
-    if len(shape) != 3 or shape[1] != inner[0] or shape[2] != inner[1]:
+    if shape[1:] != inner:
         raise ValueError(f"state must have shape [slots, {', '.join(map(str, inner))}], got {list(shape)}")
-    slots, size = shape[0], inner[0] * inner[1]
+    slots, size = shape[0], inner[0] * inner[-1] if len(inner) == 2 else inner[0]
     if state.dtype != dtype or state.device != device:
         _check_tensor("state", state, shape, dtype, device)
     if slots < 1:
         raise ValueError("state must have at least one slot")
     stride = size
     if not state.is_contiguous():
-        if (inner[1] != 1 and state.stride(2) != 1) or (inner[0] != 1 and state.stride(1) != inner[1]):
+        if (inner[-1] != 1 and state.stride(-1) != 1) or (len(inner) == 2 and inner[0] != 1 and state.stride(1) != inner[1]):
             raise ValueError("state must be dense inside a slot: it is updated in place")
         stride = state.stride(0) if slots > 1 else size
         if stride < size:
@@ -529,3 +560,210 @@ def mamba_norm_bwd(dout, x, weight, bias=None, z=None, *, groups: int = 1, eps: 
                              int(bool(center)), int(gate == "after"), silu, eps, 0, _ptr(dr), _ptr(rows), _ptr(zr), _ptr(weight),
                              _ptr(bias), _ptr(dx), _ptr(dz), _ptr(dweight), _ptr(dbias)), dev, workspace)
     return MambaNormGrads(dx, dweight, dbias, dz)
+
+
+# ---------------------------------------------------------------- gated linear recurrence
+def _check_recur(x, r, i, decay, r_bias, i_bias, z, rate, dev):
+    """The tensors with dense inner axes, parameters contiguous."""
+    if r is None or i is None or decay is None:
+        _required(r=r, i=i, decay=decay)
+    if not 0 <= rate <= 3e38:
+        raise ValueError(f"rate must be finite and not negative, got {rate}")
+    shape, dtype = x.shape, x.dtype
+    width = shape[-1:]
+    return ((_dense_inner(x, 1), _data("r", r, shape, dtype, dev), _data("i", i, shape, dtype, dev), _data("z", z, shape, dtype, dev)),
+            (_param("decay", decay, width, _F32, dev), _param("r_bias", r_bias, width, _F32, dev), _param("i_bias", i_bias, width, _F32, dev)))
+
+
+def mamba_recur_fwd(x, r, i, decay, r_bias=None, i_bias=None, z=None, initial_state=None, cu_seqlens=None, *, rate: float = 8.0,
+                    return_state: bool = False, out: Optional[Tensor] = None, workspace: Optional[Tensor] = None) -> MambaRecurOutputs:
+    """Gated linear recurrence, one state a channel:
+
+        a[t] = exp(-rate softplus(decay) sigmoid(r[t] + r_bias))
+        h[t] = a[t] h[t-1] + sqrt(1 - a[t]^2) sigmoid(i[t] + i_bias) x[t]
+        out[t] = h[t] * silu(z[t])
+
+    from ``initial_state`` (zeros without it); biases and gate are left out where r_bias, i_bias, z are None.
+
+    x, r, i, z, out [B, S, D] or packed [T, D]; decay, r_bias, i_bias [D] float32; initial_state and the returned
+    ``state`` (with ``return_state``; the last h) [n, D] float32, as ``mamba_recur_step`` takes them. Tokens
+    behind the last sequence: rows of ``out`` are left as they were when the caller gives it, else zero."""
+    dev = _device("mamba_recur_fwd", "x", x)
+    code = _data_dtype("x", x)
+    n, S, lead = _sequences("x", x, cu_seqlens, 1)
+    D = x.shape[-1]
+    (x, r, i, z), (decay, r_bias, i_bias) = _check_recur(x, r, i, decay, r_bias, i_bias, z, rate, dev)
+    cu, initial_state = _cu(cu_seqlens, dev), _param("initial_state", initial_state, (n, D), _F32, dev)
+    res = _out(out, x, x=x, r=r, i=i, decay=decay, r_bias=r_bias, i_bias=i_bias, z=z, initial_state=initial_state, cu_seqlens=cu)
+    if workspace is not None:
+        _apart("workspace", workspace, x=x, r=r, i=i, decay=decay, r_bias=r_bias, i_bias=i_bias, z=z, initial_state=initial_state,
+               cu_seqlens=cu, out=out)
+    state = decay.new_empty((n, D)) if return_state else None
+    packed = cu is not None
+    _call("mamba_recur_fwd", (n, S, D, code, int(out is None), rate, 0, _ptr(cu), *_rows(x, packed), *_rows(r, packed), *_rows(i, packed),
+                              *_rows(z, packed), _ptr(decay), _ptr(r_bias), _ptr(i_bias), _ptr(initial_state), _ptr(res), _ptr(state)), dev, workspace)
+    return MambaRecurOutputs(res, state)
+
+
+def mamba_recur_bwd(dout, x, r, i, decay, r_bias=None, i_bias=None, z=None, initial_state=None, dstate=None, cu_seqlens=None, *,
+                    rate: float = 8.0, workspace: Optional[Tensor] = None) -> MambaRecurGrads:
+    """Gradients of ``sum(out * dout) + sum(state * dstate)`` for the arguments of ``mamba_recur_fwd``: dx, dr, di, dz in
+    the data dtype, ddecay, dr_bias, di_bias, dinitial_state float32; those of absent inputs are None. dout like x,
+    dstate like initial_state. The states are recomputed, so nothing is kept from the forward call. Token
+    gradients are zero behind the last sequence."""
+    dev = _device("mamba_recur_bwd", "x", x)
+    code = _data_dtype("x", x)
+    n, S, lead = _sequences("x", x, cu_seqlens, 1)
+    D = x.shape[-1]
+    (x, r, i, z), (decay, r_bias, i_bias) = _check_recur(x, r, i, decay, r_bias, i_bias, z, rate, dev)
+    if dout is None:
+        _required(dout=dout)
+    dout = _data("dout", dout, x.shape, x.dtype, dev)
+    initial_state = _param("initial_state", initial_state, (n, D), _F32, dev)
+    cu, dstate = _cu(cu_seqlens, dev), _param("dstate", dstate, (n, D), _F32, dev)
+    if workspace is not None:
+        _apart("workspace", workspace, dout=dout, x=x, r=r, i=i, decay=decay, r_bias=r_bias, i_bias=i_bias, z=z, initial_state=initial_state,
+               dstate=dstate, cu_seqlens=cu)
+    packed = cu is not None
+    g = MambaRecurGrads(*(None if t is None else _new_like(t) for t in (x, r, i, decay, r_bias, i_bias, z, initial_state)))
+    _call("mamba_recur_bwd", (n, S, D, code, 0, rate, 0, _ptr(cu), *_rows(dout, packed), *_rows(x, packed), *_rows(r, packed), *_rows(i, packed),
+                              *_rows(z, packed), _ptr(decay), _ptr(r_bias), _ptr(i_bias), _ptr(initial_state), _ptr(dstate), _ptr(g.dx), _ptr(g.dr),
+                              _ptr(g.di), _ptr(g.dz), _ptr(g.ddecay), _ptr(g.dr_bias), _ptr(g.di_bias), _ptr(g.dinitial_state)), dev, workspace)
+    return g
+
+
+def mamba_recur_step(x, r, i, state, decay, r_bias=None, i_bias=None, z=None, state_indices=None, *, rate: float = 8.0,
+                     out: Optional[Tensor] = None) -> Tensor:
+    """One token of ``mamba_recur_fwd`` for each of n rows: x, r, i, z, out [n, D]; ``state`` [slots, D] float32 is
+    updated in place. Slots and ``state_indices`` as for ``mamba_conv_step``."""
+    dev = _device("mamba_recur_step", "x", x)
+    code = _data_dtype("x", x)
+    shape = x.shape
+    if len(shape) != 2 or 0 in shape:
+        raise ValueError(f"x must have shape [n, D] and not be empty, got {list(shape)}")
+    n, D = shape
+    (x, r, i, z), (decay, r_bias, i_bias) = _check_recur(x, r, i, decay, r_bias, i_bias, z, rate, dev)
+    slots, stride, idx = _check_pool(state, (D,), _F32, state_indices, n, dev)
+    _apart("state", state, x=x, r=r, i=i, z=z, decay=decay, r_bias=r_bias, i_bias=i_bias, state_indices=idx)
+    res = _out(out, x, x=x, r=r, i=i, z=z, decay=decay, r_bias=r_bias, i_bias=i_bias, state=state, state_indices=idx)
+    _call("mamba_recur_step", (n, D, slots, stride, code, 0, rate, 0, x.data_ptr(), x.stride(0), 0, r.data_ptr(), r.stride(0), 0,
+                               i.data_ptr(), i.stride(0), 0, *(_NO_ROWS if z is None else (z.data_ptr(), z.stride(0), 0)),
+                               decay.data_ptr(), _ptr(r_bias), _ptr(i_bias), state.data_ptr(), _ptr(idx), res.data_ptr()), dev)
+    return res
+
+
+# ---------------------------------------------------------------- residual addition and norm
+_OUT_KINDS = {torch.float8_e4m3fn: 1, torch.int8: 2}
+_BLOCKS = (32, 64, 128, 256)
+
+
+def _check_stream(name, x, dtype):
+    """The stream's type: the data's, or float32."""
+    if dtype != x and dtype != _F32:
+        raise TypeError(f"{name} must be {x} or torch.float32, got {dtype}")
+    return dtype
+
+
+def _check_add_norm(x, weight, eps, dropout, seed, dev):
+    """Columns, the share dropped of 65536, its seed, the weight."""
+    if weight is None:
+        _required(weight=weight)
+    if x.dim() < 1 or x.numel() == 0:
+        raise ValueError(f"x must have shape [..., D] and not be empty, got {list(x.shape)}")
+    D = x.shape[-1]
+    if D > 16384:
+        raise NotImplementedError(f"mamba_add_norm supports at most 16384 channels, got {D}")
+    if not eps >= 0:
+        raise ValueError(f"eps must not be negative, got {eps}")
+    if not 0 <= dropout < 1:
+        raise ValueError(f"dropout must be in [0, 1), got {dropout}")
+    drop = min(int(dropout * 65536 + 0.5), 65535)
+    if drop:
+        if seed is None:
+            raise ValueError("dropout needs a seed")
+        seed = _param("seed", seed, (2,), torch.int64, dev)
+    else:
+        seed = None
+    return D, drop, seed, _param("weight", weight, (D,), _F32, dev)
+
+
+def mamba_add_norm_fwd(x, weight, residual=None, *, eps: float = 1e-5, dropout: float = 0.0, seed: Optional[Tensor] = None,
+                       sum_dtype: Optional[torch.dtype] = None, out_dtype: Optional[torch.dtype] = None, block: Optional[int] = None,
+                       out: Optional[Tensor] = None) -> MambaAddNormOutputs:
+    """The residual stream between two blocks: ``sum`` = v = dropout(x) + residual (or dropout(x)), and
+
+        out = v / sqrt(mean(v^2) + eps) * weight
+
+    over the last axis, from v before it is rounded to ``sum``. x, residual [..., D], D at most 16384; weight [D] float32.
+    The stream (residual and sum) has x's dtype or float32: that of ``residual``, or ``sum_dtype`` without it. Where
+    nothing is added, dropped or converted, ``sum`` is x itself.
+
+    ``dropout`` (a share, taken to the nearest of 65536 parts) sets elements to zero and divides the others by 1 - dropout; which
+    ones follows from ``seed`` [2] int64 on the device (key, offset) and an element's place, by the counter-based generator
+    that ``include/mamba_layer.h`` describes, and ``mamba_add_norm_bwd`` draws the same again: no mask is stored. A program
+    changes the seed for every call, in a captured one between replays.
+
+    ``out_dtype`` torch.float8_e4m3fn or torch.int8 gives ``out`` in 8 bits with ``scale`` float32 [..., ceil(D / block)], out's
+    value times its scale for every ``block`` (32, 64, 128, 256) columns, or [..., 1] for the row without ``block``: largest
+    magnitude / 448 or 127, rounded to nearest. A block with a value that is not finite has the scale NaN."""
+    dev = _device("mamba_add_norm_fwd", "x", x)
+    code = _data_dtype("x", x)
+    D, drop, seed, weight = _check_add_norm(x, weight, eps, dropout, seed, dev)
+    dtype = x.dtype
+    if residual is not None:
+        stream = _check_stream("the dtype of residual", dtype, residual.dtype)
+        if sum_dtype is not None and sum_dtype != stream:
+            raise TypeError(f"sum_dtype must be that of residual, {stream}, got {sum_dtype}")
+        _fits("residual", residual, x.shape, stream, dev)
+        rr = _row_view(residual, D)
+    else:
+        stream, rr = dtype if sum_dtype is None else _check_stream("sum_dtype", dtype, sum_dtype), None
+    kind = 0
+    if out_dtype is not None and out_dtype != dtype:
+        kind = _OUT_KINDS.get(out_dtype)
+        if kind is None:
+            raise TypeError(f"out_dtype must be {dtype}, torch.float8_e4m3fn or torch.int8, got {out_dtype}")
+    if block is not None and (not kind or block not in _BLOCKS):
+        raise ValueError(f"block must be one of {_BLOCKS}, with an 8-bit out_dtype, got {block!r}" if kind else "block needs an 8-bit out_dtype")
+    rows = _row_view(x, D)
+    if out is None:
+        res = torch.empty(x.shape, dtype=out_dtype if kind else dtype, device=dev)
+    else:
+        _check_output("out", out, x.shape, out_dtype if kind else dtype, dev)
+        _apart("out", out, x=rows, residual=rr, weight=weight, seed=seed)
+        res = out
+    kept = residual is None and not drop and stream == dtype
+    total = x if kept else torch.empty(x.shape, dtype=stream, device=dev)
+    scale = torch.empty((*x.shape[:-1], -(-D // block) if block else 1), dtype=_F32, device=dev) if kind else None
+    _call("mamba_add_norm_fwd", (rows.shape[0], D, rows.stride(0), 0 if rr is None else rr.stride(0), code, int(stream == _F32), kind, block or 0,
+                                 drop, eps, rows.data_ptr(), _ptr(rr), _ptr(seed), weight.data_ptr(), 0 if kept else total.data_ptr(), res.data_ptr(),
+                                 _ptr(scale)), dev)
+    return MambaAddNormOutputs(res, total, scale)
+
+
+def mamba_add_norm_bwd(dout, sum, weight, dsum=None, *, eps: float = 1e-5, dropout: float = 0.0, seed: Optional[Tensor] = None,
+                       residual: bool = True, workspace: Optional[Tensor] = None) -> MambaAddNormGrads:
+    """Gradients of ``sum(out * dout) + sum(sum * dsum)`` for the arguments of ``mamba_add_norm_fwd``, from the ``sum`` that it
+    returned: dx in dout's dtype (which x had), dresidual in that of sum, dweight float32. dout [..., D]; sum, dsum like it, in its
+    dtype or float32. Without dropout and with one dtype, dresidual is dx, the same tensor; with ``residual`` false (nothing
+    was added) it is None. The statistics are recomputed, and dropped elements drawn again from ``seed``."""
+    if sum is None:
+        _required(sum=sum)
+    dev = _device("mamba_add_norm_bwd", "dout", dout)
+    code = _data_dtype("dout", dout)
+    D, drop, seed, weight = _check_add_norm(dout, weight, eps, dropout, seed, dev)
+    stream = _check_stream("the dtype of sum", dout.dtype, sum.dtype)
+    _fits("sum", sum, dout.shape, stream, dev)
+    gr, vr, sr = _row_view(dout, D), _row_view(sum, D), None
+    if dsum is not None:
+        _fits("dsum", dsum, dout.shape, stream, dev)
+        sr = _row_view(dsum, D)
+    if workspace is not None:
+        _apart("workspace", workspace, dout=gr, sum=vr, dsum=sr, weight=weight, seed=seed)
+    dx, dweight = torch.empty(dout.shape, dtype=dout.dtype, device=dev), torch.empty_like(weight)
+    same = not drop and stream == dout.dtype
+    dres = None if not residual else dx if same else torch.empty(dout.shape, dtype=stream, device=dev)
+    _call("mamba_add_norm_bwd", (gr.shape[0], D, gr.stride(0), vr.stride(0), 0 if sr is None else sr.stride(0), code, int(stream == _F32), drop, eps,
+                                 gr.data_ptr(), vr.data_ptr(), _ptr(sr), _ptr(seed), weight.data_ptr(), dx.data_ptr(),
+                                 0 if same else _ptr(dres), dweight.data_ptr()), dev, workspace)
+    return MambaAddNormGrads(dx, dres, dweight)
