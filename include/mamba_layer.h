@@ -233,8 +233,10 @@ mimo_status mamba_norm_bwd(const mamba_norm_bwd_args *args, void *stream);
  * below -87 counts as none (its softplus is below fp32's range): nothing is forgotten or
  * enters.
  *   x, r, i, z, out [.., D]; decay, r_bias, i_bias [D] (the biases optional); states
- *   [n, D] fp32. rate is not negative.
+ *   [n, D] fp32. rate is not negative. Token strides: 0 to MAMBA_RECUR_MAX_STRIDE elements
+ *   (forward and backward).
  */
+#define MAMBA_RECUR_MAX_STRIDE (1 << 26)
 typedef struct mamba_recur_fwd_args {
     int64_t n, S, D;
     int32_t dtype, zero_tail;

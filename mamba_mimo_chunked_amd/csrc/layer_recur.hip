@@ -1,6 +1,4 @@
-// Gated linear recurrence, forward pass and step of one token (formulas, gates, carry: layer_recur.hpp).
-#include <initializer_list>
-
+// Gated linear recurrence, forward pass and step of one token (formulas, gates: layer_recur.hpp).
 #include "layer_recur.hpp"
 
 namespace mimo {
@@ -8,124 +6,163 @@ namespace layer {
 namespace {
 
 constexpr int WAVES = 8;            // of a block
-constexpr int tile_tokens(int DT) { return DT == F32 ? 8 : 16; }    // of a wave
+constexpr int TT = 16;              // tokens of a wave
+constexpr int GROUP = 32, EACH = GROUP / WAVES;     // chunks of a group, and of a wave's share of it
+constexpr int POLLS = 1 << 18;      // a wait's limit: some tenths of a second
+constexpr int LINE = 64;            // counters lie this far apart: neighbours would wait for each other
+typedef unsigned long long word;
 
-// A block takes one chunk of 64 VC channels, WAVES * TT tokens a round, and the next round's rows are asked for during a
-// round. AGG: the chunk's last state from zero and its product of a; else the outputs.
-template <int DT, int VC, bool AGG> __global__ __launch_bounds__(64 * WAVES) void k_recur(RecurParams p) {
+__device__ __forceinline__ word look(const word* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ void tell(word* p, float lo, unsigned hi) {
+    __hip_atomic_store(p, (word)hi << 32 | __float_as_uint(lo), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ bool there(word w) { return (unsigned)(w >> 32) != ~0u; }
+__device__ __forceinline__ float low(word w) { return __uint_as_float((unsigned)w); }
+__device__ __forceinline__ float high(word w) { return __uint_as_float((unsigned)(w >> 32)); }
+
+// Before a call of several chunks: no step is told yet, no chunk taken.
+__global__ __launch_bounds__(256) void k_recur_clear(RecurParams p) {
+    const long step = (long)gridDim.x * 256, at = (long)blockIdx.x * 256 + threadIdx.x;
+    for (long k = at; k < p.words; k += step) p.told[k] = ~word(0);
+    for (long k = at; k <= p.tiles * LINE; k += step) p.taken[k] = 0;
+}
+
+// The outputs, in one pass over the inputs. A block takes one chunk of WAVES * TT tokens by 64 channels, all of it in registers:
+// it joins its tokens' steps, tells the joined step (last state from zero, product of a; one word of 64 bits a channel) to the
+// chunks behind it, joins those of the chunks in front, and walks its tokens from there. The chunks of a sequence are joined in
+// groups of GROUP: a chunk looks at those of its group, and at the state that the last chunk of the group in front tells. The order in
+// which steps are joined is fixed, so equal inputs give equal bits.
+// Every wait ends: a block takes the next chunk of its tile from a counter, so that whatever it waits for belongs to a block that runs
+// already, and a chunk's step is told before its block waits, a group's state after waiting for lower chunks alone. cu_seqlens that
+// decrease may leave a word that nobody tells: POLLS ends the first such wait, its mark behind the counters all others, and outputs
+// are NaN. A word holds value and mark, so no fence is needed.
+template <int DT, bool GATE> __global__ __launch_bounds__(64 * WAVES, 6) void k_recur(RecurParams p) {
     typedef raw_t<DT> raw;
-    constexpr int TT = tile_tokens(DT), ROUND = WAVES * TT;
-    __shared__ float s_h[2][WAVES][64 * VC], s_p[2][WAVES][64 * VC];
-    const unsigned slot = blockIdx.x / p.tiles, tile = blockIdx.x - slot * p.tiles;
+    constexpr int CH = WAVES * TT;
+    __shared__ float s_h[WAVES][64], s_p[WAVES][64], s_gh[WAVES][64], s_gp[WAVES][64];
+    __shared__ unsigned s_slot;
+    const unsigned tile = blockIdx.x % p.tiles;
+    unsigned slot = blockIdx.x / p.tiles;
+    if (p.chunked) {
+        if (threadIdx.x == 0) s_slot = __hip_atomic_fetch_add(p.taken + tile * LINE, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        slot = __builtin_amdgcn_readfirstlane(s_slot);
+    }
     const Place pl = place(p.q, slot);
     if (!pl.ok) return;
-    const int t0 = pl.j * p.q.CH, t1 = min(t0 + p.q.CH, pl.len);
-    if (AGG && (pl.i == p.q.n || t1 == pl.len)) return;
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const unsigned vec = tile * 64 + lane;
-    const bool act = vec < (unsigned)p.nvec;
-    const unsigned d = act ? vec * VC : 0;
+    const int t0 = pl.j * CH, t1 = min(t0 + CH, pl.len);
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), tw = t0 + w * TT, left = t1 - tw;
+    const bool act = tile * 64 + lane < (unsigned)p.D;
+    const unsigned d = act ? tile * 64 + lane : (unsigned)p.D - 1, db = d * sizeof(raw);     // of the same tile: its words are told
     const long D = p.D;
-    raw* out = static_cast<raw*>(p.out) + recur_row(p.q, pl) * D;
-    if (!AGG && pl.i == p.q.n) {    // behind the last sequence
-        const float zero[VC] = {};
+    const auto out = buffer_of(static_cast<raw*>(p.out) + (recur_row(p.q, pl) + tw) * D);
+    const unsigned step = (unsigned)D * sizeof(raw);
+    if (pl.i == p.q.n) {            // behind the last sequence
+        const float zero[1] = {};
         if (p.zero_tail && act)
-            for (int t = t0 + w; t < t1; t += WAVES) store<DT, VC>(out + t * D + d, zero);
+            for (int k = 0; k < min(left, TT); ++k) store_at<DT, 1>(out, db, k * step, zero);
         return;
     }
-    const raw *x = at<DT>(p.x, pl), *r = at<DT>(p.r, pl), *in = at<DT>(p.i, pl);
-    const raw* z = !AGG && p.has_z ? at<DT>(p.z, pl) : nullptr;
-    const Gates<VC> gates(p, d);
-    float h[VC], all[VC];
-    const float* from = AGG ? nullptr : p.chunked ? p.agg_h + slot * D : p.init ? p.init + pl.i * D : nullptr;
-#pragma unroll
-    for (int v = 0; v < VC; ++v) {
-        h[v] = from ? from[d + v] : 0.f;
-        all[v] = 1.f;
-    }
-    RowsOf<DT, VC, TT> rx, rr, ri, rz;
-    auto fetch = [&](int t) {
-        t += w * TT;
-        rx.fetch(x, p.x.ts, t, t1 - 1, d);
-        rr.fetch(r, p.r.ts, t, t1 - 1, d);
-        ri.fetch(in, p.i.ts, t, t1 - 1, d);
-    };
+    const int group = pl.j / GROUP;
+    float h = group == 0 && p.init ? p.init[pl.i * D + d] : 0.f;
     if (t0 < t1) {
-        fetch(t0);
-        if (z) rz.fetch(z, p.z.ts, t0 + w * TT, t1 - 1, d);
-    }
-    int buf = 0;
-    for (int tt = t0; tt < t1; tt += ROUND, buf ^= 1) {
-        const int tw = tt + w * TT;
-        float a[TT][VC], b[TT][VC], fold[VC], prod[VC];
+        RowsOf<DT, 1, TT> rx, rr, ri, rz;
+        rx.place(p.x, pl, p.D, tw, t1), rr.place(p.r, pl, p.D, tw, t1), ri.place(p.i, pl, p.D, tw, t1);
+        if constexpr (GATE) rz.place(p.z, pl, p.D, tw, t1);
+#pragma unroll
+        for (int k = 0; k < TT; ++k) rx.fetch(k, db), rr.fetch(k, db), ri.fetch(k, db);
+        if constexpr (GATE) {
+#pragma unroll
+            for (int k = 0; k < TT; ++k) rz.fetch(k, db);
+        }
+        const Gates<1> gates(p, d);
+        float a[TT], b[TT], fold = 0.f, prod = 1.f;
 #pragma unroll
         for (int k = 0; k < TT; ++k) {
-            float fx[VC], fr[VC], fi[VC];
-            unpack<DT, VC>(rx.t[k], fx);
-            unpack<DT, VC>(rr.t[k], fr);
-            unpack<DT, VC>(ri.t[k], fi);
-#pragma unroll
-            for (int v = 0; v < VC; ++v) {
-                float e2;
-                keep_and_enter(gates.speed[v] * sigmoid(fr[v] + gates.rb[v]), a[k][v], e2);
-                b[k][v] = root(e2) * (sigmoid(fi[v] + gates.ib[v]) * fx[v]);
-            }
+            float e2;
+            keep_and_enter(speed_of(gates, 0, k, left) * gates.open(to_f<DT>(rr.t[k].v[0]), gates.rb[0]), a[k], e2);
+            b[k] = root(e2) * (gates.open(to_f<DT>(ri.t[k].v[0]), gates.ib[0]) * to_f<DT>(rx.t[k].v[0]));
         }
-        if (tw + TT > t1) {         // tokens behind the chunk change nothing
 #pragma unroll
-            for (int k = 0; k < TT; ++k)
-                if (tw + k >= t1) {
+        for (int k = 0; k < TT; ++k) {
+            fold = __builtin_fmaf(a[k], fold, b[k]);
+            prod *= a[k];
+        }
+        s_h[w][lane] = fold;
+        s_p[w][lane] = prod;
+        __syncthreads();
+        const bool last = t1 == pl.len, closes = !last && pl.j % GROUP == GROUP - 1;
+        word* const ends = p.told + p.slots * D;
+        if (w == 0 && !last && !closes) {
+            float hh = 0.f, pp = 1.f;
 #pragma unroll
-                    for (int v = 0; v < VC; ++v) a[k][v] = 1.f, b[k][v] = 0.f;
+            for (int o = 0; o < WAVES; ++o) {
+                hh = __builtin_fmaf(s_p[o][lane], hh, s_h[o][lane]);
+                pp *= s_p[o][lane];
+            }
+            // a NaN that came in must not look like a word that is not there yet
+            if (act) tell(p.told + slot * D + d, hh, pp == pp ? __float_as_uint(pp) : 0x7fc00000u);
+        }
+        if (pl.j > 0) {
+            // this wave's share of the group's chunks in front, and in wave 0 the state that enters the group
+            const int first = group * GROUP + w * EACH, before = pl.j - first;      // how many of them: up to EACH
+            const word* from = p.told + ((long)slot - before) * D + d;
+            const word* base = ends + (long)((slot - pl.j + group * GROUP - 1) / GROUP) * D + d;
+            const bool wants = group > 0 && w == 0;
+            word told[EACH], enters;
+            for (int poll = 0;; ++poll) {
+                bool all = true;
+#pragma unroll
+                for (int e = 0; e < EACH; ++e)
+                    if (e < before) told[e] = look(from + e * D);
+                if (wants) enters = look(base);
+#pragma unroll
+                for (int e = 0; e < EACH; ++e)
+                    if (e < before) all = all && there(told[e]);
+                if (wants) all = all && there(enters);
+                if (__all(all) || __hip_atomic_load(p.taken + p.tiles * LINE, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) break;
+                if (poll == POLLS) __hip_atomic_store(p.taken + p.tiles * LINE, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                __builtin_amdgcn_s_sleep(4);
+            }
+            if (wants) h = there(enters) ? low(enters) : __builtin_nanf("");
+            float gh = w == 0 ? h : 0.f, gp = 1.f;
+#pragma unroll
+            for (int e = 0; e < EACH; ++e)
+                if (e < before) {
+                    gh = __builtin_fmaf(high(told[e]), gh, low(told[e]));
+                    gp *= high(told[e]);
                 }
+            s_gh[w][lane] = gh;
+            s_gp[w][lane] = gp;
+            __syncthreads();
+            h = s_gh[0][lane];      // from the state that enters the group
+#pragma unroll
+            for (int o = 1; o < WAVES; ++o) h = __builtin_fmaf(s_gp[o][lane], h, s_gh[o][lane]);
         }
-        if (tt + ROUND < t1) fetch(tt + ROUND);
+        float enter = 0.f;
 #pragma unroll
-        for (int v = 0; v < VC; ++v) fold[v] = 0.f, prod[v] = 1.f;
-#pragma unroll
-        for (int k = 0; k < TT; ++k)
-#pragma unroll
-            for (int v = 0; v < VC; ++v) {
-                fold[v] = __builtin_fmaf(a[k][v], fold[v], b[k][v]);
-                prod[v] *= a[k][v];
-            }
-#pragma unroll
-        for (int v = 0; v < VC; ++v) {
-            s_h[buf][w][lane * VC + v] = fold[v];
-            s_p[buf][w][lane * VC + v] = prod[v];
+        for (int o = 0; o < WAVES; ++o) {
+            if (o == w) enter = h;
+            h = __builtin_fmaf(s_p[o][lane], h, s_h[o][lane]);
         }
-        __syncthreads();            // one a round: the next one writes the other half
-        float enter[VC] = {};
-#pragma unroll
-        for (int o = 0; o < WAVES; ++o)
-#pragma unroll
-            for (int v = 0; v < VC; ++v) {
-                if (o == w) enter[v] = h[v];
-                const float q = s_p[buf][o][lane * VC + v];
-                h[v] = __builtin_fmaf(q, h[v], s_h[buf][o][lane * VC + v]);
-                if (AGG) all[v] *= q;
-            }
-        if constexpr (!AGG) {
+        if (closes && w == 0 && act) tell(ends + (long)(slot / GROUP) * D + d, h, 0u);
+        unsigned row = 0;
+        if (act) {
 #pragma unroll
             for (int k = 0; k < TT; ++k) {
-                float y[VC], fz[VC];
-                if (z) unpack<DT, VC>(rz.t[k], fz);
-#pragma unroll
-                for (int v = 0; v < VC; ++v) {
-                    enter[v] = __builtin_fmaf(a[k][v], enter[v], b[k][v]);
-                    y[v] = z ? enter[v] * (fz[v] * sigmoid(fz[v])) : enter[v];
+                enter = __builtin_fmaf(a[k], enter, b[k]);
+                float y[1] = {enter};
+                if constexpr (GATE) {
+                    const float z = to_f<DT>(rz.t[k].v[0]);
+                    y[0] *= z * sigmoid(z);
                 }
-                if (act && tw + k < t1) store<DT, VC>(out + (tw + k) * D + d, y);
+                if (k < left) store_at<DT, 1>(out, db, row, y);
+                row += step;
+                __builtin_amdgcn_sched_barrier(0);
             }
-            if (z && tt + ROUND < t1) rz.fetch(z, p.z.ts, tw + ROUND, t1 - 1, d);
         }
     }
-    if (!act || w != 0) return;
-#pragma unroll
-    for (int v = 0; v < VC; ++v) {
-        if (AGG) p.agg_h[slot * D + d + v] = h[v], p.agg_p[slot * D + d + v] = all[v];
-        else if (p.state && t1 == pl.len) p.state[pl.i * D + d + v] = h[v];
-    }
+    if (act && w == 0 && p.state && t1 == pl.len) p.state[pl.i * D + d] = h;
 }
 
 struct StepParams {
@@ -175,8 +212,8 @@ template <int DT, int VC> __global__ __launch_bounds__(256) void k_recur_step(St
 #pragma unroll
         for (int v = 0; v < VC; ++v) {
             float a, e2;
-            keep_and_enter(gates.speed[v] * sigmoid(fr[v] + gates.rb[v]), a, e2);
-            h[v] = __builtin_fmaf(a, h[v], root(e2) * (sigmoid(fi[v] + gates.ib[v]) * fx[v]));
+            keep_and_enter(gates.speed[v] * gates.open(fr[v], gates.rb[v]), a, e2);
+            h[v] = __builtin_fmaf(a, h[v], root(e2) * (gates.open(fi[v], gates.ib[v]) * fx[v]));
             y[v] = p.has_z ? h[v] * (fz[v] * sigmoid(fz[v])) : h[v];
         }
         if (act) store<DT, VC>(out + (long)row * p.D + d, y);
@@ -192,41 +229,42 @@ template <int DT, int VC> __global__ __launch_bounds__(256) void k_recur_step(St
 
 struct FwdPlan {
     Seqs q;
-    int VC;
     unsigned tiles;
     long slots;
     bool chunked;
-    size_t part, bytes;             // of one aggregate, in all
+    long words;
+    size_t told, bytes;             // of the words, in all
 };
 
 mimo_status plan_fwd(const mamba_recur_fwd_args* a, FwdPlan* pl) {
     if (a == nullptr) return bad("args must not be NULL");
-    const mimo_status s = check_recur(a->n, a->S, a->D, a->dtype, a->rate);
-    if (s != MIMO_OK) return s;
+    mimo_status s = check_recur(a->n, a->S, a->D, a->dtype, a->rate);
+    if (s != MIMO_OK || (s = check_strides({&a->x, &a->r, &a->i, &a->z})) != MIMO_OK) return s;
     const bool packed = a->cu_seqlens != nullptr;
-    pl->VC = channels_of(a->D, a->dtype, packed, {&a->x, &a->r, &a->i, &a->z}, {a->out});
-    pl->tiles = (unsigned)((a->D + 64 * pl->VC - 1) / (64 * pl->VC));
-    const int64_t round = WAVES * tile_tokens(a->dtype), T = packed ? a->S : a->n * a->S;
-    int64_t CH = (T * pl->tiles / 512 + round - 1) / round * round;
-    CH = CH < round ? round : CH > 4096 ? 4096 : CH;
-    pl->q = Seqs{a->cu_seqlens, (int)a->n, (int)a->S, (int)CH, (int)((a->S + CH - 1) / CH)};
+    pl->tiles = (unsigned)((a->D + 63) / 64);
+    const int CH = WAVES * TT;
+    pl->q = Seqs{a->cu_seqlens, (int)a->n, (int)a->S, CH, (int)((a->S + CH - 1) / CH)};
     pl->slots = slots_of(pl->q);
     if (!grid_fits(pl->slots * pl->tiles, 64 * WAVES)) return unsupported("the call needs more than 2^32 threads");
     pl->chunked = a->S > CH;
-    pl->part = up256((size_t)pl->slots * a->D * sizeof(float));
-    pl->bytes = pl->chunked ? 2 * pl->part : 0;
+    // a word of every chunk and of every group's end
+    pl->words = pl->chunked ? (pl->slots + pl->slots / GROUP + 1) * (long)a->D : 0;
+    pl->told = up256((size_t)pl->words * sizeof(word));
+    pl->bytes = pl->chunked ? pl->told + up256((pl->tiles * LINE + 1) * sizeof(unsigned)) : 0;
     return MIMO_OK;
 }
 
-template <int DT, int VC> mimo_status run_fwd(const RecurParams& p, hipStream_t st) {
-    const dim3 grid((unsigned)(p.slots * p.tiles));
+template <int DT, bool GATE> mimo_status run_fwd(const RecurParams& p, hipStream_t st) {
     if (p.chunked) {
-        mimo_status s = launch(&k_recur<DT, VC, true>, grid, 64 * WAVES, 0, st, p);
-        if (s != MIMO_OK) return s;
-        s = launch_recur_carry<false>(p, st);
+        const long blocks = (p.words + 1023) / 1024;
+        const mimo_status s = launch(&k_recur_clear, dim3((unsigned)(blocks < 1024 ? blocks : 1024)), 256, 0, st, p);
         if (s != MIMO_OK) return s;
     }
-    return launch(&k_recur<DT, VC, false>, grid, 64 * WAVES, 0, st, p);
+    return launch(&k_recur<DT, GATE>, dim3((unsigned)(p.slots * p.tiles)), 64 * WAVES, 0, st, p);
+}
+
+template <int DT> mimo_status run_type(const RecurParams& p, hipStream_t st) {
+    return p.has_z ? run_fwd<DT, true>(p, st) : run_fwd<DT, false>(p, st);
 }
 
 }  // namespace
@@ -255,18 +293,17 @@ mimo_status mamba_recur_fwd(const mamba_recur_fwd_args* a, void* stream) {
     if ((s = check_workspace(a->workspace, a->workspace_bytes, pl.bytes)) != MIMO_OK) return s;
     const bool packed = a->cu_seqlens != nullptr;
     RecurParams p{};
-    p.q = pl.q, p.D = (int)a->D, p.nvec = p.D / pl.VC, p.tiles = pl.tiles, p.slots = pl.slots;
+    p.q = pl.q, p.D = (int)a->D, p.tiles = pl.tiles, p.slots = pl.slots;
     p.has_z = a->z.data != nullptr, p.zero_tail = a->zero_tail, p.chunked = pl.chunked, p.rate = a->rate;
     p.x = rows_of(a->x, packed), p.r = rows_of(a->r, packed), p.i = rows_of(a->i, packed), p.z = rows_of(a->z, packed);
     p.decay = a->decay, p.rb = a->r_bias, p.ib = a->i_bias, p.init = a->initial_state;
     p.out = a->out, p.state = a->state;
-    p.agg_h = static_cast<float*>(a->workspace);
-    p.agg_p = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + pl.part);
+    p.words = pl.words, p.told = static_cast<unsigned long long*>(a->workspace);
+    p.taken = reinterpret_cast<unsigned*>(static_cast<char*>(a->workspace) + pl.told);
     if ((s = require_gfx950()) != MIMO_OK) return s;
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    if (a->dtype == BF16) return pl.VC == 2 ? run_fwd<BF16, 2>(p, st) : run_fwd<BF16, 1>(p, st);
-    if (a->dtype == F16) return pl.VC == 2 ? run_fwd<F16, 2>(p, st) : run_fwd<F16, 1>(p, st);
-    return pl.VC == 2 ? run_fwd<F32, 2>(p, st) : run_fwd<F32, 1>(p, st);
+    if (a->dtype == BF16) return run_type<BF16>(p, st);
+    return a->dtype == F16 ? run_type<F16>(p, st) : run_type<F32>(p, st);
 }
 
 mimo_status mamba_recur_step(const mamba_recur_step_args* a, void* stream) {
@@ -289,7 +326,7 @@ mimo_status mamba_recur_step(const mamba_recur_step_args* a, void* stream) {
     auto go = [&](auto f) { return launch(f, grid, 256, 0, st, q); };
     if (a->dtype == BF16) return VC == 2 ? go(&k_recur_step<BF16, 2>) : go(&k_recur_step<BF16, 1>);
     if (a->dtype == F16) return VC == 2 ? go(&k_recur_step<F16, 2>) : go(&k_recur_step<F16, 1>);
-    return VC == 2 ? go(&k_recur_step<F32, 2>) : go(&k_recur_step<F32, 1>);
+    return go(&k_recur_step<F32, 1>);
 }
 
 }  // extern "C"

@@ -9,6 +9,8 @@
 // owns VC neighbouring channels, a wave TT neighbouring tokens, which it keeps in registers as (a, b); the waves' joined steps
 // meet in LDS, where each wave finds the state that enters its tokens.
 #pragma once
+#include <initializer_list>
+
 #include "layer.hpp"
 
 namespace mimo {
@@ -24,8 +26,12 @@ struct RecurParams {
     const float *init, *dstate;
     void* out;
     float* state;
-    float *agg_h, *agg_p, *agg_g;   // [slots][D]: a chunk's last state from zero, its product of a, the adjoint that leaves it to the left
+    // forward: what chunks tell those behind them, [slots and groups][D], and the chunks taken of each tile
+    unsigned long long* told;
+    unsigned* taken;
+    long words;
     // backward
+    float *agg_h, *agg_p, *agg_g;   // [slots][D]: a chunk's last state from zero, its product of a, the adjoint that leaves it to the left
     void *dx, *dr, *di, *dz;
     float *ddecay, *drb, *dib, *dinit;
     float* part;                    // [slots][3][D]
@@ -45,32 +51,87 @@ __device__ __forceinline__ void keep_and_enter(float l2, float& a, float& e2) {
     s = __builtin_fmaf(y, s, 1.f / 24.f);
     s = __builtin_fmaf(y, s, 1.f / 6.f);
     s = __builtin_fmaf(y, s, 0.5f);
-    s = __builtin_fmaf(y, s, 1.f);
-    e2 = y > -0.25f ? -y * s : __builtin_fmaf(-a, a, 1.f);
+    s = -y * __builtin_fmaf(y, s, 1.f);
+    asm("" : "+v"(s));      // both are computed: a branch for each value costs more than the series
+    e2 = y > -0.25f ? s : __builtin_fmaf(-a, a, 1.f);
 }
 __device__ __forceinline__ float root(float x) { return __builtin_amdgcn_sqrtf(x); }
 
-// a lane's parameters: -rate softplus(decay) log2(e), and the biases
+// a lane's parameters: -rate softplus(decay) log2(e), and the biases times -log2(e)
 template <int VC> struct Gates {
     float speed[VC], rb[VC], ib[VC];
+    // sigmoid(x + bias), in one multiply-add, 2^x, an addition and a reciprocal
+    __device__ __forceinline__ static float open(float x, float bias) {
+        return __builtin_amdgcn_rcpf(1.f + exp2_hw(__builtin_fmaf(x, -LOG2E, bias)));
+    }
     __device__ __forceinline__ Gates(const RecurParams& p, unsigned d) {
 #pragma unroll
         for (int v = 0; v < VC; ++v) {
             speed[v] = -p.rate * LOG2E * softplus(p.decay[d + v]);
-            rb[v] = p.rb ? p.rb[d + v] : 0.f;
-            ib[v] = p.ib ? p.ib[d + v] : 0.f;
+            rb[v] = p.rb ? -LOG2E * p.rb[d + v] : 0.f;
+            ib[v] = p.ib ? -LOG2E * p.ib[d + v] : 0.f;
         }
     }
 };
 
-// TT rows from t0 on (the last one again where they end before), at a scalar base and a lane's offset
+// Rows of a tile of tokens as a buffer: a lane's offset in bytes (vector), a row's (scalar, 32 bits: MAMBA_RECUR_MAX_STRIDE) and the
+// tile's base. With pointers the compiler adds 64-bit addresses in vector registers and computes those of all rows first, spilling
+// scalar registers over it; so, too, the barriers beside an access. Loads from the buffer's end on give zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, unsigned bytes = ~0u) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x27000);
+}
+template <int DT, int VC> __device__ __forceinline__ Pack<DT, VC> load_at(__amdgpu_buffer_rsrc_t buf, unsigned lane, unsigned row) {
+    typedef Pack<DT, VC> Raw;
+    if constexpr (sizeof(Raw) == 2) return __builtin_bit_cast(Raw, __builtin_amdgcn_raw_buffer_load_b16(buf, lane, row, 0));
+    else return __builtin_bit_cast(Raw, __builtin_amdgcn_raw_buffer_load_b32(buf, lane, row, 0));
+}
+template <int DT, int VC> __device__ __forceinline__ void store_at(__amdgpu_buffer_rsrc_t buf, unsigned lane, unsigned row, const float (&x)[VC]) {
+    typedef Pack<DT, VC> Raw;
+    Raw o;
+    if constexpr (DT == BF16 && VC == 2) o = __builtin_bit_cast(Raw, __builtin_convertvector(f2{x[0], x[1]}, b16x2));
+    else {
+#pragma unroll
+        for (int v = 0; v < VC; ++v) o.v[v] = to_raw<DT>(x[v]);
+    }
+    if constexpr (sizeof(Raw) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, o), buf, lane, row, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, o), buf, lane, row, 0);
+}
+// the same value, of which the compiler knows nothing
+template <int DT, int VC> __device__ __forceinline__ void renew(Pack<DT, VC>& x) {
+    typedef Pack<DT, VC> Raw;
+    if constexpr (sizeof(Raw) == 2) {
+        unsigned r = __builtin_bit_cast(unsigned short, x);
+        asm("" : "+v"(r));
+        x = __builtin_bit_cast(Raw, (unsigned short)r);
+    } else {
+        unsigned r = __builtin_bit_cast(unsigned, x);
+        asm("" : "+v"(r));
+        x = __builtin_bit_cast(Raw, r);
+    }
+}
+// One stream's rows of a wave's tokens, TT from t0 on, asked for one by one, so that streams can be asked for token by token and a
+// token's work starts when its own rows are there. Rows from t1 on are zeros: they are asked for at the buffer's end, so nothing is read
+// where t1 <= t0.
 template <int DT, int VC, int TT> struct RowsOf {
     Pack<DT, VC> t[TT];
-    __device__ __forceinline__ void fetch(const raw_t<DT>* base, long ts, int t0, int last, unsigned d) {
-#pragma unroll
-        for (int k = 0; k < TT; ++k) t[k] = load<DT, VC>(base + min(t0 + k, last) * ts + d);
+    unsigned step, at, end;
+    int left;
+    __amdgpu_buffer_rsrc_t rows;
+    __device__ __forceinline__ void place(const Rows& r, const Place& pl, int D, int t0, int t1) {
+        step = (unsigned)r.ts * sizeof(raw_t<DT>), at = 0;
+        end = (unsigned)(min(max(t1 - t0, 1), TT) - 1) * step + D * sizeof(raw_t<DT>);
+        left = t1 - t0;
+        asm("" : "+s"(left));       // conditions of its own: those that streams share would fill the scalar registers
+        rows = buffer_of(layer::at<DT>(r, pl) + t0 * r.ts, end);
+    }
+    __device__ __forceinline__ void fetch(int k, unsigned lane) {
+        t[k] = load_at<DT, VC>(rows, lane, k < left ? at : end);
+        at += step;
+        __builtin_amdgcn_sched_barrier(0);
     }
 };
+// the exponent's factor for token k: none behind the chunk, whose a is one and which nothing enters
+template <int VC> __device__ __forceinline__ float speed_of(const Gates<VC>& gates, int v, int k, int left) { return k < left ? gates.speed[v] : 0.f; }
 
 // The states that enter the chunks of sequence blockIdx.z, in place of the aggregates. Wave w of a block takes SPAN chunks of
 // every SPAN * waves: it folds them from zero, the waves' folds are chained in LDS, and it walks them again from what enters
@@ -140,12 +201,17 @@ inline mimo_status check_recur(int64_t n, int64_t S, int64_t D, int dtype, float
     if (n * S > (int64_t)1 << 40) return unsupported("too many tokens");
     return MIMO_OK;
 }
-// the data of a call: two channels a lane where all of it allows
+// the rows of a tile of tokens lie within 32 bits of its first
+inline mimo_status check_strides(std::initializer_list<const mamba_rows*> rows) {
+    for (const mamba_rows* r : rows)
+        if (r->data && (r->token_stride < 0 || r->token_stride > MAMBA_RECUR_MAX_STRIDE)) return unsupported("token strides beyond 2^26 elements");
+    return MIMO_OK;
+}
+// channels of a lane: four bytes of them where all data allows
 inline int channels_of(int64_t D, int dtype, bool packed, std::initializer_list<const mamba_rows*> rows, std::initializer_list<const void*> dense) {
-    const int esz = dtype == F32 ? 4 : 2;
-    bool two = D % 2 == 0;
-    for (const mamba_rows* r : rows) two = two && (!r->data || aligned(r->data, packed ? 0 : r->batch_stride, r->token_stride, 2 * esz, esz));
-    for (const void* x : dense) two = two && aligned(x, 0, 0, 2 * esz, 1);
+    bool two = dtype != F32 && D % 2 == 0;
+    for (const mamba_rows* r : rows) two = two && (!r->data || aligned(r->data, packed ? 0 : r->batch_stride, r->token_stride, 4, 2));
+    for (const void* x : dense) two = two && aligned(x, 0, 0, 4, 1);
     return two ? 2 : 1;
 }
 

@@ -2,8 +2,6 @@
 // A block takes one chunk of WAVES * TT tokens; k_recur_agg leaves each chunk's joined step, forward and for the adjoint, the
 // carry turns them into the state and the adjoint that enter, and k_recur_bwd walks its tokens forward for the states and
 // back for the adjoints and the gradients. Parameters' gradients leave one partial row a chunk, added up in order.
-#include <initializer_list>
-
 #include "layer_recur.hpp"
 
 namespace mimo {
@@ -12,56 +10,71 @@ namespace {
 
 constexpr int WAVES = 8, TT = 8, CHUNK = WAVES * TT;
 
-// a wave's tokens: inputs as they lie in memory, steps, and the gradient that meets the state
-template <int DT, int VC> struct Tokens {
-    RowsOf<DT, VC, TT> x, r, i, z, g;
-    float a[TT][VC], b[TT][VC], dh[TT][VC];
+// A wave's tokens: the rows that are needed to the end, the gates, and b, later the state in front of a token. What is cheap to have
+// again (a: one 2^x) is not kept, so that four waves a SIMD fit.
+template <int DT, int VC, bool GATE> struct Tokens {
+    RowsOf<DT, VC, TT> x, r, i, g, z;
+    float sr[TT][VC], si[TT][VC], e[TT][VC], b[TT][VC];
 
-    __device__ __forceinline__ void fetch(const RecurParams& p, const Place& pl, int tw, int last, unsigned d) {
-        x.fetch(at<DT>(p.x, pl), p.x.ts, tw, last, d);
-        r.fetch(at<DT>(p.r, pl), p.r.ts, tw, last, d);
-        i.fetch(at<DT>(p.i, pl), p.i.ts, tw, last, d);
-        g.fetch(at<DT>(p.dout, pl), p.dout.ts, tw, last, d);
-        if (p.has_z) z.fetch(at<DT>(p.z, pl), p.z.ts, tw, last, d);
-    }
-    __device__ __forceinline__ void steps(const RecurParams& p, const Gates<VC>& gates, int tw, int t1) {
+    __device__ __forceinline__ void fetch(const RecurParams& p, const Place& pl, int tw, int t1, unsigned lane) {
+        x.place(p.x, pl, p.D, tw, t1), r.place(p.r, pl, p.D, tw, t1), i.place(p.i, pl, p.D, tw, t1), g.place(p.dout, pl, p.D, tw, t1);
+        if constexpr (GATE) z.place(p.z, pl, p.D, tw, t1);
 #pragma unroll
         for (int k = 0; k < TT; ++k) {
-            float fx[VC], fr[VC], fi[VC], fz[VC];
-            unpack<DT, VC>(x.t[k], fx);
-            unpack<DT, VC>(r.t[k], fr);
-            unpack<DT, VC>(i.t[k], fi);
-            unpack<DT, VC>(g.t[k], dh[k]);
-            if (p.has_z) unpack<DT, VC>(z.t[k], fz);
-#pragma unroll
-            for (int v = 0; v < VC; ++v) {
-                float e2;
-                keep_and_enter(gates.speed[v] * sigmoid(fr[v] + gates.rb[v]), a[k][v], e2);
-                b[k][v] = root(e2) * (sigmoid(fi[v] + gates.ib[v]) * fx[v]);
-                if (p.has_z) dh[k][v] *= fz[v] * sigmoid(fz[v]);
-            }
-        }
-        if (tw + TT > t1) {         // tokens behind the chunk change nothing
-#pragma unroll
-            for (int k = 0; k < TT; ++k)
-                if (tw + k >= t1) {
-#pragma unroll
-                    for (int v = 0; v < VC; ++v) a[k][v] = 1.f, b[k][v] = dh[k][v] = 0.f;
-                }
+            x.fetch(k, lane), r.fetch(k, lane), i.fetch(k, lane), g.fetch(k, lane);
+            if constexpr (GATE) z.fetch(k, lane);
         }
     }
-    // the joined step: last state from zero, product of a, adjoint that leaves to the left from zero
-    __device__ __forceinline__ void fold(float (&h)[VC], float (&q)[VC], float (&c)[VC]) const {
+    // dout silu(z)
+    __device__ __forceinline__ void meets(int k, float (&dh)[VC]) const {
+        float fz[VC];
+        unpack<DT, VC>(g.t[k], dh);
+        if constexpr (GATE) {
+            unpack<DT, VC>(z.t[k], fz);
+#pragma unroll
+            for (int v = 0; v < VC; ++v) dh[v] *= fz[v] * sigmoid(fz[v]);
+        }
+    }
+    // From here on values are taken for new: what follows from them is computed again, not kept in registers for its second use.
+    __device__ __forceinline__ void forget() {
+#pragma unroll
+        for (int k = 0; k < TT; ++k) {
+            renew(x.t[k]), renew(g.t[k]);
+            if constexpr (GATE) renew(z.t[k]);
+#pragma unroll
+            for (int v = 0; v < VC; ++v) {
+                asm("" : "+v"(sr[k][v]));
+                asm("" : "+v"(si[k][v]));
+            }
+        }
+    }
+    // Gates of the tokens, and their joined step: last state from zero, product of a, adjoint that leaves to the left from zero.
+    __device__ __forceinline__ void join(const Gates<VC>& gates, int left, float (&h)[VC], float (&q)[VC], float (&c)[VC]) {
 #pragma unroll
         for (int v = 0; v < VC; ++v) h[v] = c[v] = 0.f, q[v] = 1.f;
 #pragma unroll
-        for (int k = 0; k < TT; ++k)
+        for (int k = 0; k < TT; ++k) {
+            float fr[VC], fi[VC], fx[VC], dh[VC], a[VC];
+            unpack<DT, VC>(x.t[k], fx);
+            unpack<DT, VC>(r.t[k], fr);
+            unpack<DT, VC>(i.t[k], fi);
 #pragma unroll
             for (int v = 0; v < VC; ++v) {
-                h[v] = __builtin_fmaf(a[k][v], h[v], b[k][v]);
-                q[v] *= a[k][v];
-                c[v] = a[TT - 1 - k][v] * (dh[TT - 1 - k][v] + c[v]);
+                float e2;
+                sr[k][v] = gates.open(fr[v], gates.rb[v]);
+                si[k][v] = gates.open(fi[v], gates.ib[v]);
+                keep_and_enter(speed_of(gates, v, k, left) * sr[k][v], a[v], e2);
+                e[k][v] = root(e2);
+                b[k][v] = e[k][v] * (si[k][v] * fx[v]);
             }
+            meets(k, dh);
+#pragma unroll
+            for (int v = 0; v < VC; ++v) {
+                h[v] = __builtin_fmaf(a[v], h[v], b[k][v]);
+                q[v] *= a[v];
+                c[v] = __builtin_fmaf(q[v], dh[v], c[v]);
+            }
+        }
     }
 };
 
@@ -73,64 +86,60 @@ template <int VC> struct Join {
     }
 };
 
-template <int DT, int VC> __global__ __launch_bounds__(64 * WAVES) void k_recur_agg(RecurParams p) {
-    __shared__ Join<VC> s;
-    const unsigned slot = blockIdx.x / p.tiles, tile = blockIdx.x - slot * p.tiles;
+template <int DT, bool GATE> __global__ __launch_bounds__(64 * WAVES) void k_recur_agg(RecurParams p) {
+    __shared__ Join<1> s;
+    const unsigned tiles = (p.D + 63) / 64, slot = blockIdx.x / tiles, tile = blockIdx.x - slot * tiles;
     const Place pl = place(p.q, slot);
     if (!pl.ok || pl.i == p.q.n) return;
     const int t0 = pl.j * CHUNK, t1 = min(t0 + CHUNK, pl.len);
     if (t0 >= t1) return;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), tw = t0 + w * TT;
-    const unsigned vec = tile * 64 + lane;
-    const bool act = vec < (unsigned)p.nvec;
-    const unsigned d = act ? vec * VC : 0;
-    Tokens<DT, VC> k;
-    k.fetch(p, pl, tw, t1 - 1, d);
-    const Gates<VC> gates(p, d);
-    k.steps(p, gates, tw, t1);
-    float h[VC], q[VC], c[VC];
-    k.fold(h, q, c);
+    const bool act = tile * 64 + lane < (unsigned)p.D;
+    const unsigned d = act ? tile * 64 + lane : 0;
+    Tokens<DT, 1, GATE> k;
+    k.fetch(p, pl, tw, t1, d * sizeof(raw_t<DT>));
+    const Gates<1> gates(p, d);
+    float h[1], q[1], c[1];
+    k.join(gates, t1 - tw, h, q, c);
     s.put(w, lane, h, q, c);
     __syncthreads();
     if (w != 0 || !act) return;
+    float hh = 0.f, qq = 1.f, cc = 0.f;
 #pragma unroll
-    for (int v = 0; v < VC; ++v) {
-        float hh = 0.f, qq = 1.f, cc = 0.f;
-#pragma unroll
-        for (int o = 0; o < WAVES; ++o) {
-            hh = __builtin_fmaf(s.q[o][lane * VC + v], hh, s.h[o][lane * VC + v]);
-            qq *= s.q[o][lane * VC + v];
-            cc = __builtin_fmaf(s.q[WAVES - 1 - o][lane * VC + v], cc, s.c[WAVES - 1 - o][lane * VC + v]);
-        }
-        const long at = (long)slot * p.D + d + v;
-        p.agg_h[at] = hh, p.agg_p[at] = qq, p.agg_g[at] = cc;
+    for (int o = 0; o < WAVES; ++o) {
+        hh = __builtin_fmaf(s.q[o][lane], hh, s.h[o][lane]);
+        qq *= s.q[o][lane];
+        cc = __builtin_fmaf(s.q[WAVES - 1 - o][lane], cc, s.c[WAVES - 1 - o][lane]);
     }
+    const long at = (long)slot * p.D + d;
+    p.agg_h[at] = hh, p.agg_p[at] = qq, p.agg_g[at] = cc;
 }
 
-template <int DT, int VC> __global__ __launch_bounds__(64 * WAVES) void k_recur_bwd(RecurParams p) {
+template <int DT, int VC, bool GATE> __global__ __launch_bounds__(64 * WAVES, 4) void k_recur_bwd(RecurParams p) {
     typedef raw_t<DT> raw;
     __shared__ Join<VC> s;
-    const unsigned slot = blockIdx.x / p.tiles, tile = blockIdx.x - slot * p.tiles;
+    const unsigned index = blockIdx.x / p.tiles, tile = blockIdx.x - index * p.tiles, slot = (unsigned)p.slots - 1 - index;
     const Place pl = place(p.q, slot);
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const unsigned vec = tile * 64 + lane;
     const bool act = vec < (unsigned)p.nvec;
-    const unsigned d = act ? vec * VC : 0;
+    const unsigned d = act ? vec * VC : 0, db = d * sizeof(raw);
     const long D = p.D;
-    const int t0 = pl.j * CHUNK, t1 = pl.ok ? min(t0 + CHUNK, pl.len) : t0, tw = t0 + w * TT;
-    const long flat = recur_row(p.q, pl) * D + d;
-    raw *dx = static_cast<raw*>(p.dx) + flat, *dr = static_cast<raw*>(p.dr) + flat, *di = static_cast<raw*>(p.di) + flat;
-    raw* dz = p.has_z ? static_cast<raw*>(p.dz) + flat : nullptr;
+    const int t0 = pl.j * CHUNK, t1 = pl.ok ? min(t0 + CHUNK, pl.len) : t0, tw = t0 + w * TT, left = t1 - tw;
     float* part = p.part + (long)slot * 3 * D + d;
     const bool tail = pl.i == p.q.n;
+    const long flat = (recur_row(p.q, pl) + tw) * D;
+    const auto dx = buffer_of(static_cast<raw*>(p.dx) + flat), dr = buffer_of(static_cast<raw*>(p.dr) + flat), di = buffer_of(static_cast<raw*>(p.di) + flat),
+               dz = buffer_of(static_cast<raw*>(GATE ? p.dz : p.dx) + flat);
+    const unsigned step = (unsigned)D * sizeof(raw);
     if (t0 >= t1 || tail) {         // no tokens, or those behind the last sequence
         const float zero[VC] = {};
         if (tail && act)
-            for (int t = t0 + w; t < t1; t += WAVES) {
-                store<DT, VC>(dx + t * D, zero);
-                store<DT, VC>(dr + t * D, zero);
-                store<DT, VC>(di + t * D, zero);
-                if (dz) store<DT, VC>(dz + t * D, zero);
+            for (int k = 0; k < min(left, TT); ++k) {
+                store_at<DT, VC>(dx, db, k * step, zero);
+                store_at<DT, VC>(dr, db, k * step, zero);
+                store_at<DT, VC>(di, db, k * step, zero);
+                if constexpr (GATE) store_at<DT, VC>(dz, db, k * step, zero);
             }
         if (w == 0 && act) {
 #pragma unroll
@@ -141,8 +150,8 @@ template <int DT, int VC> __global__ __launch_bounds__(64 * WAVES) void k_recur_
         }
         return;
     }
-    Tokens<DT, VC> k;
-    k.fetch(p, pl, tw, t1 - 1, d);
+    Tokens<DT, VC, GATE> k;
+    k.fetch(p, pl, tw, t1, db);
     const Gates<VC> gates(p, d);
     float h[VC], c[VC];
     const float* from = p.chunked ? p.agg_h + slot * D : p.init ? p.init + pl.i * D : nullptr;
@@ -152,13 +161,13 @@ template <int DT, int VC> __global__ __launch_bounds__(64 * WAVES) void k_recur_
         h[v] = from ? from[d + v] : 0.f;
         c[v] = late ? late[d + v] : 0.f;
     }
-    k.steps(p, gates, tw, t1);
     {
         float fh[VC], fq[VC], fc[VC];
-        k.fold(fh, fq, fc);
+        k.join(gates, left, fh, fq, fc);
         s.put(w, lane, fh, fq, fc);
     }
     __syncthreads();
+    k.forget();
     // the state that enters this wave's tokens, and the adjoint
     for (int o = 0; o < w; ++o)
 #pragma unroll
@@ -174,46 +183,47 @@ template <int DT, int VC> __global__ __launch_bounds__(64 * WAVES) void k_recur_
         for (int v = 0; v < VC; ++v) {
             const float b = k.b[t][v];
             k.b[t][v] = h[v];
-            h[v] = __builtin_fmaf(k.a[t][v], h[v], b);
+            h[v] = __builtin_fmaf(exp2_hw(speed_of(gates, v, t, left) * k.sr[t][v]), h[v], b);
         }
+    k.forget();
+    unsigned at = TT * step;
 #pragma unroll
     for (int t = TT - 1; t >= 0; --t) {
-        float fx[VC], fr[VC], fi[VC], fz[VC], fg[VC], ox[VC], orr[VC], oi[VC], oz[VC];
+        float fx[VC], fz[VC], fg[VC], g[VC], ox[VC], orr[VC], oi[VC], oz[VC], W[VC];
         unpack<DT, VC>(k.x.t[t], fx);
-        unpack<DT, VC>(k.r.t[t], fr);
-        unpack<DT, VC>(k.i.t[t], fi);
         unpack<DT, VC>(k.g.t[t], fg);
-        if (dz) unpack<DT, VC>(k.z.t[t], fz);
-        const bool real = tw + t < t1;
+        if constexpr (GATE) unpack<DT, VC>(k.z.t[t], fz);
+        k.meets(t, g);
+        at -= step;
 #pragma unroll
         for (int v = 0; v < VC; ++v) {
-            const float sr = sigmoid(fr[v] + gates.rb[v]), si = sigmoid(fi[v] + gates.ib[v]), l2 = gates.speed[v] * sr;
-            float a, e2;
-            keep_and_enter(l2, a, e2);
-            const float inv = e2 > 0.f ? __builtin_amdgcn_rsqf(e2) : e2 - e2, e = root(e2);     // 0 where nothing enters; NaN stays
-            const float g = k.dh[t][v] + c[v], hp = k.b[t][v], u = si * fx[v], l = l2 * LN2;
-            const float W = a * g * (l * hp - (l * inv) * (a * u));
-            const float du = g * e;
-            c[v] = k.a[t][v] * g;
+            const float sr = k.sr[t][v], si = k.si[t][v], e = k.e[t][v], hp = k.b[t][v], l2 = speed_of(gates, v, t, left) * sr, l = l2 * LN2;
+            const float a = exp2_hw(l2), inv = e > 0.f ? __builtin_amdgcn_rcpf(e) : e;      // 0 where nothing enters; NaN stays
+            g[v] += c[v];
+            const float ga = a * g[v], u = si * fx[v], du = g[v] * e, dgate = du * u;
+            W[v] = ga * __builtin_fmaf(l, hp, -(l * inv) * (a * u));
+            c[v] = ga;
             ox[v] = du * si;
-            oi[v] = du * u * (1.f - si);
-            orr[v] = (1.f - sr) * W;
-            if (dz) {
-                const float now = __builtin_fmaf(a, hp, e * u), sg = sigmoid(fz[v]);
-                oz[v] = fg[v] * now * silu_slope(fz[v], sg);
+            oi[v] = __builtin_fmaf(-dgate, si, dgate);
+            orr[v] = __builtin_fmaf(-W[v], sr, W[v]);
+            if constexpr (GATE) {
+                const float sz = sigmoid(fz[v]), out = __builtin_fmaf(-fz[v], sz, fz[v]);
+                oz[v] = fg[v] * __builtin_fmaf(a, hp, e * u) * __builtin_fmaf(sz, out, sz);
             }
-            if (real) {
-                sum[0][v] += W;
+        }
+        if (t < left) {
+#pragma unroll
+            for (int v = 0; v < VC; ++v) {
+                sum[0][v] += W[v];
                 sum[1][v] += orr[v];
                 sum[2][v] += oi[v];
             }
-        }
-        if (real && act) {
-            const long at = (tw + t) * D;
-            store<DT, VC>(dx + at, ox);
-            store<DT, VC>(dr + at, orr);
-            store<DT, VC>(di + at, oi);
-            if (dz) store<DT, VC>(dz + at, oz);
+            if (act) {
+                store_at<DT, VC>(dx, db, at, ox);
+                store_at<DT, VC>(dr, db, at, orr);
+                store_at<DT, VC>(di, db, at, oi);
+                if constexpr (GATE) store_at<DT, VC>(dz, db, at, oz);
+            }
         }
     }
     if (!p.chunked && p.dinit && w == 0 && act) {
@@ -260,14 +270,14 @@ struct BwdPlan {
 
 mimo_status plan_bwd(const mamba_recur_bwd_args* a, BwdPlan* pl) {
     if (a == nullptr) return bad("args must not be NULL");
-    const mimo_status s = check_recur(a->n, a->S, a->D, a->dtype, a->rate);
-    if (s != MIMO_OK) return s;
+    mimo_status s = check_recur(a->n, a->S, a->D, a->dtype, a->rate);
+    if (s != MIMO_OK || (s = check_strides({&a->dout, &a->x, &a->r, &a->i, &a->z})) != MIMO_OK) return s;
     const bool packed = a->cu_seqlens != nullptr;
     pl->VC = channels_of(a->D, a->dtype, packed, {&a->dout, &a->x, &a->r, &a->i, &a->z}, {a->dx, a->dr, a->di, a->dz});
     pl->tiles = (unsigned)((a->D + 64 * pl->VC - 1) / (64 * pl->VC));
     pl->q = Seqs{a->cu_seqlens, (int)a->n, (int)a->S, CHUNK, (int)((a->S + CHUNK - 1) / CHUNK)};
     pl->slots = slots_of(pl->q);
-    if (!grid_fits(pl->slots * pl->tiles, 64 * WAVES)) return unsupported("the call needs more than 2^32 threads");
+    if (!grid_fits(pl->slots * ((a->D + 63) / 64), 64 * WAVES)) return unsupported("the call needs more than 2^32 threads");
     pl->chunked = a->S > CHUNK;
     pl->agg = up256((size_t)pl->slots * a->D * sizeof(float));
     pl->part = up256((size_t)pl->slots * 3 * a->D * sizeof(float));
@@ -275,17 +285,24 @@ mimo_status plan_bwd(const mamba_recur_bwd_args* a, BwdPlan* pl) {
     return MIMO_OK;
 }
 
-template <int DT, int VC> mimo_status run_bwd(const RecurParams& p, hipStream_t st) {
+template <int DT, int VC, bool GATE> mimo_status run_bwd(const RecurParams& p, hipStream_t st) {
     const dim3 grid((unsigned)(p.slots * p.tiles));
     if (p.chunked) {
-        mimo_status s = launch(&k_recur_agg<DT, VC>, grid, 64 * WAVES, 0, st, p);
+        mimo_status s = launch(&k_recur_agg<DT, GATE>, dim3((unsigned)(p.slots * ((p.D + 63) / 64))), 64 * WAVES, 0, st, p);
         if (s != MIMO_OK) return s;
         s = launch_recur_carry<true>(p, st);
         if (s != MIMO_OK) return s;
     }
-    const mimo_status s = launch(&k_recur_bwd<DT, VC>, grid, 64 * WAVES, 0, st, p);
+    const mimo_status s = launch(&k_recur_bwd<DT, VC, GATE>, grid, 64 * WAVES, 0, st, p);
     if (s != MIMO_OK) return s;
     return launch(&k_recur_sums, dim3((unsigned)((3L * p.D + SUM_COLS - 1) / SUM_COLS)), 256, 0, st, p);
+}
+
+template <int DT> mimo_status run_type(int VC, const RecurParams& p, hipStream_t st) {
+    if constexpr (DT != F32) {
+        if (VC == 2) return p.has_z ? run_bwd<DT, 2, true>(p, st) : run_bwd<DT, 2, false>(p, st);
+    }
+    return p.has_z ? run_bwd<DT, 1, true>(p, st) : run_bwd<DT, 1, false>(p, st);
 }
 
 }  // namespace
@@ -331,9 +348,8 @@ mimo_status mamba_recur_bwd(const mamba_recur_bwd_args* a, void* stream) {
     p.agg_g = reinterpret_cast<float*>(ws + pl.part + 2 * pl.agg);
     if ((s = require_gfx950()) != MIMO_OK) return s;
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    if (a->dtype == BF16) return pl.VC == 2 ? run_bwd<BF16, 2>(p, st) : run_bwd<BF16, 1>(p, st);
-    if (a->dtype == F16) return pl.VC == 2 ? run_bwd<F16, 2>(p, st) : run_bwd<F16, 1>(p, st);
-    return pl.VC == 2 ? run_bwd<F32, 2>(p, st) : run_bwd<F32, 1>(p, st);
+    if (a->dtype == BF16) return run_type<BF16>(pl.VC, p, st);
+    return a->dtype == F16 ? run_type<F16>(pl.VC, p, st) : run_type<F32>(pl.VC, p, st);
 }
 
 }  // extern "C"

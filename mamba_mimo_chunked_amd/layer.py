@@ -563,6 +563,11 @@ def mamba_norm_bwd(dout, x, weight, bias=None, z=None, *, groups: int = 1, eps: 
 
 
 # ---------------------------------------------------------------- gated linear recurrence
+def _near(x):
+    """A tensor whose tokens lie near each other: a copy where 2^26 elements or more are between two of them."""
+    return x if x is None or x.stride(-2) <= 1 << 26 else x.contiguous()
+
+
 def _check_recur(x, r, i, decay, r_bias, i_bias, z, rate, dev):
     """The tensors with dense inner axes, parameters contiguous."""
     if r is None or i is None or decay is None:
@@ -571,8 +576,8 @@ def _check_recur(x, r, i, decay, r_bias, i_bias, z, rate, dev):
         raise ValueError(f"rate must be finite and not negative, got {rate}")
     shape, dtype = x.shape, x.dtype
     width = shape[-1:]
-    return ((_dense_inner(x, 1), _data("r", r, shape, dtype, dev), _data("i", i, shape, dtype, dev), _data("z", z, shape, dtype, dev)),
-            (_param("decay", decay, width, _F32, dev), _param("r_bias", r_bias, width, _F32, dev), _param("i_bias", i_bias, width, _F32, dev)))
+    data = (_dense_inner(x, 1), _data("r", r, shape, dtype, dev), _data("i", i, shape, dtype, dev), _data("z", z, shape, dtype, dev))
+    return data, (_param("decay", decay, width, _F32, dev), _param("r_bias", r_bias, width, _F32, dev), _param("i_bias", i_bias, width, _F32, dev))
 
 
 def mamba_recur_fwd(x, r, i, decay, r_bias=None, i_bias=None, z=None, initial_state=None, cu_seqlens=None, *, rate: float = 8.0,
@@ -593,6 +598,7 @@ def mamba_recur_fwd(x, r, i, decay, r_bias=None, i_bias=None, z=None, initial_st
     n, S, lead = _sequences("x", x, cu_seqlens, 1)
     D = x.shape[-1]
     (x, r, i, z), (decay, r_bias, i_bias) = _check_recur(x, r, i, decay, r_bias, i_bias, z, rate, dev)
+    x, r, i, z = map(_near, (x, r, i, z))
     cu, initial_state = _cu(cu_seqlens, dev), _param("initial_state", initial_state, (n, D), _F32, dev)
     res = _out(out, x, x=x, r=r, i=i, decay=decay, r_bias=r_bias, i_bias=i_bias, z=z, initial_state=initial_state, cu_seqlens=cu)
     if workspace is not None:
@@ -619,6 +625,7 @@ def mamba_recur_bwd(dout, x, r, i, decay, r_bias=None, i_bias=None, z=None, init
     if dout is None:
         _required(dout=dout)
     dout = _data("dout", dout, x.shape, x.dtype, dev)
+    dout, x, r, i, z = map(_near, (dout, x, r, i, z))
     initial_state = _param("initial_state", initial_state, (n, D), _F32, dev)
     cu, dstate = _cu(cu_seqlens, dev), _param("dstate", dstate, (n, D), _F32, dev)
     if workspace is not None:
@@ -727,14 +734,14 @@ def mamba_add_norm_fwd(x, weight, residual=None, *, eps: float = 1e-5, dropout: 
         raise ValueError(f"block must be one of {_BLOCKS}, with an 8-bit out_dtype, got {block!r}" if kind else "block needs an 8-bit out_dtype")
     rows = _row_view(x, D)
     if out is None:
-        res = torch.empty(x.shape, dtype=out_dtype if kind else dtype, device=dev)
+        res = x.new_empty(x.shape, dtype=out_dtype) if kind else _new_like(x)
     else:
         _check_output("out", out, x.shape, out_dtype if kind else dtype, dev)
         _apart("out", out, x=rows, residual=rr, weight=weight, seed=seed)
         res = out
     kept = residual is None and not drop and stream == dtype
-    total = x if kept else torch.empty(x.shape, dtype=stream, device=dev)
-    scale = torch.empty((*x.shape[:-1], -(-D // block) if block else 1), dtype=_F32, device=dev) if kind else None
+    total = x if kept else x.new_empty(x.shape, dtype=stream)
+    scale = weight.new_empty((*x.shape[:-1], -(-D // block) if block else 1)) if kind else None
     _call("mamba_add_norm_fwd", (rows.shape[0], D, rows.stride(0), 0 if rr is None else rr.stride(0), code, int(stream == _F32), kind, block or 0,
                                  drop, eps, rows.data_ptr(), _ptr(rr), _ptr(seed), weight.data_ptr(), 0 if kept else total.data_ptr(), res.data_ptr(),
                                  _ptr(scale)), dev)
@@ -760,9 +767,9 @@ def mamba_add_norm_bwd(dout, sum, weight, dsum=None, *, eps: float = 1e-5, dropo
         sr = _row_view(dsum, D)
     if workspace is not None:
         _apart("workspace", workspace, dout=gr, sum=vr, dsum=sr, weight=weight, seed=seed)
-    dx, dweight = torch.empty(dout.shape, dtype=dout.dtype, device=dev), torch.empty_like(weight)
+    dx, dweight = _new_like(dout), torch.empty_like(weight)
     same = not drop and stream == dout.dtype
-    dres = None if not residual else dx if same else torch.empty(dout.shape, dtype=stream, device=dev)
+    dres = None if not residual else dx if same else dout.new_empty(dout.shape, dtype=stream)
     _call("mamba_add_norm_bwd", (gr.shape[0], D, gr.stride(0), vr.stride(0), 0 if sr is None else sr.stride(0), code, int(stream == _F32), drop, eps,
                                  gr.data_ptr(), vr.data_ptr(), _ptr(sr), _ptr(seed), weight.data_ptr(), dx.data_ptr(),
                                  0 if same else _ptr(dres), dweight.data_ptr()), dev, workspace)

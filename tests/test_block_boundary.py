@@ -18,7 +18,8 @@ BAD = [(f, kw, st) for fs, cases in (
     (RECUR, [(dict(n=0), VALUE), (dict(D=0), VALUE), (dict(dtype=3), TYPE), (dict(dtype=-1), TYPE), (dict(n=70000), UNSUPPORTED),
              (dict(D=1 << 21), UNSUPPORTED), (dict(rate=-1.0), VALUE), (dict(rate=float("nan")), VALUE), (dict(rate=float("inf")), VALUE),
              (dict(x=NONE), VALUE), (dict(r=NONE), VALUE), (dict(i=NONE), VALUE), (dict(decay=None), VALUE)]),
-    (RECUR[:2], [(dict(S=0), VALUE), (dict(S=(1 << 30) + 1), UNSUPPORTED)]),
+    (RECUR[:2], [(dict(S=0), VALUE), (dict(S=(1 << 30) + 1), UNSUPPORTED), (dict(r=_lib.MambaRows(1 << 20, 0, (1 << 26) + 1)), UNSUPPORTED),
+                 (dict(z=_lib.MambaRows(1 << 20, 0, -64)), UNSUPPORTED)]),
     (("mamba_recur_fwd", "mamba_recur_step"), [(dict(out=None), VALUE)]),
     (("mamba_recur_step",), [(dict(state=None), VALUE), (dict(slots=0), VALUE), (dict(indices=None, slots=1), VALUE)]),
     (("mamba_recur_bwd",), [(dict(dout=NONE), VALUE), (dict(dz=None), VALUE), (dict(z=NONE), VALUE), (dict(dr_bias=None), VALUE), (dict(i_bias=None), VALUE),

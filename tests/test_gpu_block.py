@@ -436,6 +436,37 @@ def test_stack_gradient():
         assert float((p.cpu().double() - q).norm() / q.norm()) < 4000 * R.U, k
 
 
+def test_recur_with_far_tokens():
+    """Tokens 2^26 elements and more apart (a time-major buffer of a huge batch) are copied, those just below are read in place."""
+    g = _gen(41)
+    D, far = 24, (1 << 26) + 8
+    x = _recur_inputs(g, (1, 3), 1, D, BF)
+    want = m.mamba_recur_fwd(**x, return_state=True)
+    dout = torch.randn(1, 3, D, generator=g).to(BF).cuda()
+    grads = m.mamba_recur_bwd(dout, **x)
+    room = torch.empty(2 * far + D, dtype=BF, device="cuda")
+    for stride in (far, 1 << 26, (1 << 26) - 8):
+        y = room.as_strided((1, 3, D), (0, stride, 1))
+        y.copy_(x["r"])
+        got = m.mamba_recur_fwd(**{**x, "r": y}, return_state=True)
+        assert _same(got.out, want.out) and _same(got.state, want.state)
+        assert all(_same(a, b) for a, b in zip(m.mamba_recur_bwd(dout, **{**x, "r": y}), grads))
+
+
+def test_recur_with_repeated_tokens():
+    """One row for every token (stride 0), and rows that overlap."""
+    g = _gen(42)
+    D, S = 40, 150
+    x = _recur_inputs(g, (2, S), 2, D, HF)
+    one = torch.randn(2, 1, D, generator=g).to(HF).cuda()
+    line = torch.randn(S + D, generator=g).to(HF).cuda()
+    dout = torch.randn(2, S, D, generator=g).to(HF).cuda()
+    for y in (one.expand(2, S, D), line.as_strided((2, S, D), (0, 1, 1))):
+        a, b = ({**x, "x": v, "z": v} for v in (y, y.contiguous()))
+        assert _same(m.mamba_recur_fwd(**a).out, m.mamba_recur_fwd(**b).out)
+        assert all(_same(p, q) for p, q in zip(m.mamba_recur_bwd(dout, **a), m.mamba_recur_bwd(dout, **b)))
+
+
 @pytest.mark.parametrize("D,S", [(8, 1 << 14)])
 def test_long_sequence_of_few_channels(D, S):
     """Many chunks of one tile, against the sequential definition."""
