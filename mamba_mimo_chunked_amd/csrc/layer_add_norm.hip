@@ -23,6 +23,7 @@ struct AddNormParams {
     float* scale;
 };
 
+typedef unsigned pair __attribute__((ext_vector_type(2)));
 constexpr float LEAST = 0x1p-100f;  // a scale is made from at least this
 
 __device__ __forceinline__ unsigned larger(unsigned a, unsigned b) { return a > b ? a : b; }
@@ -41,9 +42,10 @@ __device__ __forceinline__ unsigned max_lanes(unsigned x, int lanes) {
 }
 
 template <bool WIDE> __device__ __forceinline__ void put_bytes(unsigned char* p, int c, int D, const unsigned (&q)[2]) {
-    if constexpr (WIDE) {
-        if (c < D) *reinterpret_cast<uint2*>(p + c) = make_uint2(q[0], q[1]);
-    } else {
+    if (WIDE ? c < D : c + NV <= D) {
+        if constexpr (WIDE) *reinterpret_cast<pair*>(p + c) = pair{q[0], q[1]};
+        else *reinterpret_cast<typename Loose<pair, 1>::type*>(p + c) = pair{q[0], q[1]};
+    } else if (!WIDE) {
 #pragma unroll
         for (int k = 0; k < NV; ++k)
             if (c + k < D) p[c + k] = (unsigned char)(q[k / 4] >> (8 * (k % 4)));

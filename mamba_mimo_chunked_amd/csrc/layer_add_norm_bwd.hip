@@ -31,29 +31,38 @@ template <int DT, int ST, bool WIDE, int TPR, int IT> __global__ __launch_bounds
         rw.fetch(p.w, (t + k * TPR) * NV, p.D);
         rw.read((t + k * TPR) * NV, p.D, w[k]);
     }
-    for (long row0 = (long)blockIdx.x * RPB; row0 < p.rows; row0 += (long)gridDim.x * RPB) {
-        const bool act = row0 + sub < p.rows;
-        const long row = act ? row0 + sub : p.rows - 1;
-        Eight<ST, WIDE> rv[IT], rs[IT];
-        Eight<DT, WIDE> rg[IT];
+    Eight<ST, WIDE> rv[IT], rs[IT];
+    Eight<DT, WIDE> rg[IT];
+    auto fetch = [&](long row) {
+        row = row < p.rows ? row : p.rows - 1;
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
             const int c = (t + k * TPR) * NV;
             rv[k].fetch(static_cast<const raw_t<ST>*>(p.sum) + row * p.ss, c, p.D);
             rg[k].fetch(static_cast<const raw_t<DT>*>(p.dout) + row * p.gs, c, p.D);
+            if (p.dsum) rs[k].fetch(static_cast<const raw_t<ST>*>(p.dsum) + row * p.ds, c, p.D);
         }
-        if (p.dsum) {
+    };
+    const long step = (long)gridDim.x * RPB;
+    fetch((long)blockIdx.x * RPB + sub);
+    for (long row0 = (long)blockIdx.x * RPB; row0 < p.rows; row0 += step) {
+        const bool act = row0 + sub < p.rows;
+        const long row = act ? row0 + sub : p.rows - 1;
+        unsigned keep[IT];
+        if (p.drop) {
 #pragma unroll
-            for (int k = 0; k < IT; ++k) rs[k].fetch(static_cast<const raw_t<ST>*>(p.dsum) + row * p.ds, (t + k * TPR) * NV, p.D);
+            for (int k = 0; k < IT; ++k) keep[k] = kept8(p.seed, t + k * TPR, (unsigned)row, p.drop);
         }
-        float v[IT][NV], g[IT][NV], q = 0.f, m = 0.f;
+        float v[IT][NV], g[IT][NV], d[IT][NV] = {}, q = 0.f, m = 0.f;
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
             rv[k].read((t + k * TPR) * NV, p.D, v[k]);
             rg[k].read((t + k * TPR) * NV, p.D, g[k]);
+            if (p.dsum) rs[k].read((t + k * TPR) * NV, p.D, d[k]);
 #pragma unroll
             for (int i = 0; i < NV; ++i) q = __builtin_fmaf(v[k][i], v[k][i], q);
         }
+        if (row0 + step < p.rows) fetch(row0 + step + sub);
         q = sum_row<TPR>(q, s[0]) * p.inv;
         const float r = 1.f / __builtin_sqrtf(q + p.eps);
 #pragma unroll
@@ -70,18 +79,13 @@ template <int DT, int ST, bool WIDE, int TPR, int IT> __global__ __launch_bounds
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
             const int c = (t + k * TPR) * NV;
-            float dv[NV], d[NV];
-            if (p.dsum) rs[k].read(c, p.D, d);
+            float dv[NV];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                dv[i] = r * __builtin_fmaf(-v[k][i], m, g[k][i]);
-                if (p.dsum) dv[i] += d[i];
-            }
+            for (int i = 0; i < NV; ++i) dv[i] = __builtin_fmaf(r, __builtin_fmaf(-v[k][i], m, g[k][i]), d[k][i]);
             if (p.dres) put8<ST, WIDE>(static_cast<raw_t<ST>*>(p.dres) + row * p.D, c, p.D, dv);
             if (p.drop) {
-                const unsigned keep = kept8(p.seed, t + k * TPR, (unsigned)row, p.drop);
 #pragma unroll
-                for (int i = 0; i < NV; ++i) dv[i] = keep >> i & 1 ? dv[i] * p.factor : 0.f;
+                for (int i = 0; i < NV; ++i) dv[i] = keep[k] >> i & 1 ? dv[i] * p.factor : 0.f;
             }
             put8<DT, WIDE>(static_cast<raw_t<DT>*>(p.dx) + row * p.D, c, p.D, dv);
         }
@@ -112,10 +116,10 @@ __global__ __launch_bounds__(256) void k_add_norm_sums(AddNormBwdParams p) {
     column_sums(p.part, p.D, p.nblk, (long)blockIdx.x * SUM_COLS, p.D, [&](long col, float s) { p.dw[col] = s; });
 }
 
-// blocks: 1024 threads a CU in all, none without a row of its own
+// blocks: 512 threads a CU in all, none without a row of its own
 int64_t blocks_of(const mamba_add_norm_bwd_args* a) {
     const int lanes = row_threads(a->D), threads = block_of(lanes), per = threads / lanes;
-    const int64_t want = 256 * 1024 / threads, have = (a->rows + per - 1) / per;
+    const int64_t want = 256 * 512 / threads, have = (a->rows + per - 1) / per;
     return have < want ? have : want;
 }
 
