@@ -80,12 +80,14 @@ template <int VC> struct Gates {
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, unsigned bytes = ~0u) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x27000);
 }
-template <int DT, int VC> __device__ __forceinline__ Pack<DT, VC> load_at(__amdgpu_buffer_rsrc_t buf, unsigned lane, unsigned row) {
+// AUX: the access's cache policy, NT for data that passes by
+constexpr int NT = 2;
+template <int DT, int VC, int AUX = 0> __device__ __forceinline__ Pack<DT, VC> load_at(__amdgpu_buffer_rsrc_t buf, unsigned lane, unsigned row) {
     typedef Pack<DT, VC> Raw;
-    if constexpr (sizeof(Raw) == 2) return __builtin_bit_cast(Raw, __builtin_amdgcn_raw_buffer_load_b16(buf, lane, row, 0));
-    else return __builtin_bit_cast(Raw, __builtin_amdgcn_raw_buffer_load_b32(buf, lane, row, 0));
+    if constexpr (sizeof(Raw) == 2) return __builtin_bit_cast(Raw, __builtin_amdgcn_raw_buffer_load_b16(buf, lane, row, AUX));
+    else return __builtin_bit_cast(Raw, __builtin_amdgcn_raw_buffer_load_b32(buf, lane, row, AUX));
 }
-template <int DT, int VC> __device__ __forceinline__ void store_at(__amdgpu_buffer_rsrc_t buf, unsigned lane, unsigned row, const float (&x)[VC]) {
+template <int DT, int VC, int AUX = 0> __device__ __forceinline__ void store_at(__amdgpu_buffer_rsrc_t buf, unsigned lane, unsigned row, const float (&x)[VC]) {
     typedef Pack<DT, VC> Raw;
     Raw o;
     if constexpr (DT == BF16 && VC == 2) o = __builtin_bit_cast(Raw, __builtin_convertvector(f2{x[0], x[1]}, b16x2));
@@ -93,8 +95,8 @@ template <int DT, int VC> __device__ __forceinline__ void store_at(__amdgpu_buff
 #pragma unroll
         for (int v = 0; v < VC; ++v) o.v[v] = to_raw<DT>(x[v]);
     }
-    if constexpr (sizeof(Raw) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, o), buf, lane, row, 0);
-    else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, o), buf, lane, row, 0);
+    if constexpr (sizeof(Raw) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, o), buf, lane, row, AUX);
+    else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, o), buf, lane, row, AUX);
 }
 // the same value, of which the compiler knows nothing
 template <int DT, int VC> __device__ __forceinline__ void renew(Pack<DT, VC>& x) {
@@ -112,7 +114,7 @@ template <int DT, int VC> __device__ __forceinline__ void renew(Pack<DT, VC>& x)
 // One stream's rows of a wave's tokens, TT from t0 on, asked for one by one, so that streams can be asked for token by token and a
 // token's work starts when its own rows are there. Rows from t1 on are zeros: they are asked for at the buffer's end, so nothing is read
 // where t1 <= t0.
-template <int DT, int VC, int TT> struct RowsOf {
+template <int DT, int VC, int TT, int AUX = 0> struct RowsOf {
     Pack<DT, VC> t[TT];
     unsigned step, at, end;
     int left;
@@ -125,7 +127,7 @@ template <int DT, int VC, int TT> struct RowsOf {
         rows = buffer_of(layer::at<DT>(r, pl) + t0 * r.ts, end);
     }
     __device__ __forceinline__ void fetch(int k, unsigned lane) {
-        t[k] = load_at<DT, VC>(rows, lane, k < left ? at : end);
+        t[k] = load_at<DT, VC, AUX>(rows, lane, k < left ? at : end);
         at += step;
         __builtin_amdgcn_sched_barrier(0);
     }

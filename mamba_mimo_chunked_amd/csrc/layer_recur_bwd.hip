@@ -9,12 +9,13 @@ namespace layer {
 namespace {
 
 constexpr int WAVES = 8, TT = 8, CHUNK = WAVES * TT;
+constexpr long LAST_LEVEL = 256L << 20;     // bytes of the last-level cache
 
 // A wave's tokens: the rows that are needed to the end, the gates, and b, later the state in front of a token. What is cheap to have
 // again (a: one 2^x) is not kept, so that four waves a SIMD fit.
-template <int DT, int VC, bool GATE> struct Tokens {
-    RowsOf<DT, VC, TT> x, r, i, g, z;
-    float sr[TT][VC], si[TT][VC], e[TT][VC], b[TT][VC];
+template <int DT, int VC, bool GATE, int AUX> struct Tokens {
+    RowsOf<DT, VC, TT, AUX> x, r, i, g, z;
+    float l2[TT][VC], si[TT][VC], e[TT][VC], b[TT][VC];     // l2: l in powers of two
 
     __device__ __forceinline__ void fetch(const RecurParams& p, const Place& pl, int tw, int t1, unsigned lane) {
         x.place(p.x, pl, p.D, tw, t1), r.place(p.r, pl, p.D, tw, t1), i.place(p.i, pl, p.D, tw, t1), g.place(p.dout, pl, p.D, tw, t1);
@@ -43,7 +44,7 @@ template <int DT, int VC, bool GATE> struct Tokens {
             if constexpr (GATE) renew(z.t[k]);
 #pragma unroll
             for (int v = 0; v < VC; ++v) {
-                asm("" : "+v"(sr[k][v]));
+                asm("" : "+v"(l2[k][v]));
                 asm("" : "+v"(si[k][v]));
             }
         }
@@ -61,9 +62,9 @@ template <int DT, int VC, bool GATE> struct Tokens {
 #pragma unroll
             for (int v = 0; v < VC; ++v) {
                 float e2;
-                sr[k][v] = gates.open(fr[v], gates.rb[v]);
+                l2[k][v] = speed_of(gates, v, k, left) * gates.open(fr[v], gates.rb[v]);
                 si[k][v] = gates.open(fi[v], gates.ib[v]);
-                keep_and_enter(speed_of(gates, v, k, left) * sr[k][v], a[v], e2);
+                keep_and_enter(l2[k][v], a[v], e2);
                 e[k][v] = root(e2);
                 b[k][v] = e[k][v] * (si[k][v] * fx[v]);
             }
@@ -96,7 +97,7 @@ template <int DT, bool GATE> __global__ __launch_bounds__(64 * WAVES) void k_rec
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), tw = t0 + w * TT;
     const bool act = tile * 64 + lane < (unsigned)p.D;
     const unsigned d = act ? tile * 64 + lane : 0;
-    Tokens<DT, 1, GATE> k;
+    Tokens<DT, 1, GATE, 0> k;
     k.fetch(p, pl, tw, t1, d * sizeof(raw_t<DT>));
     const Gates<1> gates(p, d);
     float h[1], q[1], c[1];
@@ -115,7 +116,9 @@ template <int DT, bool GATE> __global__ __launch_bounds__(64 * WAVES) void k_rec
     p.agg_h[at] = hh, p.agg_p[at] = qq, p.agg_g[at] = cc;
 }
 
-template <int DT, int VC, bool GATE> __global__ __launch_bounds__(64 * WAVES, 4) void k_recur_bwd(RecurParams p) {
+// AUX: the policy of its accesses, the last ones to the inputs. The chunks come from the last to the first: the inputs that the
+// aggregates read last are still in the last-level cache.
+template <int DT, int VC, bool GATE, int AUX> __global__ __launch_bounds__(64 * WAVES, 4) void k_recur_bwd(RecurParams p) {
     typedef raw_t<DT> raw;
     __shared__ Join<VC> s;
     const unsigned index = blockIdx.x / p.tiles, tile = blockIdx.x - index * p.tiles, slot = (unsigned)p.slots - 1 - index;
@@ -150,7 +153,7 @@ template <int DT, int VC, bool GATE> __global__ __launch_bounds__(64 * WAVES, 4)
         }
         return;
     }
-    Tokens<DT, VC, GATE> k;
+    Tokens<DT, VC, GATE, AUX> k;
     k.fetch(p, pl, tw, t1, db);
     const Gates<VC> gates(p, d);
     float h[VC], c[VC];
@@ -183,9 +186,12 @@ template <int DT, int VC, bool GATE> __global__ __launch_bounds__(64 * WAVES, 4)
         for (int v = 0; v < VC; ++v) {
             const float b = k.b[t][v];
             k.b[t][v] = h[v];
-            h[v] = __builtin_fmaf(exp2_hw(speed_of(gates, v, t, left) * k.sr[t][v]), h[v], b);
+            h[v] = __builtin_fmaf(exp2_hw(k.l2[t][v]), h[v], b);
         }
     k.forget();
+    float shut[VC];                 // -ln(2) / speed: what takes l2 to -ln(2) sigmoid(r)
+#pragma unroll
+    for (int v = 0; v < VC; ++v) shut[v] = gates.speed[v] < 0.f ? -LN2 / gates.speed[v] : 0.f;
     unsigned at = TT * step;
 #pragma unroll
     for (int t = TT - 1; t >= 0; --t) {
@@ -197,18 +203,19 @@ template <int DT, int VC, bool GATE> __global__ __launch_bounds__(64 * WAVES, 4)
         at -= step;
 #pragma unroll
         for (int v = 0; v < VC; ++v) {
-            const float sr = k.sr[t][v], si = k.si[t][v], e = k.e[t][v], hp = k.b[t][v], l2 = speed_of(gates, v, t, left) * sr, l = l2 * LN2;
-            const float a = exp2_hw(l2), inv = e > 0.f ? __builtin_amdgcn_rcpf(e) : e;      // 0 where nothing enters; NaN stays
+            const float l2 = k.l2[t][v], si = k.si[t][v], e = k.e[t][v], hp = k.b[t][v], a = exp2_hw(l2);
+            // l / e, which is zero where nothing enters
+            const float part = l2 * __builtin_amdgcn_rcpf(__builtin_fmaxf(e, 1e-30f));
             g[v] += c[v];
             const float ga = a * g[v], u = si * fx[v], du = g[v] * e, dgate = du * u;
-            W[v] = ga * __builtin_fmaf(l, hp, -(l * inv) * (a * u));
+            W[v] = ga * __builtin_fmaf(l2, hp, -part * (a * u));        // times log2(e)
             c[v] = ga;
             ox[v] = du * si;
             oi[v] = __builtin_fmaf(-dgate, si, dgate);
-            orr[v] = __builtin_fmaf(-W[v], sr, W[v]);
+            orr[v] = W[v] * __builtin_fmaf(l2, shut[v], LN2);           // 1 - sigmoid(r), times ln(2)
             if constexpr (GATE) {
                 const float sz = sigmoid(fz[v]), out = __builtin_fmaf(-fz[v], sz, fz[v]);
-                oz[v] = fg[v] * __builtin_fmaf(a, hp, e * u) * __builtin_fmaf(sz, out, sz);
+                oz[v] = fg[v] * (t + 1 < TT ? k.b[t + 1 < TT ? t + 1 : 0][v] : h[v]) * __builtin_fmaf(sz, out, sz);
             }
         }
         if (t < left) {
@@ -219,10 +226,10 @@ template <int DT, int VC, bool GATE> __global__ __launch_bounds__(64 * WAVES, 4)
                 sum[2][v] += oi[v];
             }
             if (act) {
-                store_at<DT, VC>(dx, db, at, ox);
-                store_at<DT, VC>(dr, db, at, orr);
-                store_at<DT, VC>(di, db, at, oi);
-                if constexpr (GATE) store_at<DT, VC>(dz, db, at, oz);
+                store_at<DT, VC, AUX>(dx, db, at, ox);
+                store_at<DT, VC, AUX>(dr, db, at, orr);
+                store_at<DT, VC, AUX>(di, db, at, oi);
+                if constexpr (GATE) store_at<DT, VC, AUX>(dz, db, at, oz);
             }
         }
     }
@@ -254,7 +261,7 @@ __global__ __launch_bounds__(256) void k_recur_sums(RecurParams p) {
         } else {
             // sigmoid / softplus, one where both vanish
             const float x = p.decay[col], sp = softplus(x);
-            p.ddecay[col] = sp > 0.f ? s * (sigmoid(x) / sp) : s;
+            p.ddecay[col] = LN2 * (sp > 0.f ? s * (sigmoid(x) / sp) : s);
         }
     });
 }
@@ -286,14 +293,16 @@ mimo_status plan_bwd(const mamba_recur_bwd_args* a, BwdPlan* pl) {
 }
 
 template <int DT, int VC, bool GATE> mimo_status run_bwd(const RecurParams& p, hipStream_t st) {
-    const dim3 grid((unsigned)(p.slots * p.tiles));
     if (p.chunked) {
         mimo_status s = launch(&k_recur_agg<DT, GATE>, dim3((unsigned)(p.slots * ((p.D + 63) / 64))), 64 * WAVES, 0, st, p);
         if (s != MIMO_OK) return s;
         s = launch_recur_carry<true>(p, st);
         if (s != MIMO_OK) return s;
     }
-    const mimo_status s = launch(&k_recur_bwd<DT, VC, GATE>, grid, 64 * WAVES, 0, st, p);
+    const dim3 grid((unsigned)(p.slots * p.tiles));
+    const long bytes = (p.q.cu ? (long)p.q.S : (long)p.q.n * p.q.S) * p.D * (GATE ? 9 : 7) * sizeof(raw_t<DT>);
+    const mimo_status s = bytes > LAST_LEVEL ? launch(&k_recur_bwd<DT, VC, GATE, NT>, grid, 64 * WAVES, 0, st, p)
+                                             : launch(&k_recur_bwd<DT, VC, GATE, 0>, grid, 64 * WAVES, 0, st, p);
     if (s != MIMO_OK) return s;
     return launch(&k_recur_sums, dim3((unsigned)((3L * p.D + SUM_COLS - 1) / SUM_COLS)), 256, 0, st, p);
 }

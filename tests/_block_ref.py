@@ -111,7 +111,7 @@ def recur(x, r, i, decay, r_bias, i_bias, z, initial, cu, rate, dout=None, dstat
         We = t1 * (ca + cl + 6) + a * la * (Ge * prev_m + Gm * prev_e) + t2 * (2 * ca + cl + ce + csi + 8) + la * inv * a * a * u.abs() * Ge
         We = We + 2 * FLUSH * la * (Gm + 1) * (prev_m + inv * u.abs() + 1) + Gm * (prev_m * gone / U + u.abs() * efl)
         Wm = t1 + t2
-        dr, dr_e = (1 - sr) * W, (1 - sr) * (We + 2 * Wm) + Wm * (sr * csr + 1)
+        dr, dr_e = (1 - sr) * W, (1 - sr) * (We + 2 * Wm) + Wm * (sr * (csr + 4) + 1)     # 1 + l / (rate softplus): four more roundings
         du = G * e
         # sums over the tokens: a wave's eight, eight waves, a sixteenth of the chunks in four sums, sixteen of those
         adds = 8 + 8 + T // 1024 + n + 20
