@@ -1,4 +1,4 @@
-// Gated linear recurrence, forward pass and step of one token (formulas, gates: layer_recur.hpp).
+// Gated linear recurrence, forward pass and step of one token (formulas, gates, rows: layer_recur.hpp).
 #include "layer_recur.hpp"
 
 namespace mimo {
@@ -48,7 +48,7 @@ template <int DT, bool GATE> __global__ __launch_bounds__(64 * WAVES, 6) void k_
         __syncthreads();
         slot = __builtin_amdgcn_readfirstlane(s_slot);
     }
-    const Place pl = place(p.q, slot);
+    const Place pl = place_by_wave(p.q, slot);
     if (!pl.ok) return;
     const int t0 = pl.j * CH, t1 = min(t0 + CH, pl.len);
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), tw = t0 + w * TT, left = t1 - tw;
@@ -67,26 +67,28 @@ template <int DT, bool GATE> __global__ __launch_bounds__(64 * WAVES, 6) void k_
     float h = group == 0 && p.init ? p.init[pl.i * D + d] : 0.f;
     if (t0 < t1) {
         RowsOf<DT, 1, TT> rx, rr, ri, rz;
-        rx.place(p.x, pl, p.D, tw, t1), rr.place(p.r, pl, p.D, tw, t1), ri.place(p.i, pl, p.D, tw, t1);
-        if constexpr (GATE) rz.place(p.z, pl, p.D, tw, t1);
-#pragma unroll
-        for (int k = 0; k < TT; ++k) rx.fetch(k, db), rr.fetch(k, db), ri.fetch(k, db);
-        if constexpr (GATE) {
-#pragma unroll
-            for (int k = 0; k < TT; ++k) rz.fetch(k, db);
-        }
-        const Gates<1> gates(p, d);
         float a[TT], b[TT], fold = 0.f, prod = 1.f;
+        if (left > 0) {             // a short sequence leaves waves without tokens
+            rx.place(p.x, pl, p.D, tw, t1), rr.place(p.r, pl, p.D, tw, t1), ri.place(p.i, pl, p.D, tw, t1);
+            if constexpr (GATE) rz.place(p.z, pl, p.D, tw, t1);
 #pragma unroll
-        for (int k = 0; k < TT; ++k) {
-            float e2;
-            keep_and_enter(speed_of(gates, 0, k, left) * gates.open(to_f<DT>(rr.t[k].v[0]), gates.rb[0]), a[k], e2);
-            b[k] = root(e2) * (gates.open(to_f<DT>(ri.t[k].v[0]), gates.ib[0]) * to_f<DT>(rx.t[k].v[0]));
-        }
+            for (int k = 0; k < TT; ++k) rx.fetch(k, db), rr.fetch(k, db), ri.fetch(k, db);
+            if constexpr (GATE) {
 #pragma unroll
-        for (int k = 0; k < TT; ++k) {
-            fold = __builtin_fmaf(a[k], fold, b[k]);
-            prod *= a[k];
+                for (int k = 0; k < TT; ++k) rz.fetch(k, db);
+            }
+            const Gates<1> gates(p, d);
+#pragma unroll
+            for (int k = 0; k < TT; ++k) {
+                float e2;
+                keep_and_enter(speed_of(gates, 0, k, left) * gates.open(to_f<DT>(rr.t[k].v[0]), gates.rb[0]), a[k], e2);
+                b[k] = root(e2) * (gates.open(to_f<DT>(ri.t[k].v[0]), gates.ib[0]) * to_f<DT>(rx.t[k].v[0]));
+            }
+#pragma unroll
+            for (int k = 0; k < TT; ++k) {
+                fold = __builtin_fmaf(a[k], fold, b[k]);
+                prod *= a[k];
+            }
         }
         s_h[w][lane] = fold;
         s_p[w][lane] = prod;
@@ -147,7 +149,7 @@ template <int DT, bool GATE> __global__ __launch_bounds__(64 * WAVES, 6) void k_
         }
         if (closes && w == 0 && act) tell(ends + (long)(slot / GROUP) * D + d, h, 0u);
         unsigned row = 0;
-        if (act) {
+        if (act && left > 0) {
 #pragma unroll
             for (int k = 0; k < TT; ++k) {
                 enter = __builtin_fmaf(a[k], enter, b[k]);

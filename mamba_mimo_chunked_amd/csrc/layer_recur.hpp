@@ -1,4 +1,4 @@
-// Gated linear recurrence, one state a channel: parameters, the gates, and the carry between chunks.
+// Gated linear recurrence, one state a channel: parameters, the gates, and rows of tokens.
 //
 //   l = -rate softplus(decay) sr, sr = sigmoid(r + rb);  a = exp(l);  e = sqrt(1 - a^2)
 //   h[t] = a h[t-1] + e si x, si = sigmoid(i + ib);  out = h silu(z)
@@ -37,6 +37,30 @@ struct RecurParams {
     float* part;                    // [slots][3][D]
     long slots;
 };
+
+// place(), by a whole wave: its lanes look at 64 sequences at a time, two or three dependent loads where bisection takes up to
+// sixteen, which is what blocks of short sequences wait for (2000 sequences of 8 tokens, D = 2048, forward: 795 us, 990 by bisection).
+__device__ __forceinline__ Place place_by_wave(const Seqs& q, int slot) {
+    if (q.cu == nullptr) return place(q, slot);
+    const int lane = threadIdx.x & 63;
+    int lo = 0, hi = q.n;           // the largest sequence whose base(lo) <= slot is in [lo, hi]
+    while (lo < hi) {
+        const int step = (hi - lo + 63) / 64, at = lo + (lane + 1) * step;
+        // those in front of the first that is behind: base(lo) <= slot, also where cu_seqlens decrease
+        const unsigned long long behind = ~__ballot(at <= hi && q.base(min(at, hi)) <= slot);
+        const int below = behind ? __builtin_ctzll(behind) : 64;
+        const int from = lo + below * step;
+        hi = min(hi, from + step - 1);
+        lo = from;
+    }
+    Place r;
+    r.i = lo;
+    r.j = slot - q.base(lo);
+    r.row0 = q.start(lo);
+    r.len = max((lo < q.n ? q.start(lo + 1) : q.S) - r.row0, 0);
+    r.ok = r.j == 0 || (long)r.j * q.CH < r.len;
+    return r;
+}
 
 // first row of the flat token axis of a place
 __device__ __forceinline__ long recur_row(const Seqs& q, const Place& pl) { return q.cu ? (long)pl.row0 : (long)pl.i * q.S; }
@@ -135,67 +159,7 @@ template <int DT, int VC, int TT, int AUX = 0> struct RowsOf {
 // the exponent's factor for token k: none behind the chunk, whose a is one and which nothing enters
 template <int VC> __device__ __forceinline__ float speed_of(const Gates<VC>& gates, int v, int k, int left) { return k < left ? gates.speed[v] : 0.f; }
 
-// The states that enter the chunks of sequence blockIdx.z, in place of the aggregates. Wave w of a block takes SPAN chunks of
-// every SPAN * waves: it folds them from zero, the waves' folds are chained in LDS, and it walks them again from what enters
-// them, so that all loads of up to 128 chunks are in flight together. With ADJ, blockIdx.y = 1 runs the adjoints from the last
-// chunk to the first, from dstate, and leaves the gradient of the initial state.
-constexpr int RSPAN = 8, RSPAN_WAVES = 16;
-template <bool ADJ> __global__ __launch_bounds__(64 * RSPAN_WAVES) void k_recur_carry(RecurParams p) {
-    __shared__ float s_h[RSPAN_WAVES][64], s_p[RSPAN_WAVES][64];
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-    const int i = blockIdx.z;
-    const unsigned d0 = blockIdx.x * 64 + lane;
-    const bool rev = ADJ && blockIdx.y, act = d0 < (unsigned)p.D;
-    const unsigned d = act ? d0 : 0;
-    const long D = p.D;
-    const int slot0 = p.q.cu ? p.q.base(i) : i * p.q.nc;
-    const int len = p.q.cu ? max((i < p.q.n ? p.q.start(i + 1) : p.q.S) - p.q.start(i), 0) : p.q.S;
-    const int nc = max((len + p.q.CH - 1) / p.q.CH, 1);
-    const int have = ADJ ? (len > 0 ? nc : 0) : nc - 1;    // chunks with an aggregate: the forward pass needs none of the last
-    const float* from = rev ? p.dstate : p.init;
-    float h = from ? from[(long)i * D + d] : 0.f;
-    float* agg = (rev ? p.agg_g : p.agg_h) + (long)slot0 * D + d;
-    const float* prod = p.agg_p + (long)slot0 * D + d;
-    for (int j0 = 0; j0 < nc; j0 += RSPAN * waves) {
-        float x[RSPAN], e[RSPAN], fold = 0.f, all = 1.f;
-#pragma unroll
-        for (int k = 0; k < RSPAN; ++k) {
-            const int j = j0 + w * RSPAN + k, at = rev ? nc - 1 - j : j;
-            x[k] = j < have ? agg[(long)at * D] : 0.f;
-            e[k] = j < have ? prod[(long)at * D] : 1.f;
-        }
-#pragma unroll
-        for (int k = 0; k < RSPAN; ++k) {
-            fold = __builtin_fmaf(e[k], fold, x[k]);
-            all *= e[k];
-        }
-        s_h[w][lane] = fold;
-        s_p[w][lane] = all;
-        __syncthreads();
-        float g = h;
-        for (int o = 0; o < waves; ++o) {
-            if (o == w) g = h;
-            h = __builtin_fmaf(s_p[o][lane], h, s_h[o][lane]);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < RSPAN; ++k) {
-            const int j = j0 + w * RSPAN + k;
-            if (j < nc && act) agg[(long)(rev ? nc - 1 - j : j) * D] = g;
-            g = __builtin_fmaf(e[k], g, x[k]);
-        }
-    }
-    if (rev && p.dinit && w == 0 && act) p.dinit[(long)i * D + d] = h;
-}
-
 // ---------------------------------------------------------------- host side
-// Waves for the chunks of a sequence, of a packed one for twice the average: longer ones take more rounds.
-template <bool ADJ> mimo_status launch_recur_carry(const RecurParams& p, hipStream_t st) {
-    long chunks = p.q.nc;
-    if (p.q.cu && 2 * p.slots / p.q.n < chunks) chunks = 2 * p.slots / p.q.n;
-    const int waves = (int)(chunks <= RSPAN ? 1 : chunks < RSPAN * RSPAN_WAVES ? (chunks + RSPAN - 1) / RSPAN : RSPAN_WAVES);
-    return launch(&k_recur_carry<ADJ>, dim3((unsigned)((p.D + 63) / 64), ADJ ? 2 : 1, p.q.n), 64 * waves, 0, st, p);
-}
 inline mimo_status check_recur(int64_t n, int64_t S, int64_t D, int dtype, float rate) {
     const mimo_status s = check_sequences(n, S, D, dtype);
     if (s != MIMO_OK) return s;

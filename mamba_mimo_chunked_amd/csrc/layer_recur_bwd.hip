@@ -1,4 +1,4 @@
-// Gated linear recurrence, backward pass (formulas, gates, carry: layer_recur.hpp). Nothing is kept from the forward pass.
+// Gated linear recurrence, backward pass (formulas, gates, rows: layer_recur.hpp). Nothing is kept from the forward pass.
 // A block takes one chunk of WAVES * TT tokens; k_recur_agg leaves each chunk's joined step, forward and for the adjoint, the
 // carry turns them into the state and the adjoint that enter, and k_recur_bwd walks its tokens forward for the states and
 // back for the adjoints and the gradients. Parameters' gradients leave one partial row a chunk, added up in order.
@@ -8,7 +8,11 @@ namespace mimo {
 namespace layer {
 namespace {
 
-constexpr int WAVES = 8, TT = 8, CHUNK = WAVES * TT;
+constexpr int TT = 8;               // tokens of a wave
+// Waves of a block, and with them the tokens of a chunk: eight, or two where the sequences of a packed batch have fewer than SHORT tokens
+// in the mean, whose last chunks leave the other waves idle (16000 tokens, D = 2048, bf16: mean 8 tokens 871 us with eight, 415 with
+// two; 32: 368 and 255; 100: 258 and 226; 200: 233 and 220; 400: 212 and 215; dense [4 x 4096]: 195 and 215).
+constexpr int SHORT = 256;
 constexpr long LAST_LEVEL = 256L << 20;     // bytes of the last-level cache
 
 // A wave's tokens: the rows that are needed to the end, the gates, and b, later the state in front of a token. What is cheap to have
@@ -79,7 +83,7 @@ template <int DT, int VC, bool GATE, int AUX> struct Tokens {
     }
 };
 
-template <int VC> struct Join {
+template <int VC, int WAVES> struct Join {
     float h[WAVES][64 * VC], q[WAVES][64 * VC], c[WAVES][64 * VC];
     __device__ __forceinline__ void put(int w, int lane, const float (&fh)[VC], const float (&fq)[VC], const float (&fc)[VC]) {
 #pragma unroll
@@ -87,10 +91,11 @@ template <int VC> struct Join {
     }
 };
 
-template <int DT, bool GATE> __global__ __launch_bounds__(64 * WAVES) void k_recur_agg(RecurParams p) {
-    __shared__ Join<1> s;
+template <int DT, bool GATE, int WAVES> __global__ __launch_bounds__(64 * WAVES) void k_recur_agg(RecurParams p) {
+    constexpr int CHUNK = WAVES * TT;
+    __shared__ Join<1, WAVES> s;
     const unsigned tiles = (p.D + 63) / 64, slot = blockIdx.x / tiles, tile = blockIdx.x - slot * tiles;
-    const Place pl = place(p.q, slot);
+    const Place pl = place_by_wave(p.q, slot);
     if (!pl.ok || pl.i == p.q.n) return;
     const int t0 = pl.j * CHUNK, t1 = min(t0 + CHUNK, pl.len);
     if (t0 >= t1) return;
@@ -98,10 +103,11 @@ template <int DT, bool GATE> __global__ __launch_bounds__(64 * WAVES) void k_rec
     const bool act = tile * 64 + lane < (unsigned)p.D;
     const unsigned d = act ? tile * 64 + lane : 0;
     Tokens<DT, 1, GATE, 0> k;
-    k.fetch(p, pl, tw, t1, d * sizeof(raw_t<DT>));
-    const Gates<1> gates(p, d);
-    float h[1], q[1], c[1];
-    k.join(gates, t1 - tw, h, q, c);
+    float h[1] = {0.f}, q[1] = {1.f}, c[1] = {0.f};
+    if (tw < t1) {                  // a short sequence leaves waves without tokens
+        k.fetch(p, pl, tw, t1, d * sizeof(raw_t<DT>));
+        k.join(Gates<1>(p, d), t1 - tw, h, q, c);
+    }
     s.put(w, lane, h, q, c);
     __syncthreads();
     if (w != 0 || !act) return;
@@ -116,13 +122,67 @@ template <int DT, bool GATE> __global__ __launch_bounds__(64 * WAVES) void k_rec
     p.agg_h[at] = hh, p.agg_p[at] = qq, p.agg_g[at] = cc;
 }
 
+// The states that enter the chunks of sequence blockIdx.z, in place of the aggregates. Wave w of a block takes SPAN chunks of
+// every SPAN * waves: it folds them from zero, the waves' folds are chained in LDS, and it walks them again from what enters
+// them, so that all loads of up to 128 chunks are in flight together. blockIdx.y = 1 runs the adjoints from the last chunk to the
+// first, from dstate, and leaves the gradient of the initial state.
+constexpr int RSPAN = 8, RSPAN_WAVES = 16;
+__global__ __launch_bounds__(64 * RSPAN_WAVES) void k_recur_carry(RecurParams p) {
+    __shared__ float s_h[RSPAN_WAVES][64], s_p[RSPAN_WAVES][64];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    const int i = blockIdx.z;
+    const unsigned d0 = blockIdx.x * 64 + lane;
+    const bool rev = blockIdx.y, act = d0 < (unsigned)p.D;
+    const unsigned d = act ? d0 : 0;
+    const long D = p.D;
+    const int slot0 = p.q.cu ? p.q.base(i) : i * p.q.nc;
+    const int len = p.q.cu ? max((i < p.q.n ? p.q.start(i + 1) : p.q.S) - p.q.start(i), 0) : p.q.S;
+    const int nc = max((len + p.q.CH - 1) / p.q.CH, 1);
+    const int have = len > 0 ? nc : 0;      // chunks with an aggregate
+    const float* from = rev ? p.dstate : p.init;
+    float h = from ? from[(long)i * D + d] : 0.f;
+    float* agg = (rev ? p.agg_g : p.agg_h) + (long)slot0 * D + d;
+    const float* prod = p.agg_p + (long)slot0 * D + d;
+    for (int j0 = 0; j0 < nc; j0 += RSPAN * waves) {
+        float x[RSPAN], e[RSPAN], fold = 0.f, all = 1.f;
+#pragma unroll
+        for (int k = 0; k < RSPAN; ++k) {
+            const int j = j0 + w * RSPAN + k, at = rev ? nc - 1 - j : j;
+            x[k] = j < have ? agg[(long)at * D] : 0.f;
+            e[k] = j < have ? prod[(long)at * D] : 1.f;
+        }
+#pragma unroll
+        for (int k = 0; k < RSPAN; ++k) {
+            fold = __builtin_fmaf(e[k], fold, x[k]);
+            all *= e[k];
+        }
+        s_h[w][lane] = fold;
+        s_p[w][lane] = all;
+        __syncthreads();
+        float g = h;
+        for (int o = 0; o < waves; ++o) {
+            if (o == w) g = h;
+            h = __builtin_fmaf(s_p[o][lane], h, s_h[o][lane]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < RSPAN; ++k) {
+            const int j = j0 + w * RSPAN + k;
+            if (j < nc && act) agg[(long)(rev ? nc - 1 - j : j) * D] = g;
+            g = __builtin_fmaf(e[k], g, x[k]);
+        }
+    }
+    if (rev && p.dinit && w == 0 && act) p.dinit[(long)i * D + d] = h;
+}
+
 // AUX: the policy of its accesses, the last ones to the inputs. The chunks come from the last to the first: the inputs that the
 // aggregates read last are still in the last-level cache.
-template <int DT, int VC, bool GATE, int AUX> __global__ __launch_bounds__(64 * WAVES, 4) void k_recur_bwd(RecurParams p) {
+template <int DT, int VC, bool GATE, int AUX, int WAVES> __global__ __launch_bounds__(64 * WAVES, 4) void k_recur_bwd(RecurParams p) {
     typedef raw_t<DT> raw;
-    __shared__ Join<VC> s;
+    constexpr int CHUNK = WAVES * TT;
+    __shared__ Join<VC, WAVES> s;
     const unsigned index = blockIdx.x / p.tiles, tile = blockIdx.x - index * p.tiles, slot = (unsigned)p.slots - 1 - index;
-    const Place pl = place(p.q, slot);
+    const Place pl = place_by_wave(p.q, slot);
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const unsigned vec = tile * 64 + lane;
     const bool act = vec < (unsigned)p.nvec;
@@ -154,7 +214,7 @@ template <int DT, int VC, bool GATE, int AUX> __global__ __launch_bounds__(64 * 
         return;
     }
     Tokens<DT, VC, GATE, AUX> k;
-    k.fetch(p, pl, tw, t1, db);
+    if (left > 0) k.fetch(p, pl, tw, t1, db);
     const Gates<VC> gates(p, d);
     float h[VC], c[VC];
     const float* from = p.chunked ? p.agg_h + slot * D : p.init ? p.init + pl.i * D : nullptr;
@@ -166,7 +226,9 @@ template <int DT, int VC, bool GATE, int AUX> __global__ __launch_bounds__(64 * 
     }
     {
         float fh[VC], fq[VC], fc[VC];
-        k.join(gates, left, fh, fq, fc);
+#pragma unroll
+        for (int v = 0; v < VC; ++v) fh[v] = fc[v] = 0.f, fq[v] = 1.f;
+        if (left > 0) k.join(gates, left, fh, fq, fc);
         s.put(w, lane, fh, fq, fc);
     }
     __syncthreads();
@@ -179,57 +241,59 @@ template <int DT, int VC, bool GATE, int AUX> __global__ __launch_bounds__(64 * 
 #pragma unroll
         for (int v = 0; v < VC; ++v) c[v] = __builtin_fmaf(s.q[o][lane * VC + v], c[v], s.c[o][lane * VC + v]);
     float sum[3][VC] = {};
-    // b becomes the state in front of a token
+    if (left > 0) {
+        // b becomes the state in front of a token
 #pragma unroll
-    for (int t = 0; t < TT; ++t)
-#pragma unroll
-        for (int v = 0; v < VC; ++v) {
-            const float b = k.b[t][v];
-            k.b[t][v] = h[v];
-            h[v] = __builtin_fmaf(exp2_hw(k.l2[t][v]), h[v], b);
-        }
-    k.forget();
-    float shut[VC];                 // -ln(2) / speed: what takes l2 to -ln(2) sigmoid(r)
-#pragma unroll
-    for (int v = 0; v < VC; ++v) shut[v] = gates.speed[v] < 0.f ? -LN2 / gates.speed[v] : 0.f;
-    unsigned at = TT * step;
-#pragma unroll
-    for (int t = TT - 1; t >= 0; --t) {
-        float fx[VC], fz[VC], fg[VC], g[VC], ox[VC], orr[VC], oi[VC], oz[VC], W[VC];
-        unpack<DT, VC>(k.x.t[t], fx);
-        unpack<DT, VC>(k.g.t[t], fg);
-        if constexpr (GATE) unpack<DT, VC>(k.z.t[t], fz);
-        k.meets(t, g);
-        at -= step;
-#pragma unroll
-        for (int v = 0; v < VC; ++v) {
-            const float l2 = k.l2[t][v], si = k.si[t][v], e = k.e[t][v], hp = k.b[t][v], a = exp2_hw(l2);
-            // l / e, which is zero where nothing enters
-            const float part = l2 * __builtin_amdgcn_rcpf(__builtin_fmaxf(e, 1e-30f));
-            g[v] += c[v];
-            const float ga = a * g[v], u = si * fx[v], du = g[v] * e, dgate = du * u;
-            W[v] = ga * __builtin_fmaf(l2, hp, -part * (a * u));        // times log2(e)
-            c[v] = ga;
-            ox[v] = du * si;
-            oi[v] = __builtin_fmaf(-dgate, si, dgate);
-            orr[v] = W[v] * __builtin_fmaf(l2, shut[v], LN2);           // 1 - sigmoid(r), times ln(2)
-            if constexpr (GATE) {
-                const float sz = sigmoid(fz[v]), out = __builtin_fmaf(-fz[v], sz, fz[v]);
-                oz[v] = fg[v] * (t + 1 < TT ? k.b[t + 1 < TT ? t + 1 : 0][v] : h[v]) * __builtin_fmaf(sz, out, sz);
-            }
-        }
-        if (t < left) {
+        for (int t = 0; t < TT; ++t)
 #pragma unroll
             for (int v = 0; v < VC; ++v) {
-                sum[0][v] += W[v];
-                sum[1][v] += orr[v];
-                sum[2][v] += oi[v];
+                const float b = k.b[t][v];
+                k.b[t][v] = h[v];
+                h[v] = __builtin_fmaf(exp2_hw(k.l2[t][v]), h[v], b);
             }
-            if (act) {
-                store_at<DT, VC, AUX>(dx, db, at, ox);
-                store_at<DT, VC, AUX>(dr, db, at, orr);
-                store_at<DT, VC, AUX>(di, db, at, oi);
-                if constexpr (GATE) store_at<DT, VC, AUX>(dz, db, at, oz);
+        k.forget();
+        float shut[VC];                 // -ln(2) / speed: what takes l2 to -ln(2) sigmoid(r)
+#pragma unroll
+        for (int v = 0; v < VC; ++v) shut[v] = gates.speed[v] < 0.f ? -LN2 / gates.speed[v] : 0.f;
+        unsigned at = TT * step;
+#pragma unroll
+        for (int t = TT - 1; t >= 0; --t) {
+            float fx[VC], fz[VC], fg[VC], g[VC], ox[VC], orr[VC], oi[VC], oz[VC], W[VC];
+            unpack<DT, VC>(k.x.t[t], fx);
+            unpack<DT, VC>(k.g.t[t], fg);
+            if constexpr (GATE) unpack<DT, VC>(k.z.t[t], fz);
+            k.meets(t, g);
+            at -= step;
+#pragma unroll
+            for (int v = 0; v < VC; ++v) {
+                const float l2 = k.l2[t][v], si = k.si[t][v], e = k.e[t][v], hp = k.b[t][v], a = exp2_hw(l2);
+                // l / e, which is zero where nothing enters
+                const float part = l2 * __builtin_amdgcn_rcpf(__builtin_fmaxf(e, 1e-30f));
+                g[v] += c[v];
+                const float ga = a * g[v], u = si * fx[v], du = g[v] * e, dgate = du * u;
+                W[v] = ga * __builtin_fmaf(l2, hp, -part * (a * u));        // times log2(e)
+                c[v] = ga;
+                ox[v] = du * si;
+                oi[v] = __builtin_fmaf(-dgate, si, dgate);
+                orr[v] = W[v] * __builtin_fmaf(l2, shut[v], LN2);           // 1 - sigmoid(r), times ln(2)
+                if constexpr (GATE) {
+                    const float sz = sigmoid(fz[v]), out = __builtin_fmaf(-fz[v], sz, fz[v]);
+                    oz[v] = fg[v] * (t + 1 < TT ? k.b[t + 1 < TT ? t + 1 : 0][v] : h[v]) * __builtin_fmaf(sz, out, sz);
+                }
+            }
+            if (t < left) {
+#pragma unroll
+                for (int v = 0; v < VC; ++v) {
+                    sum[0][v] += W[v];
+                    sum[1][v] += orr[v];
+                    sum[2][v] += oi[v];
+                }
+                if (act) {
+                    store_at<DT, VC, AUX>(dx, db, at, ox);
+                    store_at<DT, VC, AUX>(dr, db, at, orr);
+                    store_at<DT, VC, AUX>(di, db, at, oi);
+                    if constexpr (GATE) store_at<DT, VC, AUX>(dz, db, at, oz);
+                }
             }
         }
     }
@@ -266,9 +330,16 @@ __global__ __launch_bounds__(256) void k_recur_sums(RecurParams p) {
     });
 }
 
+// Waves for the chunks of a sequence, of a packed one for twice the average: longer ones take more rounds.
+mimo_status launch_recur_carry(const RecurParams& p, hipStream_t st) {
+    long chunks = p.q.nc;
+    if (p.q.cu && 2 * p.slots / p.q.n < chunks) chunks = 2 * p.slots / p.q.n;
+    const int waves = (int)(chunks <= RSPAN ? 1 : chunks < RSPAN * RSPAN_WAVES ? (chunks + RSPAN - 1) / RSPAN : RSPAN_WAVES);
+    return launch(&k_recur_carry, dim3((unsigned)((p.D + 63) / 64), 2, p.q.n), 64 * waves, 0, st, p);
+}
 struct BwdPlan {
     Seqs q;
-    int VC;
+    int VC, waves;
     unsigned tiles;
     long slots;
     bool chunked;
@@ -282,36 +353,40 @@ mimo_status plan_bwd(const mamba_recur_bwd_args* a, BwdPlan* pl) {
     const bool packed = a->cu_seqlens != nullptr;
     pl->VC = channels_of(a->D, a->dtype, packed, {&a->dout, &a->x, &a->r, &a->i, &a->z}, {a->dx, a->dr, a->di, a->dz});
     pl->tiles = (unsigned)((a->D + 64 * pl->VC - 1) / (64 * pl->VC));
-    pl->q = Seqs{a->cu_seqlens, (int)a->n, (int)a->S, CHUNK, (int)((a->S + CHUNK - 1) / CHUNK)};
+    pl->waves = packed && a->S > 8 * TT && a->S / a->n < SHORT ? 2 : 8;
+    const int CH = pl->waves * TT;
+    pl->q = Seqs{a->cu_seqlens, (int)a->n, (int)a->S, CH, (int)((a->S + CH - 1) / CH)};
     pl->slots = slots_of(pl->q);
-    if (!grid_fits(pl->slots * ((a->D + 63) / 64), 64 * WAVES)) return unsupported("the call needs more than 2^32 threads");
-    pl->chunked = a->S > CHUNK;
+    if (!grid_fits(pl->slots * ((a->D + 63) / 64), 64 * pl->waves)) return unsupported("the call needs more than 2^32 threads");
+    pl->chunked = a->S > CH;
     pl->agg = up256((size_t)pl->slots * a->D * sizeof(float));
     pl->part = up256((size_t)pl->slots * 3 * a->D * sizeof(float));
     pl->bytes = pl->part + (pl->chunked ? 3 * pl->agg : 0);
     return MIMO_OK;
 }
 
-template <int DT, int VC, bool GATE> mimo_status run_bwd(const RecurParams& p, hipStream_t st) {
+template <int DT, int VC, bool GATE, int WAVES> mimo_status run_bwd(const RecurParams& p, hipStream_t st) {
     if (p.chunked) {
-        mimo_status s = launch(&k_recur_agg<DT, GATE>, dim3((unsigned)(p.slots * ((p.D + 63) / 64))), 64 * WAVES, 0, st, p);
+        mimo_status s = launch(&k_recur_agg<DT, GATE, WAVES>, dim3((unsigned)(p.slots * ((p.D + 63) / 64))), 64 * WAVES, 0, st, p);
         if (s != MIMO_OK) return s;
-        s = launch_recur_carry<true>(p, st);
+        s = launch_recur_carry(p, st);
         if (s != MIMO_OK) return s;
     }
     const dim3 grid((unsigned)(p.slots * p.tiles));
     const long bytes = (p.q.cu ? (long)p.q.S : (long)p.q.n * p.q.S) * p.D * (GATE ? 9 : 7) * sizeof(raw_t<DT>);
-    const mimo_status s = bytes > LAST_LEVEL ? launch(&k_recur_bwd<DT, VC, GATE, NT>, grid, 64 * WAVES, 0, st, p)
-                                             : launch(&k_recur_bwd<DT, VC, GATE, 0>, grid, 64 * WAVES, 0, st, p);
+    const mimo_status s = bytes > LAST_LEVEL ? launch(&k_recur_bwd<DT, VC, GATE, NT, WAVES>, grid, 64 * WAVES, 0, st, p)
+                                             : launch(&k_recur_bwd<DT, VC, GATE, 0, WAVES>, grid, 64 * WAVES, 0, st, p);
     if (s != MIMO_OK) return s;
     return launch(&k_recur_sums, dim3((unsigned)((3L * p.D + SUM_COLS - 1) / SUM_COLS)), 256, 0, st, p);
 }
-
-template <int DT> mimo_status run_type(int VC, const RecurParams& p, hipStream_t st) {
+template <int DT, int VC, bool GATE> mimo_status run_waves(const BwdPlan& pl, const RecurParams& p, hipStream_t st) {
+    return pl.waves == 8 ? run_bwd<DT, VC, GATE, 8>(p, st) : run_bwd<DT, VC, GATE, 2>(p, st);
+}
+template <int DT> mimo_status run_type(const BwdPlan& pl, const RecurParams& p, hipStream_t st) {
     if constexpr (DT != F32) {
-        if (VC == 2) return p.has_z ? run_bwd<DT, 2, true>(p, st) : run_bwd<DT, 2, false>(p, st);
+        if (pl.VC == 2) return p.has_z ? run_waves<DT, 2, true>(pl, p, st) : run_waves<DT, 2, false>(pl, p, st);
     }
-    return p.has_z ? run_bwd<DT, 1, true>(p, st) : run_bwd<DT, 1, false>(p, st);
+    return p.has_z ? run_waves<DT, 1, true>(pl, p, st) : run_waves<DT, 1, false>(pl, p, st);
 }
 
 }  // namespace
@@ -357,8 +432,8 @@ mimo_status mamba_recur_bwd(const mamba_recur_bwd_args* a, void* stream) {
     p.agg_g = reinterpret_cast<float*>(ws + pl.part + 2 * pl.agg);
     if ((s = require_gfx950()) != MIMO_OK) return s;
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    if (a->dtype == BF16) return run_type<BF16>(pl.VC, p, st);
-    return a->dtype == F16 ? run_type<F16>(pl.VC, p, st) : run_type<F32>(pl.VC, p, st);
+    if (a->dtype == BF16) return run_type<BF16>(pl, p, st);
+    return a->dtype == F16 ? run_type<F16>(pl, p, st) : run_type<F32>(pl, p, st);
 }
 
 }  // extern "C"

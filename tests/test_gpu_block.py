@@ -41,6 +41,8 @@ RECUR = [  # dtype, D, sequences, options
     (FF, 72, ("packed", [0, 1, 5, 0, 170, 33, 2], 9), {}), (BF, 130, ("packed", [300, 0, 1, 129], 50), {}), (HF, 12, ("packed", [1], 0), dict(bias=False)),
     (FF, 36, PACKED, dict(gate=False, init=False)), (BF, 68, PACKED, dict(strided=True)), (HF, 64, ("packed", [2] * 65, 3), {}),
     (BF, 20, ("packed", [0, 0], 70), {}), (FF, 16, ("packed", [1] * 30 + [1500] + [0] * 5, 2), {}), (BF, 32, ("packed", [64, 128, 256, 63, 1], 200), {}),
+    # few long sequences, and many of some tokens: the chunks of a gradient differ
+    (BF, 34, ("packed", [600, 1, 0, 500], 3), {}), (FF, 9, ("packed", [1030], 0), dict(gate=False)), (HF, 17, ("packed", [16, 17, 15, 31, 33] * 14, 1), {}),
     # decays so small that nearly nothing is forgotten or enters, and so large that nothing is kept
     (FF, 32, (1, 200), dict(slow=16.0)), (BF, 32, (1, 200), dict(slow=-40.0)), (FF, 32, (2, 200), dict(slow=100.0)),
 ]
@@ -465,6 +467,29 @@ def test_recur_with_repeated_tokens():
         a, b = ({**x, "x": v, "z": v} for v in (y, y.contiguous()))
         assert _same(m.mamba_recur_fwd(**a).out, m.mamba_recur_fwd(**b).out)
         assert all(_same(p, q) for p, q in zip(m.mamba_recur_bwd(dout, **a), m.mamba_recur_bwd(dout, **b)))
+
+
+@pytest.mark.parametrize("dtype,D,S,gate", [(BF, 2048, 2048, True), (HF, 2047, 2050, False), (FF, 1030, 2000, True)])
+def test_recur_gradient_larger_than_the_cache(dtype, D, S, gate):
+    """A call beyond the last-level cache's size gives a sequence's gradients the bits that a call for the sequence alone gives them."""
+    g = torch.Generator(device="cuda").manual_seed(51)
+    n = 5
+    new = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x = {k: new(n, S, D).to(dtype) for k in ("x", "r", "i")}
+    x["z"] = new(n, S, D).to(dtype) if gate else None
+    x.update(decay=new(D) - 3, r_bias=new(D), i_bias=None, initial_state=new(n, D))
+    dout, ds = new(n, S, D).to(dtype), new(n, D)
+    assert n * S * D * (9 if gate else 7) * dout.element_size() > 256 << 20
+    whole = m.mamba_recur_bwd(dout, **x, dstate=ds)
+    total = torch.zeros(D, dtype=torch.float64, device="cuda")
+    for k in range(n):
+        one = m.mamba_recur_bwd(dout[k:k + 1], **{a: v if v is None or v.dim() == 1 else v[k:k + 1] for a, v in x.items()}, dstate=ds[k:k + 1])
+        for name in ("dx", "dr", "di", "dz", "dinitial_state"):
+            a, b = getattr(whole, name), getattr(one, name)
+            assert (a is None and b is None) or _same(a[k:k + 1], b), name
+        total += one.ddecay.double()
+    # sums of n * S terms in fp32: their errors are those of some hundred roundings of the terms' size, sqrt(n S) of which remain
+    assert float((whole.ddecay.double() - total).norm() / total.norm()) < 300 * R.U
 
 
 @pytest.mark.parametrize("D,S", [(8, 1 << 14)])
