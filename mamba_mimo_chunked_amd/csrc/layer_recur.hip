@@ -5,9 +5,8 @@ namespace mimo {
 namespace layer {
 namespace {
 
-constexpr int WAVES = 8;            // of a block
 constexpr int TT = 16;              // tokens of a wave
-constexpr int GROUP = 32, EACH = GROUP / WAVES;     // chunks of a group, and of a wave's share of it
+constexpr int EACH = 4;             // chunks of a wave's share of a group
 constexpr int POLLS = 1 << 18;      // a wait's limit: some tenths of a second
 constexpr int LINE = 64;            // counters lie this far apart: neighbours would wait for each other
 typedef unsigned long long word;
@@ -30,15 +29,15 @@ __global__ __launch_bounds__(256) void k_recur_clear(RecurParams p) {
 // The outputs, in one pass over the inputs. A block takes one chunk of WAVES * TT tokens by 64 channels, all of it in registers:
 // it joins its tokens' steps, tells the joined step (last state from zero, product of a; one word of 64 bits a channel) to the
 // chunks behind it, joins those of the chunks in front, and walks its tokens from there. The chunks of a sequence are joined in
-// groups of GROUP: a chunk looks at those of its group, and at the state that the last chunk of the group in front tells. The order in
+// groups of WAVES * EACH: a chunk looks at those of its group, and at the state that the last chunk of the group in front tells. The order in
 // which steps are joined is fixed, so equal inputs give equal bits.
 // Every wait ends: a block takes the next chunk of its tile from a counter, so that whatever it waits for belongs to a block that runs
 // already, and a chunk's step is told before its block waits, a group's state after waiting for lower chunks alone. cu_seqlens that
 // decrease may leave a word that nobody tells: POLLS ends the first such wait, its mark behind the counters all others, and outputs
 // are NaN. A word holds value and mark, so no fence is needed.
-template <int DT, bool GATE> __global__ __launch_bounds__(64 * WAVES, 6) void k_recur(RecurParams p) {
+template <int DT, bool GATE, int WAVES> __global__ __launch_bounds__(64 * WAVES, 6) void k_recur(RecurParams p) {
     typedef raw_t<DT> raw;
-    constexpr int CH = WAVES * TT;
+    constexpr int CH = WAVES * TT, GROUP = WAVES * EACH;
     __shared__ float s_h[WAVES][64], s_p[WAVES][64], s_gh[WAVES][64], s_gp[WAVES][64];
     __shared__ unsigned s_slot;
     const unsigned tile = blockIdx.x % p.tiles;
@@ -232,6 +231,7 @@ template <int DT, int VC> __global__ __launch_bounds__(256) void k_recur_step(St
 struct FwdPlan {
     Seqs q;
     unsigned tiles;
+    int waves;
     long slots;
     bool chunked;
     long words;
@@ -244,10 +244,11 @@ mimo_status plan_fwd(const mamba_recur_fwd_args* a, FwdPlan* pl) {
     if (s != MIMO_OK || (s = check_strides({&a->x, &a->r, &a->i, &a->z})) != MIMO_OK) return s;
     const bool packed = a->cu_seqlens != nullptr;
     pl->tiles = (unsigned)((a->D + 63) / 64);
-    const int CH = WAVES * TT;
+    pl->waves = waves_of(packed, a->n, a->S);
+    const int CH = pl->waves * TT, GROUP = pl->waves * EACH;
     pl->q = Seqs{a->cu_seqlens, (int)a->n, (int)a->S, CH, (int)((a->S + CH - 1) / CH)};
     pl->slots = slots_of(pl->q);
-    if (!grid_fits(pl->slots * pl->tiles, 64 * WAVES)) return unsupported("the call needs more than 2^32 threads");
+    if (!grid_fits(pl->slots * pl->tiles, 64 * pl->waves)) return unsupported("the call needs more than 2^32 threads");
     pl->chunked = a->S > CH;
     // a word of every chunk and of every group's end
     pl->words = pl->chunked ? (pl->slots + pl->slots / GROUP + 1) * (long)a->D : 0;
@@ -256,17 +257,20 @@ mimo_status plan_fwd(const mamba_recur_fwd_args* a, FwdPlan* pl) {
     return MIMO_OK;
 }
 
-template <int DT, bool GATE> mimo_status run_fwd(const RecurParams& p, hipStream_t st) {
+template <int DT, bool GATE, int WAVES> mimo_status run_fwd(const RecurParams& p, hipStream_t st) {
     if (p.chunked) {
         const long blocks = (p.words + 1023) / 1024;
         const mimo_status s = launch(&k_recur_clear, dim3((unsigned)(blocks < 1024 ? blocks : 1024)), 256, 0, st, p);
         if (s != MIMO_OK) return s;
     }
-    return launch(&k_recur<DT, GATE>, dim3((unsigned)(p.slots * p.tiles)), 64 * WAVES, 0, st, p);
+    return launch(&k_recur<DT, GATE, WAVES>, dim3((unsigned)(p.slots * p.tiles)), 64 * WAVES, 0, st, p);
 }
 
-template <int DT> mimo_status run_type(const RecurParams& p, hipStream_t st) {
-    return p.has_z ? run_fwd<DT, true>(p, st) : run_fwd<DT, false>(p, st);
+template <int DT, bool GATE> mimo_status run_waves(const FwdPlan& pl, const RecurParams& p, hipStream_t st) {
+    return pl.waves == 8 ? run_fwd<DT, GATE, 8>(p, st) : pl.waves == 4 ? run_fwd<DT, GATE, 4>(p, st) : run_fwd<DT, GATE, 2>(p, st);
+}
+template <int DT> mimo_status run_type(const FwdPlan& pl, const RecurParams& p, hipStream_t st) {
+    return p.has_z ? run_waves<DT, true>(pl, p, st) : run_waves<DT, false>(pl, p, st);
 }
 
 }  // namespace
@@ -304,8 +308,8 @@ mimo_status mamba_recur_fwd(const mamba_recur_fwd_args* a, void* stream) {
     p.taken = reinterpret_cast<unsigned*>(static_cast<char*>(a->workspace) + pl.told);
     if ((s = require_gfx950()) != MIMO_OK) return s;
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    if (a->dtype == BF16) return run_type<BF16>(p, st);
-    return a->dtype == F16 ? run_type<F16>(p, st) : run_type<F32>(p, st);
+    if (a->dtype == BF16) return run_type<BF16>(pl, p, st);
+    return a->dtype == F16 ? run_type<F16>(pl, p, st) : run_type<F32>(pl, p, st);
 }
 
 mimo_status mamba_recur_step(const mamba_recur_step_args* a, void* stream) {

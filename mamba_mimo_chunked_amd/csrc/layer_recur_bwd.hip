@@ -9,10 +9,6 @@ namespace layer {
 namespace {
 
 constexpr int TT = 8;               // tokens of a wave
-// Waves of a block, and with them the tokens of a chunk: eight, or two where the sequences of a packed batch have fewer than SHORT tokens
-// in the mean, whose last chunks leave the other waves idle (16000 tokens, D = 2048, bf16: mean 8 tokens 871 us with eight, 415 with
-// two; 32: 368 and 255; 100: 258 and 226; 200: 233 and 220; 400: 212 and 215; dense [4 x 4096]: 195 and 215).
-constexpr int SHORT = 256;
 constexpr long LAST_LEVEL = 256L << 20;     // bytes of the last-level cache
 
 // A wave's tokens: the rows that are needed to the end, the gates, and b, later the state in front of a token. What is cheap to have
@@ -353,7 +349,7 @@ mimo_status plan_bwd(const mamba_recur_bwd_args* a, BwdPlan* pl) {
     const bool packed = a->cu_seqlens != nullptr;
     pl->VC = channels_of(a->D, a->dtype, packed, {&a->dout, &a->x, &a->r, &a->i, &a->z}, {a->dx, a->dr, a->di, a->dz});
     pl->tiles = (unsigned)((a->D + 64 * pl->VC - 1) / (64 * pl->VC));
-    pl->waves = packed && a->S > 8 * TT && a->S / a->n < SHORT ? 2 : 8;
+    pl->waves = waves_of(packed, a->n, a->S);
     const int CH = pl->waves * TT;
     pl->q = Seqs{a->cu_seqlens, (int)a->n, (int)a->S, CH, (int)((a->S + CH - 1) / CH)};
     pl->slots = slots_of(pl->q);
@@ -380,7 +376,7 @@ template <int DT, int VC, bool GATE, int WAVES> mimo_status run_bwd(const RecurP
     return launch(&k_recur_sums, dim3((unsigned)((3L * p.D + SUM_COLS - 1) / SUM_COLS)), 256, 0, st, p);
 }
 template <int DT, int VC, bool GATE> mimo_status run_waves(const BwdPlan& pl, const RecurParams& p, hipStream_t st) {
-    return pl.waves == 8 ? run_bwd<DT, VC, GATE, 8>(p, st) : run_bwd<DT, VC, GATE, 2>(p, st);
+    return pl.waves == 8 ? run_bwd<DT, VC, GATE, 8>(p, st) : pl.waves == 4 ? run_bwd<DT, VC, GATE, 4>(p, st) : run_bwd<DT, VC, GATE, 2>(p, st);
 }
 template <int DT> mimo_status run_type(const BwdPlan& pl, const RecurParams& p, hipStream_t st) {
     if constexpr (DT != F32) {
