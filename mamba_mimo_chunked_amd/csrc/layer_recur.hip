@@ -35,7 +35,9 @@ __global__ __launch_bounds__(256) void k_recur_clear(RecurParams p) {
 // already, and a chunk's step is told before its block waits, a group's state after waiting for lower chunks alone. cu_seqlens that
 // decrease may leave a word that nobody tells: POLLS ends the first such wait, its mark behind the counters all others, and outputs
 // are NaN. A word holds value and mark, so no fence is needed.
-template <int DT, bool GATE, int WAVES> __global__ __launch_bounds__(64 * WAVES, 6) void k_recur(RecurParams p) {
+// AUX: the policy of its accesses: past the last-level cache where the call is larger than it (bf16, D = 2048: [8 x 2048] 77 us, 80 without,
+// [1 x 8192], which is smaller, 44.6 and 46.2, but what reads the outputs next finds them there).
+template <int DT, bool GATE, int AUX, int WAVES> __global__ __launch_bounds__(64 * WAVES, 6) void k_recur(RecurParams p) {
     typedef raw_t<DT> raw;
     constexpr int CH = WAVES * TT, GROUP = WAVES * EACH;
     __shared__ float s_h[WAVES][64], s_p[WAVES][64], s_gh[WAVES][64], s_gp[WAVES][64];
@@ -65,7 +67,7 @@ template <int DT, bool GATE, int WAVES> __global__ __launch_bounds__(64 * WAVES,
     const int group = pl.j / GROUP;
     float h = group == 0 && p.init ? p.init[pl.i * D + d] : 0.f;
     if (t0 < t1) {
-        RowsOf<DT, 1, TT> rx, rr, ri, rz;
+        RowsOf<DT, 1, TT, AUX> rx, rr, ri, rz;
         float a[TT], b[TT], fold = 0.f, prod = 1.f;
         if (left > 0) {             // a short sequence leaves waves without tokens
             rx.place(p.x, pl, p.D, tw, t1), rr.place(p.r, pl, p.D, tw, t1), ri.place(p.i, pl, p.D, tw, t1);
@@ -157,7 +159,7 @@ template <int DT, bool GATE, int WAVES> __global__ __launch_bounds__(64 * WAVES,
                     const float z = to_f<DT>(rz.t[k].v[0]);
                     y[0] *= z * sigmoid(z);
                 }
-                if (k < left) store_at<DT, 1>(out, db, row, y);
+                if (k < left) store_at<DT, 1, AUX>(out, db, row, y);
                 row += step;
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -263,7 +265,9 @@ template <int DT, bool GATE, int WAVES> mimo_status run_fwd(const RecurParams& p
         const mimo_status s = launch(&k_recur_clear, dim3((unsigned)(blocks < 1024 ? blocks : 1024)), 256, 0, st, p);
         if (s != MIMO_OK) return s;
     }
-    return launch(&k_recur<DT, GATE, WAVES>, dim3((unsigned)(p.slots * p.tiles)), 64 * WAVES, 0, st, p);
+    const dim3 grid((unsigned)(p.slots * p.tiles));
+    return passes_by<DT>(p.q, p.D, GATE ? 5 : 4) ? launch(&k_recur<DT, GATE, NT, WAVES>, grid, 64 * WAVES, 0, st, p)
+                                                 : launch(&k_recur<DT, GATE, 0, WAVES>, grid, 64 * WAVES, 0, st, p);
 }
 
 template <int DT, bool GATE> mimo_status run_waves(const FwdPlan& pl, const RecurParams& p, hipStream_t st) {

@@ -173,6 +173,10 @@ inline mimo_status check_strides(std::initializer_list<const mamba_rows*> rows) 
         if (r->data && (r->token_stride < 0 || r->token_stride > MAMBA_RECUR_MAX_STRIDE)) return unsupported("token strides beyond 2^26 elements");
     return MIMO_OK;
 }
+// whether a call of so many streams is larger than the last-level cache, 256 MB
+template <int DT> bool passes_by(const Seqs& q, int D, int streams) {
+    return (q.cu ? (long)q.S : (long)q.n * q.S) * D * streams * (long)sizeof(raw_t<DT>) > 256L << 20;
+}
 // Waves of a block, and with them the tokens of a chunk. The last chunk of a packed sequence leaves some of them idle, so there are
 // fewer, and fewest where the sequences have less than 64 tokens in the mean. bf16, 16000 tokens, D = 2048, in us with 8, 4 and 2:
 //   mean length     8               32              100             200             400             dense [1 x 8192]

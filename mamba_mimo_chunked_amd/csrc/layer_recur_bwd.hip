@@ -9,7 +9,6 @@ namespace layer {
 namespace {
 
 constexpr int TT = 8;               // tokens of a wave
-constexpr long LAST_LEVEL = 256L << 20;     // bytes of the last-level cache
 
 // A wave's tokens: the rows that are needed to the end, the gates, and b, later the state in front of a token. What is cheap to have
 // again (a: one 2^x) is not kept, so that four waves a SIMD fit.
@@ -369,9 +368,8 @@ template <int DT, int VC, bool GATE, int WAVES> mimo_status run_bwd(const RecurP
         if (s != MIMO_OK) return s;
     }
     const dim3 grid((unsigned)(p.slots * p.tiles));
-    const long bytes = (p.q.cu ? (long)p.q.S : (long)p.q.n * p.q.S) * p.D * (GATE ? 9 : 7) * sizeof(raw_t<DT>);
-    const mimo_status s = bytes > LAST_LEVEL ? launch(&k_recur_bwd<DT, VC, GATE, NT, WAVES>, grid, 64 * WAVES, 0, st, p)
-                                             : launch(&k_recur_bwd<DT, VC, GATE, 0, WAVES>, grid, 64 * WAVES, 0, st, p);
+    const mimo_status s = passes_by<DT>(p.q, p.D, GATE ? 9 : 7) ? launch(&k_recur_bwd<DT, VC, GATE, NT, WAVES>, grid, 64 * WAVES, 0, st, p)
+                                                                : launch(&k_recur_bwd<DT, VC, GATE, 0, WAVES>, grid, 64 * WAVES, 0, st, p);
     if (s != MIMO_OK) return s;
     return launch(&k_recur_sums, dim3((unsigned)((3L * p.D + SUM_COLS - 1) / SUM_COLS)), 256, 0, st, p);
 }

@@ -492,6 +492,22 @@ def test_recur_gradient_larger_than_the_cache(dtype, D, S, gate):
     assert float((whole.ddecay.double() - total).norm() / total.norm()) < 300 * R.U
 
 
+@pytest.mark.parametrize("dtype,D,S,gate", [(BF, 2000, 3001, True), (HF, 517, 13001, False), (FF, 1001, 3001, True)])
+def test_recur_larger_than_the_cache(dtype, D, S, gate):
+    """A call beyond the last-level cache's size gives a sequence the bits that a call for the sequence alone gives it."""
+    g = torch.Generator(device="cuda").manual_seed(52)
+    n = 5
+    new = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x = {k: new(n, S, D).to(dtype) for k in ("x", "r", "i")}
+    x["z"] = new(n, S, D).to(dtype) if gate else None
+    x.update(decay=new(D) - 3, r_bias=None, i_bias=new(D), initial_state=new(n, D))
+    assert n * S * D * (5 if gate else 4) * x["x"].element_size() > 256 << 20
+    whole = m.mamba_recur_fwd(**x, return_state=True)
+    for k in range(n):
+        one = m.mamba_recur_fwd(**{a: v if v is None or v.dim() == 1 else v[k:k + 1] for a, v in x.items()}, return_state=True)
+        assert _same(whole.out[k:k + 1], one.out) and _same(whole.state[k:k + 1], one.state), k
+
+
 @pytest.mark.parametrize("D,S", [(8, 1 << 14)])
 def test_long_sequence_of_few_channels(D, S):
     """Many chunks of one tile, against the sequential definition."""
