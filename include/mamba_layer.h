@@ -233,8 +233,14 @@ mimo_status mamba_norm_bwd(const mamba_norm_bwd_args *args, void *stream);
  * below -87 counts as none (its softplus is below fp32's range): nothing is forgotten or
  * enters.
  *   x, r, i, z, out [.., D]; decay, r_bias, i_bias [D] (the biases optional); states
- *   [n, D] fp32. rate is not negative. Token strides: 0 to MAMBA_RECUR_MAX_STRIDE elements
- *   (forward and backward).
+ *   [n, D] fp32. rate is not negative; rate * softplus(decay) beyond 1e29 counts as
+ *   some 1e30. Token strides: 0 to MAMBA_RECUR_MAX_STRIDE elements (forward and backward).
+ * Blocks of the forward pass wait for those in front of them, with a limit: where
+ * cu_seqlens decreases, a call may take some tenths of a second and leave NaN.
+ * Workspace, in bytes, with chunks of C tokens: dense 128 forward and 64 backward, packed
+ * 64 and 32, or 32 and 16 where S / n < 64; n ceil(S / C) chunks, packed S / C + n + 1.
+ *   forward: 8 D for each chunk and for every C / 4 of them, none where S <= C
+ *   backward: 12 D for each chunk, 24 D where S > C
  */
 #define MAMBA_RECUR_MAX_STRIDE (1 << 26)
 typedef struct mamba_recur_fwd_args {

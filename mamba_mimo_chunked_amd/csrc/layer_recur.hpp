@@ -81,6 +81,8 @@ __device__ __forceinline__ void keep_and_enter(float l2, float& a, float& e2) {
 }
 __device__ __forceinline__ float root(float x) { return __builtin_amdgcn_sqrtf(x); }
 
+// From here on a step keeps nothing, and the products of l in the gradients still stay in range.
+constexpr float FASTEST = 1e30f;
 // a lane's parameters: -rate softplus(decay) log2(e), and the biases times -log2(e)
 template <int VC> struct Gates {
     float speed[VC], rb[VC], ib[VC];
@@ -91,7 +93,8 @@ template <int VC> struct Gates {
     __device__ __forceinline__ Gates(const RecurParams& p, unsigned d) {
 #pragma unroll
         for (int v = 0; v < VC; ++v) {
-            speed[v] = -p.rate * LOG2E * softplus(p.decay[d + v]);
+            const float s = p.rate * (LOG2E * softplus(p.decay[d + v]));
+            speed[v] = s > FASTEST ? -FASTEST : -s;
             rb[v] = p.rb ? -LOG2E * p.rb[d + v] : 0.f;
             ib[v] = p.ib ? -LOG2E * p.ib[d + v] : 0.f;
         }

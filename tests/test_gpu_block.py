@@ -469,6 +469,38 @@ def test_recur_with_repeated_tokens():
         assert all(_same(p, q) for p, q in zip(m.mamba_recur_bwd(dout, **a), m.mamba_recur_bwd(dout, **b)))
 
 
+@pytest.mark.parametrize("rate,decay", [(3e38, [0.0, 3.0, 50.0, 3e38, -20.0]), (8.0, [1e31, 3e38, 5e37, 1e36, 2e30])])
+def test_recur_of_decays_without_measure(rate, decay):
+    """rate softplus(decay) up to fp32's range and beyond it: nothing is kept, nothing but the token itself has a gradient, and no
+    product of zero and infinity comes up."""
+    g = _gen(43)
+    D, S = len(decay), 150
+    x = _recur_inputs(g, (2, S), 2, D, FF)
+    x["decay"] = torch.tensor(decay, device="cuda")
+    x["initial_state"] *= 1e6
+    dout, ds = _rows(g, (2, S), D, FF, False), torch.randn(2, D, generator=g).cuda()
+    o, gr = m.mamba_recur_fwd(**x, rate=rate, return_state=True), m.mamba_recur_bwd(dout, **x, dstate=ds, rate=rate)
+    v = {k: t.double() for k, t in x.items()}
+    si, sz = torch.sigmoid(v["i"] + v["i_bias"]), torch.sigmoid(v["z"])
+    h = si * v["x"]
+    dh = dout.double() * v["z"] * sz
+    dh[:, -1] += ds
+    # sigmoids of arguments below 8: (8 * 1.5 + 4) u each; up to three of them and six products
+    near = lambda a, b, size: bool(((a.double() - b).abs() <= 60 * R.U * size.abs()).all())  # noqa: E731
+    assert near(o.out, h * v["z"] * sz, h * v["z"] * sz) and near(o.state, h[:, -1], h[:, -1])
+    size = dout.double().abs() * v["z"].abs() * sz
+    size[:, -1] += ds.abs()
+    assert near(gr.dx, dh * si, size * si) and near(gr.di, dh * h * (1 - si), size * h)
+    dz = dout.double() * h
+    assert near(gr.dz, dz * (sz + v["z"] * sz * (1 - sz)), dz * (1 + v["z"].abs()))
+    for t in (gr.dr, gr.ddecay, gr.dr_bias, gr.dinitial_state):
+        assert not t.any()
+    s = torch.zeros(2, D, device="cuda")
+    one = {k: t[:, 0].contiguous() for k, t in x.items() if k in "xriz"}
+    y = m.mamba_recur_step(state=s, **one, decay=x["decay"], r_bias=x["r_bias"], i_bias=x["i_bias"], rate=rate)
+    assert _same(y, o.out[:, 0]) and near(s, h[:, 0], h[:, 0])
+
+
 @pytest.mark.parametrize("dtype,D,S,gate", [(BF, 2048, 2048, True), (HF, 2047, 2050, False), (FF, 1030, 2000, True)])
 def test_recur_gradient_larger_than_the_cache(dtype, D, S, gate):
     """A call beyond the last-level cache's size gives a sequence's gradients the bits that a call for the sequence alone gives them."""
