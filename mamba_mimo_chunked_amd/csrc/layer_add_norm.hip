@@ -52,33 +52,34 @@ template <bool WIDE> __device__ __forceinline__ void put_bytes(unsigned char* p,
     }
 }
 
-template <int DT, int ST, bool WIDE, int TPR, int IT> __global__ __launch_bounds__(block_of(TPR)) void k_add_norm(AddNormParams p) {
-    constexpr int RPB = block_of(TPR) / TPR;
+template <int DT, int ST, bool WIDE, int TPR, int IT> __global__ __launch_bounds__(most_threads(TPR)) void k_add_norm(AddNormParams p) {
+    constexpr int RPB = TPR ? 256 / (TPR ? TPR : 1) : 1;
+    const int lanes = lanes_of_row<TPR>();
     __shared__ float s_sum[16];
     __shared__ unsigned s_max[16];
-    const long item = ((long)blockIdx.y * gridDim.x + blockIdx.x) * RPB + threadIdx.x / TPR;
+    const long item = ((long)blockIdx.y * gridDim.x + blockIdx.x) * RPB + (TPR ? threadIdx.x / (TPR ? TPR : 1) : 0);
     const bool act = item < p.rows;
     const long row = act ? item : p.rows - 1;
-    const int t = threadIdx.x % TPR;
+    const int t = lane_of_row<TPR>();
     const raw_t<DT>* x = static_cast<const raw_t<DT>*>(p.x) + row * p.xs;
     Eight<DT, WIDE> rx[IT];
     Eight<ST, WIDE> rr[IT];
     Eight<F32, WIDE> rw[IT];
 #pragma unroll
-    for (int k = 0; k < IT; ++k) rx[k].fetch(x, (t + k * TPR) * NV, p.D);
+    for (int k = 0; k < IT; ++k) rx[k].fetch(x, (t + k * lanes) * NV, p.D);
     if (p.res) {
 #pragma unroll
-        for (int k = 0; k < IT; ++k) rr[k].fetch(static_cast<const raw_t<ST>*>(p.res) + row * p.rs, (t + k * TPR) * NV, p.D);
+        for (int k = 0; k < IT; ++k) rr[k].fetch(static_cast<const raw_t<ST>*>(p.res) + row * p.rs, (t + k * lanes) * NV, p.D);
     }
 #pragma unroll
-    for (int k = 0; k < IT; ++k) rw[k].fetch(p.w, (t + k * TPR) * NV, p.D);
+    for (int k = 0; k < IT; ++k) rw[k].fetch(p.w, (t + k * lanes) * NV, p.D);
     float v[IT][NV];
 #pragma unroll
-    for (int k = 0; k < IT; ++k) rx[k].read((t + k * TPR) * NV, p.D, v[k]);
+    for (int k = 0; k < IT; ++k) rx[k].read((t + k * lanes) * NV, p.D, v[k]);
     if (p.drop) {
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
-            const unsigned keep = kept8(p.seed, t + k * TPR, (unsigned)row, p.drop);
+            const unsigned keep = kept8(p.seed, t + k * lanes, (unsigned)row, p.drop);
 #pragma unroll
             for (int i = 0; i < NV; ++i) v[k][i] = keep >> i & 1 ? v[k][i] * p.factor : 0.f;
         }
@@ -87,7 +88,7 @@ template <int DT, int ST, bool WIDE, int TPR, int IT> __global__ __launch_bounds
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
             float r[NV];
-            rr[k].read((t + k * TPR) * NV, p.D, r);
+            rr[k].read((t + k * lanes) * NV, p.D, r);
 #pragma unroll
             for (int i = 0; i < NV; ++i) v[k][i] += r[i];
         }
@@ -99,13 +100,13 @@ template <int DT, int ST, bool WIDE, int TPR, int IT> __global__ __launch_bounds
         for (int i = 0; i < NV; ++i) q = __builtin_fmaf(v[k][i], v[k][i], q);
     if (p.sum && act) {
 #pragma unroll
-        for (int k = 0; k < IT; ++k) put8<ST, WIDE>(static_cast<raw_t<ST>*>(p.sum) + row * p.D, (t + k * TPR) * NV, p.D, v[k]);
+        for (int k = 0; k < IT; ++k) put8<ST, WIDE>(static_cast<raw_t<ST>*>(p.sum) + row * p.D, (t + k * lanes) * NV, p.D, v[k]);
     }
     unsigned top[IT] = {};
 #pragma unroll
     for (int k = 0; k < IT; ++k) {
         float w[NV];
-        rw[k].read((t + k * TPR) * NV, p.D, w);
+        rw[k].read((t + k * lanes) * NV, p.D, w);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             v[k][i] *= w[i];
@@ -115,12 +116,12 @@ template <int DT, int ST, bool WIDE, int TPR, int IT> __global__ __launch_bounds
     if (p.kind != MAMBA_OUT_SAME) {
         if (p.block) {
 #pragma unroll
-            for (int k = 0; k < IT; ++k) top[k] = max_lanes(top[k], min(p.block / NV, TPR < 64 ? TPR : 64));
+            for (int k = 0; k < IT; ++k) top[k] = max_lanes(top[k], min(p.block / NV, TPR && TPR < 64 ? TPR : 64));
         } else {
 #pragma unroll
             for (int k = 1; k < IT; ++k) top[0] = larger(top[0], top[k]);
-            top[0] = max_lanes(top[0], TPR < 64 ? TPR : 64);
-            if (TPR > 64 && (threadIdx.x & 63) == 0) s_max[threadIdx.x >> 6] = top[0];
+            top[0] = max_lanes(top[0], TPR && TPR < 64 ? TPR : 64);
+            if ((TPR == 0 || TPR > 64) && (threadIdx.x & 63) == 0) s_max[threadIdx.x >> 6] = top[0];
         }
     }
     q = sum_row<TPR>(q, s_sum) * p.inv;     // its barrier also serves s_max
@@ -132,22 +133,19 @@ template <int DT, int ST, bool WIDE, int TPR, int IT> __global__ __launch_bounds
         for (int i = 0; i < NV; ++i) v[k][i] *= r;
     if (p.kind == MAMBA_OUT_SAME) {
 #pragma unroll
-        for (int k = 0; k < IT; ++k) put8<DT, WIDE>(static_cast<raw_t<DT>*>(p.out) + row * p.D, (t + k * TPR) * NV, p.D, v[k]);
+        for (int k = 0; k < IT; ++k) put8<DT, WIDE>(static_cast<raw_t<DT>*>(p.out) + row * p.D, (t + k * lanes) * NV, p.D, v[k]);
         return;
     }
     if (p.block == 0) {
-        if constexpr (TPR > 64) {
-            const int first = threadIdx.x / TPR * (TPR / 64);
-#pragma unroll
-            for (int k = 0; k < TPR / 64; ++k) top[0] = larger(top[0], s_max[first + k]);
-        }
+        if constexpr (TPR == 128) top[0] = larger(s_max[threadIdx.x >> 7 << 1], s_max[(threadIdx.x >> 7 << 1) + 1]);
+        if constexpr (TPR == 0) top[0] = max_lanes((threadIdx.x & 15) < blockDim.x >> 6 ? s_max[threadIdx.x & 15] : 0u, 16);
 #pragma unroll
         for (int k = 1; k < IT; ++k) top[k] = top[0];
     }
     const float most = p.kind == MAMBA_OUT_E4M3 ? 448.f : 127.f;
 #pragma unroll
     for (int k = 0; k < IT; ++k) {
-        const int c = (t + k * TPR) * NV;
+        const int c = (t + k * lanes) * NV;
         float m = __uint_as_float(top[k]) * r;
         const bool fine = m < __builtin_inff();     // false for NaN too
         m = m < LEAST ? LEAST : m;
@@ -181,11 +179,11 @@ struct Run {
         AddNormParams p;
         hipStream_t st;
         template <int TPR, int IT> mimo_status operator()() {
-            constexpr int per = block_of(TPR) / TPR;
+            const RowShape shape = shape_of(p.D);
             // in more than one row of blocks where they are too many for one
-            const long blocks = (p.rows + per - 1) / per, most = 0xffffffffL / block_of(TPR), along = blocks < most ? blocks : most;
-            return launch(&k_add_norm<DT, ST, WIDE, TPR, IT>, dim3((unsigned)along, (unsigned)((blocks + along - 1) / along)), block_of(TPR), 0,
-                          st, p);
+            const long blocks = (p.rows + shape.rows - 1) / shape.rows, most = 0xffffffffL / shape.threads, along = blocks < most ? blocks : most;
+            return launch(&k_add_norm<DT, ST, WIDE, TPR, IT>, dim3((unsigned)along, (unsigned)((blocks + along - 1) / along)), shape.threads,
+                          0, st, p);
         }
     };
 };

@@ -3,9 +3,11 @@
 //   v = dropout(x) + residual;  r = 1 / sqrt(mean(v^2) + eps);  y = v r w
 //   backward: q = dout w;  hat = v r;  dv = r (q - hat mean(q hat)) + dsum;  dw = sum dout hat;  dx = dropout(dv)
 //
-// TPR threads share a row; thread t takes the eight columns from 8 t on (and 8 TPR further on, where a row needs more
-// than 1024 threads), whatever the types: 16 bytes of a 16-bit type, twice 16 of fp32, 8 of an 8-bit output, and the
-// eight elements that one counter of the generator covers. Rows that allow no 16-byte access take elements of their own.
+// A row belongs to TPR = 8, 16, 32, 64 or 128 lanes, or (TPR = 0) to the whole block, of up to 16 waves; thread t takes the eight columns from 8 t
+// on (and, in rows beyond 8192 columns, 8 threads further on), whatever the types: 16 bytes of a 16-bit type, twice 16 of fp32, 8 of an 8-bit
+// output, and the eight elements that one counter of the generator covers. A row has as few lanes as it needs, as idle ones cost as much as
+// others. bf16, 16.8 M elements, backward, us: 64 columns by 8 lanes 29.5, by 16 41.3; 256 by 32 29.2, by 64 42.9; 2056 by 5 waves 34.5, by 8
+// 45.3; 4104 by 9 waves 32.2, by 16 57. Rows of two waves are two to a block ([16384, 1000]: 30.3, one by one 34.8).
 #pragma once
 #include "layer.hpp"
 
@@ -14,22 +16,22 @@ namespace layer {
 
 constexpr int NV = 8;   // columns of a thread's access
 
-// the sum over the TPR threads of a row, in all of them; `s`: LDS of a float a wave, safe to use again after the
+template <int TPR> __device__ __forceinline__ int lane_of_row() { return TPR ? threadIdx.x % (TPR ? TPR : 1) : threadIdx.x; }
+template <int TPR> __device__ __forceinline__ int lanes_of_row() { return TPR ? TPR : blockDim.x; }
+// the sum over the threads of a row, in all of them; `s`: LDS of a float a wave, safe to use again after the
 // next call on another one
 template <int TPR> __device__ __forceinline__ float sum_row(float x, float* s) {
-    if constexpr (TPR <= 64) return sum_wave<TPR>(x);
+    if constexpr (TPR && TPR <= 64) return sum_wave<TPR>(x);
     else {
         x = sum_wave<64>(x);
         if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = x;
         __syncthreads();
-        const int first = threadIdx.x / TPR * (TPR / 64);
-        x = 0.f;
-#pragma unroll
-        for (int k = 0; k < TPR / 64; ++k) x += s[first + k];
-        return x;
+        const unsigned k = threadIdx.x & 15;
+        if constexpr (TPR) return s[threadIdx.x >> 7 << 1] + s[(threadIdx.x >> 7 << 1) + 1];
+        else return sum_wave<16>(k < blockDim.x >> 6 ? s[k] : 0.f);
     }
 }
-constexpr int block_of(int TPR) { return TPR < 256 ? 256 : TPR; }
+constexpr int most_threads(int TPR) { return TPR ? 256 : 1024; }
 
 // Eight neighbouring elements from column c of a row of D on, zeros behind the row. WIDE: rows of whole, aligned 16-byte accesses.
 // Else accesses of 16 bytes at any element's address, which global memory takes; the row's last, broken eight are read as the
@@ -114,20 +116,26 @@ __device__ __forceinline__ unsigned kept8(const long* seed, unsigned c, unsigned
 }
 
 // ---------------------------------------------------------------- host side
-// Threads of a row: one access each where 1024 threads allow it, 16 or whole waves.
+// f<TPR, accesses a thread>
 template <class F> mimo_status with_row(int64_t D, F f) {
     const int64_t nv = (D + NV - 1) / NV;
+    if (nv <= 8) return f.template operator()<8, 1>();
     if (nv <= 16) return f.template operator()<16, 1>();
+    if (nv <= 32) return f.template operator()<32, 1>();
     if (nv <= 64) return f.template operator()<64, 1>();
     if (nv <= 128) return f.template operator()<128, 1>();
-    if (nv <= 256) return f.template operator()<256, 1>();
-    if (nv <= 512) return f.template operator()<512, 1>();
-    if (nv <= 1024) return f.template operator()<1024, 1>();
-    return f.template operator()<1024, 2>();
+    if (nv <= 1024) return f.template operator()<0, 1>();
+    return f.template operator()<0, 2>();
 }
-inline int row_threads(int64_t D) {
-    const int64_t nv = (D + NV - 1) / NV;
-    return nv <= 16 ? 16 : nv <= 64 ? 64 : nv <= 128 ? 128 : nv <= 256 ? 256 : nv <= 512 ? 512 : 1024;
+// threads of a block, and its rows
+struct RowShape {
+    int threads, rows;
+};
+inline RowShape shape_of(int64_t D) {
+    const int nv = (int)((D + NV - 1) / NV);
+    if (nv <= 128) return {256, nv <= 8 ? 32 : nv <= 16 ? 16 : nv <= 32 ? 8 : nv <= 64 ? 4 : 2};
+    const int each = nv <= 1024 ? 1 : 2;
+    return {(nv + 64 * each - 1) / (64 * each) * 64, 1};
 }
 // f<type of the data, type of the stream, wide accesses>
 template <class F> mimo_status with_types(int dtype, int wide_stream, bool even, F f) {

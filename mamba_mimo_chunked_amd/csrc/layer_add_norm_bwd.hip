@@ -19,17 +19,53 @@ struct AddNormBwdParams {
     float *part, *dw;               // part: [nblk][D]
 };
 
-template <int DT, int ST, bool WIDE, int TPR, int IT> __global__ __launch_bounds__(block_of(TPR)) void k_add_norm_bwd(AddNormBwdParams p) {
-    constexpr int RPB = block_of(TPR) / TPR;
+typedef float f4v __attribute__((ext_vector_type(4)));
+// Eight floats of a thread for each of its accesses: in registers, or, where it has two (1024 threads, 128 registers each), in LDS of its own
+// ([1024, 16384] bf16 42 us; with registers in scratch memory, and half as many blocks, 87).
+template <int IT> struct Held {
+    float v[IT][NV];
+    __device__ __forceinline__ void put(f4v*, int k, const float (&x)[NV]) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[k][i] = x[i];
+    }
+    __device__ __forceinline__ void get(const f4v*, int k, float (&x)[NV]) const {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) x[i] = v[k][i];
+    }
+};
+template <> struct Held<2> {
+    __device__ __forceinline__ void put(f4v* s, int k, const float (&x)[NV]) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) s[(2 * k + j) * 1024 + threadIdx.x] = f4v{x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]};
+    }
+    __device__ __forceinline__ void get(const f4v* s, int k, float (&x)[NV]) const {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const f4v q = s[(2 * k + j) * 1024 + threadIdx.x];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[4 * j + i] = q[i];
+        }
+    }
+};
+
+template <int DT, int ST, bool WIDE, int TPR, int IT> __global__ __launch_bounds__(most_threads(TPR)) void k_add_norm_bwd(AddNormBwdParams p) {
+    constexpr int RPB = TPR ? 256 / (TPR ? TPR : 1) : 1;
+    // fp32 [8192, 2047] 52 us, 65 without; bf16 [1024, 16384] 42 and 46; but bf16 [4100, 4096] with dropout 46 and 40
+    constexpr bool LATE = !WIDE || IT == 2;
     __shared__ float s[2][16];
     __shared__ float s_dw[RPB > 1 ? RPB * TPR * NV : 1];
-    const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-    float w[IT][NV], dw[IT][NV] = {};
+    __shared__ f4v s_w[IT == 2 ? 4096 : 1], s_sum[IT == 2 ? 4096 : 1];
+    const int t = lane_of_row<TPR>(), lanes = lanes_of_row<TPR>(), sub = TPR ? threadIdx.x / (TPR ? TPR : 1) : 0;
+    Held<IT> w, dw;
 #pragma unroll
     for (int k = 0; k < IT; ++k) {
         Eight<F32, WIDE> rw;
-        rw.fetch(p.w, (t + k * TPR) * NV, p.D);
-        rw.read((t + k * TPR) * NV, p.D, w[k]);
+        float x[NV];
+        const float zero[NV] = {};
+        rw.fetch(p.w, (t + k * lanes) * NV, p.D);
+        rw.read((t + k * lanes) * NV, p.D, x);
+        w.put(s_w, k, x);
+        dw.put(s_sum, k, zero);
     }
     Eight<ST, WIDE> rv[IT], rs[IT];
     Eight<DT, WIDE> rg[IT];
@@ -37,49 +73,66 @@ template <int DT, int ST, bool WIDE, int TPR, int IT> __global__ __launch_bounds
         row = row < p.rows ? row : p.rows - 1;
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
-            const int c = (t + k * TPR) * NV;
+            const int c = (t + k * lanes) * NV;
             rv[k].fetch(static_cast<const raw_t<ST>*>(p.sum) + row * p.ss, c, p.D);
             rg[k].fetch(static_cast<const raw_t<DT>*>(p.dout) + row * p.gs, c, p.D);
-            if (p.dsum) rs[k].fetch(static_cast<const raw_t<ST>*>(p.dsum) + row * p.ds, c, p.D);
+        }
+    };
+    // dsum, which a row needs last: asked for with the others, or, for the registers' sake, when the row before is done
+    auto fetch_dsum = [&](long row) {
+        row = row < p.rows ? row : p.rows - 1;
+        if (p.dsum) {
+#pragma unroll
+            for (int k = 0; k < IT; ++k) rs[k].fetch(static_cast<const raw_t<ST>*>(p.dsum) + row * p.ds, (t + k * lanes) * NV, p.D);
         }
     };
     const long step = (long)gridDim.x * RPB;
     fetch((long)blockIdx.x * RPB + sub);
+    fetch_dsum((long)blockIdx.x * RPB + sub);
     for (long row0 = (long)blockIdx.x * RPB; row0 < p.rows; row0 += step) {
         const bool act = row0 + sub < p.rows;
         const long row = act ? row0 + sub : p.rows - 1;
         unsigned keep[IT];
         if (p.drop) {
 #pragma unroll
-            for (int k = 0; k < IT; ++k) keep[k] = kept8(p.seed, t + k * TPR, (unsigned)row, p.drop);
+            for (int k = 0; k < IT; ++k) keep[k] = kept8(p.seed, t + k * lanes, (unsigned)row, p.drop);
         }
         float v[IT][NV], g[IT][NV], d[IT][NV] = {}, q = 0.f, m = 0.f;
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
-            rv[k].read((t + k * TPR) * NV, p.D, v[k]);
-            rg[k].read((t + k * TPR) * NV, p.D, g[k]);
-            if (p.dsum) rs[k].read((t + k * TPR) * NV, p.D, d[k]);
+            rv[k].read((t + k * lanes) * NV, p.D, v[k]);
+            rg[k].read((t + k * lanes) * NV, p.D, g[k]);
+            if (!LATE && p.dsum) rs[k].read((t + k * lanes) * NV, p.D, d[k]);
 #pragma unroll
             for (int i = 0; i < NV; ++i) q = __builtin_fmaf(v[k][i], v[k][i], q);
         }
-        if (row0 + step < p.rows) fetch(row0 + step + sub);
+        if (row0 + step < p.rows) {
+            fetch(row0 + step + sub);
+            if (!LATE) fetch_dsum(row0 + step + sub);
+        }
         q = sum_row<TPR>(q, s[0]) * p.inv;
         const float r = 1.f / __builtin_sqrtf(q + p.eps);
 #pragma unroll
-        for (int k = 0; k < IT; ++k)
+        for (int k = 0; k < IT; ++k) {
+            float ww[NV], sum[NV];
+            w.get(s_w, k, ww);
+            dw.get(s_sum, k, sum);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 v[k][i] *= r;
-                if (act) dw[k][i] = __builtin_fmaf(g[k][i], v[k][i], dw[k][i]);
-                g[k][i] *= w[k][i];
+                if (act) sum[i] = __builtin_fmaf(g[k][i], v[k][i], sum[i]);
+                g[k][i] *= ww[i];
                 m = __builtin_fmaf(g[k][i], v[k][i], m);
             }
+            dw.put(s_sum, k, sum);
+        }
         m = sum_row<TPR>(m, s[1]) * p.inv;
         if (!act) continue;
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
-            const int c = (t + k * TPR) * NV;
+            const int c = (t + k * lanes) * NV;
             float dv[NV];
+            if (LATE && p.dsum) rs[k].read(c, p.D, d[k]);
 #pragma unroll
             for (int i = 0; i < NV; ++i) dv[i] = __builtin_fmaf(r, __builtin_fmaf(-v[k][i], m, g[k][i]), d[k][i]);
             if (p.dres) put8<ST, WIDE>(static_cast<raw_t<ST>*>(p.dres) + row * p.D, c, p.D, dv);
@@ -89,25 +142,28 @@ template <int DT, int ST, bool WIDE, int TPR, int IT> __global__ __launch_bounds
             }
             put8<DT, WIDE>(static_cast<raw_t<DT>*>(p.dx) + row * p.D, c, p.D, dv);
         }
+        if (LATE && row0 + step < p.rows) fetch_dsum(row0 + step + sub);
     }
     float* part = p.part + (long)blockIdx.x * p.D;
 #pragma unroll
     for (int k = 0; k < IT; ++k) {
-        const int c = (t + k * TPR) * NV;
+        const int c = (t + k * lanes) * NV;
+        float sum[NV];
+        dw.get(s_sum, k, sum);
         if constexpr (RPB > 1) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) s_dw[threadIdx.x * NV + i] = dw[k][i];
+            for (int i = 0; i < NV; ++i) s_dw[threadIdx.x * NV + i] = sum[i];
             __syncthreads();
             if (sub == 0) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
-                    for (int y = 1; y < RPB; ++y) dw[k][i] += s_dw[(y * TPR + t) * NV + i];
+                    for (int y = 1; y < RPB; ++y) sum[i] += s_dw[(y * TPR + t) * NV + i];
             }
         }
         if (sub == 0) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (c + i < p.D) part[c + i] = dw[k][i];
+                if (c + i < p.D) part[c + i] = sum[i];
         }
     }
 }
@@ -116,10 +172,10 @@ __global__ __launch_bounds__(256) void k_add_norm_sums(AddNormBwdParams p) {
     column_sums(p.part, p.D, p.nblk, (long)blockIdx.x * SUM_COLS, p.D, [&](long col, float s) { p.dw[col] = s; });
 }
 
-// blocks: 512 threads a CU in all, none without a row of its own
+// blocks: as many a CU as have 512 threads, none without a row of its own
 int64_t blocks_of(const mamba_add_norm_bwd_args* a) {
-    const int lanes = row_threads(a->D), threads = block_of(lanes), per = threads / lanes;
-    const int64_t want = 256 * 512 / threads, have = (a->rows + per - 1) / per;
+    const RowShape shape = shape_of(a->D);
+    const int64_t want = 256 * ((511 + shape.threads) / shape.threads), have = (a->rows + shape.rows - 1) / shape.rows;
     return have < want ? have : want;
 }
 
@@ -133,7 +189,7 @@ struct Run {
         AddNormBwdParams p;
         hipStream_t st;
         template <int TPR, int IT> mimo_status operator()() {
-            const mimo_status s = launch(&k_add_norm_bwd<DT, ST, WIDE, TPR, IT>, dim3(p.nblk), block_of(TPR), 0, st, p);
+            const mimo_status s = launch(&k_add_norm_bwd<DT, ST, WIDE, TPR, IT>, dim3(p.nblk), shape_of(p.D).threads, 0, st, p);
             if (s != MIMO_OK) return s;
             return launch(&k_add_norm_sums, dim3((unsigned)((p.D + SUM_COLS - 1) / SUM_COLS)), 256, 0, st, p);
         }

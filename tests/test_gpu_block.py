@@ -167,6 +167,9 @@ NORM = [  # dtype, stream, leading axes, D, residual, dropout, strided
     (BF, FF, (2,), 16381, True, 0.0, True), (BF, BF, (19,), 40, True, 0.3, False), (BF, FF, (6,), 72, True, 0.1, False), (HF, HF, (4,), 65, False, 0.5, True),
     (FF, FF, (3,), 260, True, 0.9, False), (BF, BF, (2,), 520, False, 0.1, False), (FF, FF, (700,), 24, True, 0.0, False), (BF, BF, (5000,), 16, True, 0.0, False),
     (HF, FF, (300,), 200, True, 0.25, False),
+    # blocks of 3, 5, 9 and 16 waves that take several rows each, and rows of two accesses a thread
+    (BF, BF, (1700,), 1100, True, 0.0, False), (HF, FF, (1300,), 2056, True, 0.1, False), (BF, BF, (600,), 4104, True, 0.2, False),
+    (FF, FF, (520,), 8190, True, 0.0, True), (BF, FF, (530,), 8200, True, 0.1, False), (FF, FF, (600,), 8201, True, 0.0, False),
 ]
 SEED = (0x1234567_89ABCDEF, -0x0FEDCBA9_87654321)
 
@@ -213,7 +216,7 @@ def test_add_norm(dtype, stream, lead, D, add, drop, strided):
 
 
 @pytest.mark.parametrize("dtype,D,lead", [(BF, 64, (3,)), (HF, 1003, (5,)), (FF, 300, (4,)), (BF, 2048, (9,)), (FF, 33, (2, 2)), (BF, 8200, (2,)), (HF, 16384, (1,)),
-                                          (BF, 1, (3,)), (BF, 640, (17,)), (HF, 100, (50,))])
+                                          (BF, 1, (3,)), (BF, 640, (17,)), (HF, 100, (50,)), (BF, 1100, (6,)), (FF, 2056, (3,)), (BF, 8192, (2,)), (HF, 256, (11,))])
 @pytest.mark.parametrize("kind", [E4, I8])
 def test_add_norm_in_8_bits(dtype, D, lead, kind):
     g = _gen(D)
