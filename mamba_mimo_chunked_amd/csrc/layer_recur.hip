@@ -246,7 +246,7 @@ mimo_status plan_fwd(const mamba_recur_fwd_args* a, FwdPlan* pl) {
     if (s != MIMO_OK || (s = check_strides({&a->x, &a->r, &a->i, &a->z})) != MIMO_OK) return s;
     const bool packed = a->cu_seqlens != nullptr;
     pl->tiles = (unsigned)((a->D + 63) / 64);
-    pl->waves = waves_of(packed, a->n, a->S);
+    pl->waves = waves_of(packed, a->n, a->S, TT);
     const int CH = pl->waves * TT, GROUP = pl->waves * EACH;
     pl->q = Seqs{a->cu_seqlens, (int)a->n, (int)a->S, CH, (int)((a->S + CH - 1) / CH)};
     pl->slots = slots_of(pl->q);

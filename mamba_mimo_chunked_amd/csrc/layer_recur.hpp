@@ -176,16 +176,22 @@ inline mimo_status check_strides(std::initializer_list<const mamba_rows*> rows) 
         if (r->data && (r->token_stride < 0 || r->token_stride > MAMBA_RECUR_MAX_STRIDE)) return unsupported("token strides beyond 2^26 elements");
     return MIMO_OK;
 }
-// whether a call of so many streams is larger than the last-level cache, 256 MB
+// Whether a call of so many streams passes the last-level cache by: it is larger than it, 256 MB, and its rows are whole lines of 128 bytes
+// (parts of lines that nothing keeps are fetched again: [16384, 1001] backward, bf16, 194 us past the cache, 164 through it, fp32 266 and 253).
 template <int DT> bool passes_by(const Seqs& q, int D, int streams) {
-    return (q.cu ? (long)q.S : (long)q.n * q.S) * D * streams * (long)sizeof(raw_t<DT>) > 256L << 20;
+    const long row = (long)D * sizeof(raw_t<DT>);
+    return row % 128 == 0 && (q.cu ? (long)q.S : (long)q.n * q.S) * row * streams > 256L << 20;
 }
-// Waves of a block, and with them the tokens of a chunk. The last chunk of a packed sequence leaves some of them idle, so there are
-// fewer, and fewest where the sequences have less than 64 tokens in the mean. bf16, 16000 tokens, D = 2048, in us with 8, 4 and 2:
+// Waves of a block of TT tokens each, and with them the tokens of a chunk. The last chunk of a packed sequence leaves some of them idle, so
+// there are fewer, and fewest where the sequences have less than 64 tokens in the mean; short dense sequences have one chunk that fits.
+// bf16, 16000 tokens, D = 2048, in us with 8, 4 and 2:
 //   mean length     8               32              100             200             400             dense [1 x 8192]
 //   forward     555 312 203     192 131 110     120  97  97     104  91  97      94  88  96      47  47  61
 //   backward    877 547 418     372 283 257     260 225 227     234 217 222     215 206 219     102 109 118
-inline int waves_of(bool packed, int64_t n, int64_t S) { return !packed ? 8 : S / n < 64 ? 2 : 4; }
+inline int waves_of(bool packed, int64_t n, int64_t S, int TT) {
+    if (packed) return S / n < 64 ? 2 : 4;
+    return S <= 2 * TT ? 2 : S <= 4 * TT ? 4 : 8;
+}
 // channels of a lane: four bytes of them where all data allows
 inline int channels_of(int64_t D, int dtype, bool packed, std::initializer_list<const mamba_rows*> rows, std::initializer_list<const void*> dense) {
     bool two = dtype != F32 && D % 2 == 0;

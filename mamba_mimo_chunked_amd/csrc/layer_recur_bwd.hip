@@ -348,7 +348,7 @@ mimo_status plan_bwd(const mamba_recur_bwd_args* a, BwdPlan* pl) {
     const bool packed = a->cu_seqlens != nullptr;
     pl->VC = channels_of(a->D, a->dtype, packed, {&a->dout, &a->x, &a->r, &a->i, &a->z}, {a->dx, a->dr, a->di, a->dz});
     pl->tiles = (unsigned)((a->D + 64 * pl->VC - 1) / (64 * pl->VC));
-    pl->waves = waves_of(packed, a->n, a->S);
+    pl->waves = waves_of(packed, a->n, a->S, TT);
     const int CH = pl->waves * TT;
     pl->q = Seqs{a->cu_seqlens, (int)a->n, (int)a->S, CH, (int)((a->S + CH - 1) / CH)};
     pl->slots = slots_of(pl->q);

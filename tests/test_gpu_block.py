@@ -504,7 +504,7 @@ def test_recur_of_decays_without_measure(rate, decay):
     assert _same(y, o.out[:, 0]) and near(s, h[:, 0], h[:, 0])
 
 
-@pytest.mark.parametrize("dtype,D,S,gate", [(BF, 2048, 2048, True), (HF, 2047, 2050, False), (FF, 1030, 2000, True)])
+@pytest.mark.parametrize("dtype,D,S,gate", [(BF, 2048, 2048, True), (HF, 2047, 2050, False), (FF, 1030, 2000, True), (FF, 1024, 2010, False), (HF, 1984, 2050, False)])
 def test_recur_gradient_larger_than_the_cache(dtype, D, S, gate):
     """A call beyond the last-level cache's size gives a sequence's gradients the bits that a call for the sequence alone gives them."""
     g = torch.Generator(device="cuda").manual_seed(51)
@@ -527,7 +527,7 @@ def test_recur_gradient_larger_than_the_cache(dtype, D, S, gate):
     assert float((whole.ddecay.double() - total).norm() / total.norm()) < 300 * R.U
 
 
-@pytest.mark.parametrize("dtype,D,S,gate", [(BF, 2000, 3001, True), (HF, 517, 13001, False), (FF, 1001, 3001, True)])
+@pytest.mark.parametrize("dtype,D,S,gate", [(BF, 1984, 3001, True), (HF, 517, 13001, False), (FF, 1001, 3001, True), (FF, 1056, 3201, False), (HF, 704, 10001, False)])
 def test_recur_larger_than_the_cache(dtype, D, S, gate):
     """A call beyond the last-level cache's size gives a sequence the bits that a call for the sequence alone gives it."""
     g = torch.Generator(device="cuda").manual_seed(52)
