@@ -1,6 +1,7 @@
 // Addition to the residual stream and root-mean-square norm of the sum, forward (what it shares with the backward
 // pass: layer_add_norm.hpp). A row's values stay in registers between the sum of squares and the output, so each input
-// is read once and each output written once: memory binds, for single rows the launch.
+// is read once and each output written once: memory binds ([8192, 2048] bf16 with a stream in fp32, to e4m3 with scales: 33 us, 5.5 TB/s),
+// for single rows the launch.
 //
 // 8 bits: the largest |v w| of a block of columns joins the same exchange between waves as the sum of squares, and
 // times r it is the largest |y|, as rounding keeps the order. Largest values are compared as bit patterns, in which a

@@ -36,7 +36,7 @@ constexpr int most_threads(int TPR) { return TPR ? 256 : 1024; }
 // Eight neighbouring elements from column c of a row of D on, zeros behind the row. WIDE: rows of whole, aligned 16-byte accesses.
 // Else accesses of 16 bytes at any element's address, which global memory takes; the row's last, broken eight are read as the
 // row's last eight elements and moved into place when they are used, so that no lane reads otherwise than its neighbours ([8192, 2047]
-// bf16 with a stream in fp32 and dropout, forward: 45 us, 123 with single elements).
+// bf16 with a stream in fp32 and dropout, forward: 42 us, 123 with single elements).
 template <class V, int ESZ> struct Loose { typedef V __attribute__((aligned(ESZ))) type; };
 typedef unsigned quad __attribute__((ext_vector_type(4)));
 template <int DT, bool WIDE> struct Eight {

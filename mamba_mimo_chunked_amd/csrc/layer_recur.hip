@@ -35,6 +35,8 @@ __global__ __launch_bounds__(256) void k_recur_clear(RecurParams p) {
 // already, and a chunk's step is told before its block waits, a group's state after waiting for lower chunks alone. cu_seqlens that
 // decrease may leave a word that nobody tells: POLLS ends the first such wait, its mark behind the counters all others, and outputs
 // are NaN. A word holds value and mark, so no fence is needed.
+// [8192, 2048] bf16: 42 us, 4.0 TB/s, vector units 45 % busy; in two passes over the inputs 82. What is left is that a block loads, joins,
+// waits and walks one after the other, with three blocks of 79 registers on a CU.
 // AUX: the policy of its accesses: past the last-level cache where the call is larger than it (bf16, D = 2048: [8 x 2048] 77 us, 80 without,
 // [1 x 8192], which is smaller, 44.6 and 46.2, but what reads the outputs next finds them there).
 template <int DT, bool GATE, int AUX, int WAVES> __global__ __launch_bounds__(64 * WAVES, 6) void k_recur(RecurParams p) {
@@ -177,7 +179,7 @@ struct StepParams {
 };
 
 // One token of row blockIdx.y, a thread a lane's channels. Everything it reads is asked for before the index is looked at: the
-// chain from a row's index to its store is what a wave waits for.
+// chain from a row's index to its store is what a wave waits for. One row of 1024 channels 3.0 us, 128 of 2048 from a pool 4.4.
 template <int DT, int VC> __global__ __launch_bounds__(256) void k_recur_step(StepParams s) {
     typedef raw_t<DT> raw;
     const RecurParams& p = s.p;
