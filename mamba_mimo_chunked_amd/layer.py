@@ -737,7 +737,7 @@ def mamba_add_norm_fwd(x, weight, residual=None, *, eps: float = 1e-5, dropout: 
         res = x.new_empty(x.shape, dtype=out_dtype) if kind else _new_like(x)
     else:
         _check_output("out", out, x.shape, out_dtype if kind else dtype, dev)
-        _apart("out", out, x=rows, residual=rr, weight=weight, seed=seed)
+        _apart("out", out, x=x, residual=rr, weight=weight, seed=seed)
         res = out
     kept = residual is None and not drop and stream == dtype
     total = x if kept else x.new_empty(x.shape, dtype=stream)

@@ -157,3 +157,11 @@ def test_overlaps_of_the_addition(on_cpu):  # noqa: F811
     a, seed = _addb(), Z(2, dtype=torch.int64)
     with pytest.raises(ValueError, match="workspace must not overlap seed"):
         m.mamba_add_norm_bwd(**a, dropout=0.1, seed=seed, workspace=_over(seed))
+
+
+def test_output_over_the_sum_that_is_x(on_cpu):  # noqa: F811
+    """Where nothing is added the sum is x itself, whose rows are copied for the call if their strides need it."""
+    buf = Z(96)
+    x = buf.view(3, 4, 8)[:, :3]
+    with pytest.raises(ValueError, match="out must not overlap x"):
+        m.mamba_add_norm_fwd(x, Z(8), out=buf[:72].view(3, 3, 8))
