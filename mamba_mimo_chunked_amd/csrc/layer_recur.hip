@@ -37,7 +37,7 @@ __global__ __launch_bounds__(256) void k_recur_clear(RecurParams p) {
 // are NaN. A word holds value and mark, so no fence is needed.
 // [8192, 2048] bf16: 42 us, 4.0 TB/s, vector units 45 % busy; in two passes over the inputs 82. What is left is that a block loads, joins,
 // waits and walks one after the other, with three blocks of 79 registers on a CU.
-// AUX: the policy of its accesses: past the last-level cache where the call is larger than it (bf16, D = 2048: [8 x 2048] 77 us, 80 without,
+// AUX: the policy of its accesses: past the last-level cache where the call is larger than it (bf16, D = 2048: [8 x 2048] 75 us, 78 without,
 // [1 x 8192], which is smaller, 44.6 and 46.2, but what reads the outputs next finds them there).
 template <int DT, bool GATE, int AUX, int WAVES> __global__ __launch_bounds__(64 * WAVES, 6) void k_recur(RecurParams p) {
     typedef raw_t<DT> raw;
@@ -76,10 +76,6 @@ template <int DT, bool GATE, int AUX, int WAVES> __global__ __launch_bounds__(64
             if constexpr (GATE) rz.place(p.z, pl, p.D, tw, t1);
 #pragma unroll
             for (int k = 0; k < TT; ++k) rx.fetch(k, db), rr.fetch(k, db), ri.fetch(k, db);
-            if constexpr (GATE) {
-#pragma unroll
-                for (int k = 0; k < TT; ++k) rz.fetch(k, db);
-            }
             const Gates<1> gates(p, d);
 #pragma unroll
             for (int k = 0; k < TT; ++k) {
@@ -107,6 +103,12 @@ template <int DT, bool GATE, int AUX, int WAVES> __global__ __launch_bounds__(64
             }
             // a NaN that came in must not look like a word that is not there yet
             if (act) tell(p.told + slot * D + d, hh, pp == pp ? __float_as_uint(pp) : 0x7fc00000u);
+        }
+        if constexpr (GATE) {       // late, in the registers that x, r and i have left ([8 x 2048, 2048] bf16 75 us, asked for with them 78)
+            if (left > 0) {
+#pragma unroll
+                for (int k = 0; k < TT; ++k) rz.fetch(k, db);
+            }
         }
         if (pl.j > 0) {
             // this wave's share of the group's chunks in front, and in wave 0 the state that enters the group
