@@ -37,8 +37,8 @@ __global__ __launch_bounds__(256) void k_recur_clear(RecurParams p) {
 // are NaN. A word holds value and mark, so no fence is needed.
 // [8192, 2048] bf16: 42 us, 4.0 TB/s, vector units 45 % busy; in two passes over the inputs 82. What is left is that a block loads, joins,
 // waits and walks one after the other, with three blocks of 79 registers on a CU.
-// AUX: the policy of its accesses: past the last-level cache where the call is larger than it (bf16, D = 2048: [8 x 2048] 75 us, 78 without,
-// [1 x 8192], which is smaller, 44.6 and 46.2, but what reads the outputs next finds them there).
+// AUX: the policy of its accesses: past the last-level cache where the call is larger than it (bf16, D = 2048: [8 x 2048] 75 us, 79 through it,
+// [1 x 8192], which is smaller, 43 and 46, but what reads the outputs next finds them there).
 template <int DT, bool GATE, int AUX, int WAVES> __global__ __launch_bounds__(64 * WAVES, 6) void k_recur(RecurParams p) {
     typedef raw_t<DT> raw;
     constexpr int CH = WAVES * TT, GROUP = WAVES * EACH;

@@ -49,6 +49,22 @@ def test_more_threads_than_a_grid_holds(fn):
     assert _query(fn, n=1, S=1 << 26, D=64)[0] == _lib.MIMO_OK
 
 
+@pytest.mark.parametrize("n,S,D,packed", [(4, 4096, 2048, False), (1, 128, 64, False), (1, 129, 64, False), (5, 64, 10, False), (5, 65, 10, False), (9, 16, 70, False),
+                                          (9, 17, 70, False), (1, 1, 1, False), (2000, 16000, 2048, True), (160, 16000, 1025, True), (1, 16, 8, True), (1, 5, 8, True),
+                                          (3, 64, 8, True), (2, 200, 33, True), (70, 4, 8, True)])
+def test_workspace_of_the_recurrence_is_what_the_header_states(n, S, D, packed):
+    cu = 1 << 20 if packed else None
+    short = packed and S // n < 64
+    for fn, C in (("mamba_recur_fwd", 32 if short else 64 if packed else 128), ("mamba_recur_bwd", 16 if short else 32 if packed else 64)):
+        chunks = S // C + n + 1 if packed else n * -(-S // C)
+        if fn.endswith("fwd"):
+            want, slack = (8 * D * (chunks + chunks // (C // 4)), 8 * D + 256 * (-(-D // 64) + 3)) if S > C else (0, 0)
+        else:
+            want, slack = 12 * D * chunks * (2 if S > C else 1), 4 * 256
+        status, got = _query(fn, n=n, S=S, D=D, cu_seqlens=cu)
+        assert status == _lib.MIMO_OK and want <= got <= want + slack, (fn, want, got)
+
+
 Z, F16, I32, U8 = torch.zeros, torch.float16, torch.int32, torch.uint8
 
 

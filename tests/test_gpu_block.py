@@ -543,6 +543,63 @@ def test_recur_larger_than_the_cache(dtype, D, S, gate):
         assert _same(whole.out[k:k + 1], one.out) and _same(whole.state[k:k + 1], one.state), k
 
 
+@pytest.mark.parametrize("packed", [False, True])
+def test_recur_beyond_32_bits(packed):
+    """More than 2^31 elements in a tensor: the last sequence gets the bits that a call for it alone gets."""
+    g = torch.Generator(device="cuda").manual_seed(53)
+    S, D = 1 << 20, 1032
+    new = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x = {k: torch.empty(2, S, D, dtype=BF, device="cuda") for k in ("x", "r", "i", "z")}
+    for t in x.values():
+        assert t.numel() > 1 << 31
+        t[0] = 0.5
+        t[1].view(64, S // 64, D)[:] = new(S // 64, D)
+    dout = x["z"]                   # any tensor of its size does
+    par, init = dict(decay=new(D) - 3, r_bias=new(D)), new(2, D)
+    cu = torch.tensor([0, S, 2 * S], dtype=torch.int32, device="cuda") if packed else None
+    flat = (lambda t: t.view(-1, D)) if packed else (lambda t: t)
+    whole = {k: flat(t) for k, t in x.items()}
+    one = {k: t[1] if packed else t[1:] for k, t in x.items()}
+    args = dict(cu_seqlens=cu), dict(cu_seqlens=None if cu is None else cu[:2].contiguous())
+    a = m.mamba_recur_fwd(**whole, **par, initial_state=init, return_state=True, **args[0])
+    b = m.mamba_recur_fwd(**one, **par, initial_state=init[1:], return_state=True, **args[1])
+    assert _same(a.out.view(2, S, D)[1], b.out.view(S, D)) and _same(a.state[1:], b.state)
+    del a, b
+    a = m.mamba_recur_bwd(flat(dout), **whole, **par, initial_state=init, dstate=init, **args[0])
+    b = m.mamba_recur_bwd(one["z"], **one, **par, initial_state=init[1:], dstate=init[1:], **args[1])
+    for k in ("dx", "dr", "di", "dz"):
+        assert _same(getattr(a, k).view(2, S, D)[1], getattr(b, k).view(S, D)), k
+    assert _same(a.dinitial_state[1:], b.dinitial_state)
+
+
+def test_recur_step_from_a_pool_beyond_32_bits():
+    g = torch.Generator(device="cuda").manual_seed(55)
+    D = 1032
+    slots = (1 << 31) // D + 3
+    pool = torch.empty(slots, D, device="cuda")
+    pool[-1].normal_(generator=g)
+    alone = pool[-1:].clone()
+    x = [torch.randn(1, D, generator=g, device="cuda").to(HF) for _ in range(4)]
+    decay = torch.randn(D, generator=g, device="cuda")
+    y = m.mamba_recur_step(x[0], x[1], x[2], pool, decay, z=x[3], state_indices=torch.tensor([slots - 1], dtype=torch.int32).cuda())
+    assert _same(y, m.mamba_recur_step(x[0], x[1], x[2], alone, decay, z=x[3])) and _same(pool[-1], alone[0])
+
+
+def test_add_norm_beyond_32_bits():
+    g = torch.Generator(device="cuda").manual_seed(54)
+    D, rows = 1032, (1 << 21) + 300
+    x, res, w = torch.zeros(rows, D, dtype=BF, device="cuda"), torch.zeros(rows, D, dtype=BF, device="cuda"), torch.rand(D, generator=g, device="cuda") + 0.5
+    assert x.numel() > 1 << 31
+    for t in (x, res):
+        t[-300:] = torch.randn(300, D, generator=g, device="cuda")
+    for kw in ({}, dict(out_dtype=E4, block=64)):
+        a, b = m.mamba_add_norm_fwd(x, w, res, **kw), m.mamba_add_norm_fwd(x[-300:].clone(), w, res[-300:].clone(), **kw)
+        assert _same(a.sum[-300:], b.sum) and torch.equal(a.out[-300:].view(torch.uint8), b.out.view(torch.uint8))
+        assert a.scale is None or _same(a.scale[-300:], b.scale)
+    p, q = m.mamba_add_norm_bwd(x, res, w, x), m.mamba_add_norm_bwd(x[-300:].clone(), res[-300:].clone(), w, x[-300:].clone())
+    assert _same(p.dx[-300:], q.dx)
+
+
 @pytest.mark.parametrize("D,S", [(8, 1 << 14)])
 def test_long_sequence_of_few_channels(D, S):
     """Many chunks of one tile, against the sequential definition."""
