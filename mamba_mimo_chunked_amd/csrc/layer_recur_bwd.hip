@@ -9,6 +9,9 @@ namespace layer {
 namespace {
 
 constexpr int TT = 8;               // tokens of a wave
+// Just below the root of fp32's smallest normal number: below 2^-126 the hardware's root counts 1 - a^2 as zero, while l, half of it, may still be
+// there. l / e, in truth e / 2, is taken with at least this e, so it is off by 1e-19 at most.
+constexpr float LEAST_ROOT = 1e-19f;
 
 // Two halves are split where they are used: else the compiler holds them in a register each and lacks twelve ([4 x 4096, 2048] fp16: 200 us, 277 without).
 template <int DT, int VC> __device__ __forceinline__ void unpack_late(Pack<DT, VC> x, float (&y)[VC]) {
@@ -270,8 +273,8 @@ template <int DT, int VC, bool GATE, int AUX, int WAVES> __global__ __launch_bou
 #pragma unroll
             for (int v = 0; v < VC; ++v) {
                 const float l2 = k.l2[t][v], si = k.si[t][v], e = k.e[t][v], hp = k.b[t][v], a = exp2_hw(l2);
-                // l / e, which is zero where nothing enters
-                const float part = l2 * __builtin_amdgcn_rcpf(__builtin_fmaxf(e, 1e-30f));
+                // l / e, which vanishes with e
+                const float part = l2 * __builtin_amdgcn_rcpf(__builtin_fmaxf(e, LEAST_ROOT));
                 g[v] += c[v];
                 const float ga = a * g[v], u = si * fx[v], du = g[v] * e, dgate = du * u;
                 W[v] = ga * __builtin_fmaf(l2, hp, -part * (a * u));        // times log2(e)

@@ -1,0 +1,36 @@
+"""The gated linear recurrence on the GPU at the ends of its parameters' range, with tokens far apart, and with what its forward
+pass and its special values must not mix: stale workspaces, calls at once, sequences of a packed batch."""
+
+import pytest
+import torch
+
+import mamba_mimo_chunked_amd as m
+
+from . import _block_ref as R
+from .test_gpu_block import _recur_inputs, _reference
+from .test_gpu_layer import _gen, _need_gpu, _rows, _same  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+BF, HF, FF = torch.bfloat16, torch.float16, torch.float32
+
+
+def _params(x, decay, r_bias=None):
+    x["decay"] = torch.tensor(decay, device="cuda")
+    if r_bias is not None:
+        x["r_bias"] = torch.tensor(r_bias, device="cuda")
+    return x
+
+
+# ---------------------------------------------------------------- decays near the smallest number
+@pytest.mark.parametrize("S", [24, 200])
+@pytest.mark.parametrize("dtype", [FF, BF])
+def test_recur_of_steps_below_the_smallest_number(dtype, S):
+    """A decay at the edge of fp32's range, or gates so shut, that 1 - exp(2 l) is below it while l is not yet zero: what it gives the
+    gradients of r and decay is the limit's, not l over some constant."""
+    g = _gen(S + 1)
+    decay = [-87.0, -87.0, -87.0, -87.0, -86.0, -80.0, -5.0, 0.0]
+    x = _params(_recur_inputs(g, (2, S), 2, 8, dtype), decay, [-3.0, -5.0, -9.0, 0.0, -6.0, -9.0, -86.0, -85.0])
+    dout, ds = _rows(g, (2, S), 8, dtype, False), torch.randn(2, 8, generator=g).cuda()
+    gr = m.mamba_recur_bwd(dout, **x, dstate=ds)
+    ref, bound = _reference(x, None, 8.0, dout, ds)
+    R.check(gr._asdict(), ref, bound, (dtype, S))
