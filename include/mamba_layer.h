@@ -230,8 +230,8 @@ mimo_status mamba_norm_bwd(const mamba_norm_bwd_args *args, void *stream);
  * from h = initial_state (zeros where NULL); state (optional) receives the last h.
  * Long sequences are cut into chunks whose factors exp(l) are multiplied before they
  * meet a state: a product below fp32's range turns an infinite state into NaN. A decay
- * below -87 counts as none (its softplus is below fp32's range): nothing is forgotten or
- * enters.
+ * below -87 counts as none (its softplus is below fp32's range), and so does rate *
+ * softplus(decay) below 8e-39: nothing is forgotten or enters.
  *   x, r, i, z, out [.., D]; decay, r_bias, i_bias [D] (the biases optional); states
  *   [n, D] fp32. rate is not negative; rate * softplus(decay) beyond 1e29 counts as
  *   some 1e30. Token strides: 0 to MAMBA_RECUR_MAX_STRIDE elements (forward and backward).

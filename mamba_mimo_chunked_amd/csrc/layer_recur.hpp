@@ -83,6 +83,8 @@ __device__ __forceinline__ float root(float x) { return __builtin_amdgcn_sqrtf(x
 
 // From here on a step keeps nothing, and the products of l in the gradients still stay in range.
 constexpr float FASTEST = 1e30f;
+// Below it a channel counts as one that forgets nothing: what enters it in a token is below 2e-19 of x, and from 2e-39 down ln(2) / speed is infinite.
+constexpr float SLOWEST = 0x1p-126f;
 // a lane's parameters: -rate softplus(decay) log2(e), and the biases times -log2(e)
 template <int VC> struct Gates {
     float speed[VC], rb[VC], ib[VC];
@@ -94,7 +96,7 @@ template <int VC> struct Gates {
 #pragma unroll
         for (int v = 0; v < VC; ++v) {
             const float s = p.rate * (LOG2E * softplus(p.decay[d + v]));
-            speed[v] = s > FASTEST ? -FASTEST : -s;
+            speed[v] = s > FASTEST ? -FASTEST : s < SLOWEST ? 0.f : -s;
             rb[v] = p.rb ? -LOG2E * p.rb[d + v] : 0.f;
             ib[v] = p.ib ? -LOG2E * p.ib[d + v] : 0.f;
         }

@@ -22,6 +22,24 @@ def _params(x, decay, r_bias=None):
 
 
 # ---------------------------------------------------------------- decays near the smallest number
+@pytest.mark.parametrize("S", [20, 200])
+@pytest.mark.parametrize("rate,decay", [(0.05, [-86.9, -87.0, -87.3, -85.0, -84.0, -80.0, 0.0]), (2.0 ** -127, [-3.0, 0.0, 5.0, 100.0, 1e10, -20.0, 1e30]),
+                                        (2.0 ** -149, [0.0, 3.0, 1e4, 1e20, 1e36, 1.0, -5.0]), (0.0, [0.0, -50.0, 20.0, 1e30, -100.0, 1.0, 3.0])])
+def test_recur_of_the_smallest_rates(rate, decay, S):
+    """rate softplus(decay) around 2^-126 and below it: nothing is forgotten or enters, and all gradients are finite and within the
+    reference's bound."""
+    g = _gen(S)
+    D = len(decay)
+    x = _params(_recur_inputs(g, (2, S), 2, D, FF), decay)
+    dout, ds = _rows(g, (2, S), D, FF, False), torch.randn(2, D, generator=g).cuda()
+    o = m.mamba_recur_fwd(**x, rate=rate, return_state=True)
+    gr = m.mamba_recur_bwd(dout, **x, dstate=ds, rate=rate)
+    for k, t in {**gr._asdict(), "out": o.out, "state": o.state}.items():
+        assert torch.isfinite(t).all(), k
+    ref, bound = _reference(x, None, rate, dout, ds)
+    R.check({**gr._asdict(), "out": o.out, "state": o.state}, ref, bound, (rate, decay))
+
+
 @pytest.mark.parametrize("S", [24, 200])
 @pytest.mark.parametrize("dtype", [FF, BF])
 def test_recur_of_steps_below_the_smallest_number(dtype, S):
