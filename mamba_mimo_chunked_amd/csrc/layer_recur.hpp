@@ -81,7 +81,7 @@ __device__ __forceinline__ void keep_and_enter(float l2, float& a, float& e2) {
 }
 __device__ __forceinline__ float root(float x) { return __builtin_amdgcn_sqrtf(x); }
 
-// From here on a step keeps nothing, and the products of l in the gradients still stay in range.
+// From here on a step keeps nothing, and l itself stays in range.
 constexpr float FASTEST = 1e30f;
 // Below it a channel counts as one that forgets nothing: what enters it in a token is below 2e-19 of x, and from 2e-39 down ln(2) / speed is infinite.
 constexpr float SLOWEST = 0x1p-126f;

@@ -277,7 +277,8 @@ template <int DT, int VC, bool GATE, int AUX, int WAVES> __global__ __launch_bou
                 const float part = l2 * __builtin_amdgcn_rcpf(__builtin_fmaxf(e, LEAST_ROOT));
                 g[v] += c[v];
                 const float ga = a * g[v], u = si * fx[v], du = g[v] * e, dgate = du * u;
-                W[v] = ga * __builtin_fmaf(l2, hp, -part * (a * u));        // times log2(e)
+                // l times a log2(e), before it meets a state: where a token keeps nothing that is zero, and l h may be beyond fp32's range
+                W[v] = __builtin_fmaf(ga * l2, hp, -(ga * part) * (a * u));
                 c[v] = ga;
                 ox[v] = du * si;
                 oi[v] = __builtin_fmaf(-dgate, si, dgate);

@@ -52,3 +52,23 @@ def test_recur_of_steps_below_the_smallest_number(dtype, S):
     gr = m.mamba_recur_bwd(dout, **x, dstate=ds)
     ref, bound = _reference(x, None, 8.0, dout, ds)
     R.check(gr._asdict(), ref, bound, (dtype, S))
+
+
+@pytest.mark.parametrize("size", [1e9, 1e12, 1e30, 3e38])
+@pytest.mark.parametrize("S", [8, 150])
+def test_recur_forgets_states_of_any_size(size, S):
+    """Where a token keeps nothing (exp(l) = 0), a state of any size in front of it has no part in the gradients."""
+    g = _gen(S + 2)
+    decay = [3e38, 1e31, 1e30, 1e20, 1e6]
+    x = _params(_recur_inputs(g, (2, S), 2, 5, FF), decay, [0.0] * 5)
+    x["initial_state"] = size * x["initial_state"].sign()
+    dout, ds = _rows(g, (2, S), 5, FF, False), torch.randn(2, 5, generator=g).cuda()
+    o, gr = m.mamba_recur_fwd(**x, return_state=True), m.mamba_recur_bwd(dout, **x, dstate=ds)
+    y = {**x, "initial_state": torch.zeros(2, 5, device="cuda")}
+    p, gp = m.mamba_recur_fwd(**y, return_state=True), m.mamba_recur_bwd(dout, **y, dstate=ds)
+    assert _same(o.out, p.out) and _same(o.state, p.state)
+    for k, a, b in zip(gr._fields, gr, gp):
+        assert torch.equal(a, b), k         # zeros may differ in sign
+        assert torch.isfinite(a).all(), k
+    for t in (gr.dr, gr.ddecay, gr.dr_bias, gr.dinitial_state):
+        assert not t.any()
