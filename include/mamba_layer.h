@@ -234,7 +234,8 @@ mimo_status mamba_norm_bwd(const mamba_norm_bwd_args *args, void *stream);
  * softplus(decay) below 8e-39: nothing is forgotten or enters.
  *   x, r, i, z, out [.., D]; decay, r_bias, i_bias [D] (the biases optional); states
  *   [n, D] fp32. rate is not negative; rate * softplus(decay) beyond 1e29 counts as
- *   some 1e30. Token strides: 0 to MAMBA_RECUR_MAX_STRIDE elements (forward and backward).
+ *   some 1e30. Token strides: 0 to MAMBA_RECUR_MAX_STRIDE elements (forward and backward;
+ *   not used where S = 1).
  * Blocks of the forward pass wait for those in front of them, with a limit: where
  * cu_seqlens decreases, a call may take some tenths of a second and leave NaN.
  * Workspace, in bytes, with chunks of C tokens: dense 128 forward and 64 backward, packed

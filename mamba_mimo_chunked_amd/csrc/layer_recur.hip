@@ -247,7 +247,7 @@ struct FwdPlan {
 mimo_status plan_fwd(const mamba_recur_fwd_args* a, FwdPlan* pl) {
     if (a == nullptr) return bad("args must not be NULL");
     mimo_status s = check_recur(a->n, a->S, a->D, a->dtype, a->rate);
-    if (s != MIMO_OK || (s = check_strides({&a->x, &a->r, &a->i, &a->z})) != MIMO_OK) return s;
+    if (s != MIMO_OK || (s = check_strides(a->S, {&a->x, &a->r, &a->i, &a->z})) != MIMO_OK) return s;
     const bool packed = a->cu_seqlens != nullptr;
     pl->tiles = (unsigned)((a->D + 63) / 64);
     pl->waves = waves_of(packed, a->n, a->S, TT);

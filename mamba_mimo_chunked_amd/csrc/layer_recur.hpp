@@ -172,8 +172,9 @@ inline mimo_status check_recur(int64_t n, int64_t S, int64_t D, int dtype, float
     if (n * S > (int64_t)1 << 40) return unsupported("too many tokens");
     return MIMO_OK;
 }
-// the rows of a tile of tokens lie within 32 bits of its first
-inline mimo_status check_strides(std::initializer_list<const mamba_rows*> rows) {
+// the rows of a tile of tokens lie within 32 bits of its first; a single token's stride is not used
+inline mimo_status check_strides(int64_t S, std::initializer_list<const mamba_rows*> rows) {
+    if (S == 1) return MIMO_OK;
     for (const mamba_rows* r : rows)
         if (r->data && (r->token_stride < 0 || r->token_stride > MAMBA_RECUR_MAX_STRIDE)) return unsupported("token strides beyond 2^26 elements");
     return MIMO_OK;

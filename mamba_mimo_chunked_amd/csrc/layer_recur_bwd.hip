@@ -356,7 +356,7 @@ struct BwdPlan {
 mimo_status plan_bwd(const mamba_recur_bwd_args* a, BwdPlan* pl) {
     if (a == nullptr) return bad("args must not be NULL");
     mimo_status s = check_recur(a->n, a->S, a->D, a->dtype, a->rate);
-    if (s != MIMO_OK || (s = check_strides({&a->dout, &a->x, &a->r, &a->i, &a->z})) != MIMO_OK) return s;
+    if (s != MIMO_OK || (s = check_strides(a->S, {&a->dout, &a->x, &a->r, &a->i, &a->z})) != MIMO_OK) return s;
     const bool packed = a->cu_seqlens != nullptr;
     pl->VC = channels_of(a->D, a->dtype, packed, {&a->dout, &a->x, &a->r, &a->i, &a->z}, {a->dx, a->dr, a->di, a->dz});
     pl->tiles = (unsigned)((a->D + 64 * pl->VC - 1) / (64 * pl->VC));

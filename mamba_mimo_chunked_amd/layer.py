@@ -564,8 +564,8 @@ def mamba_norm_bwd(dout, x, weight, bias=None, z=None, *, groups: int = 1, eps: 
 
 # ---------------------------------------------------------------- gated linear recurrence
 def _near(x):
-    """A tensor whose tokens lie near each other: a copy where 2^26 elements or more are between two of them."""
-    return x if x is None or x.stride(-2) <= 1 << 26 else x.contiguous()
+    """A tensor whose tokens lie near each other: a copy where more than 2^26 elements are between two of them."""
+    return x if x is None or x.stride(-2) <= 1 << 26 or x.shape[-2] == 1 else x.contiguous()
 
 
 def _check_recur(x, r, i, decay, r_bias, i_bias, z, rate, dev):

@@ -72,3 +72,25 @@ def test_recur_forgets_states_of_any_size(size, S):
         assert torch.isfinite(a).all(), k
     for t in (gr.dr, gr.ddecay, gr.dr_bias, gr.dinitial_state):
         assert not t.any()
+
+
+# ---------------------------------------------------------------- one token
+@pytest.mark.parametrize("packed", [False, True])
+def test_recur_with_one_token_whose_stride_is_far(packed):
+    """One token of each sequence, in a buffer in which the next one would lie 2^26 elements and more behind it."""
+    g = _gen(61)
+    D, n = 40, 1 if packed else 4
+    x = _recur_inputs(g, (n, 1), n, D, BF)
+    dout = torch.randn(n, 1, D, generator=g).to(BF).cuda()
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda") if packed else None
+    near, far = {}, {}
+    for k, t in {**x, "dout": dout}.items():
+        if t.dim() == 3:
+            near[k] = t[0] if packed else t
+            far[k] = t.as_strided((1, D), ((1 << 26) + 8, 1)) if packed else t.as_strided((n, 1, D), (D, (1 << 26) + 8, 1))
+        else:
+            near[k] = far[k] = t
+    a, b = (m.mamba_recur_fwd(**{k: v for k, v in y.items() if k != "dout"}, cu_seqlens=cu, return_state=True) for y in (near, far))
+    assert _same(a.out, b.out) and _same(a.state, b.state)
+    for p, q in zip(m.mamba_recur_bwd(**near, cu_seqlens=cu), m.mamba_recur_bwd(**far, cu_seqlens=cu)):
+        assert _same(p, q)
