@@ -95,7 +95,7 @@ template <int VC> struct Gates {
     __device__ __forceinline__ Gates(const RecurParams& p, unsigned d) {
 #pragma unroll
         for (int v = 0; v < VC; ++v) {
-            const float s = p.rate * (LOG2E * softplus(p.decay[d + v]));
+            const float s = LOG2E * (p.rate * softplus(p.decay[d + v]));     // in this order: LOG2E * softplus may be infinite, and a rate zero
             speed[v] = s > FASTEST ? -FASTEST : s < SLOWEST ? 0.f : -s;
             rb[v] = p.rb ? -LOG2E * p.rb[d + v] : 0.f;
             ib[v] = p.ib ? -LOG2E * p.ib[d + v] : 0.f;

@@ -54,6 +54,26 @@ def test_recur_of_steps_below_the_smallest_number(dtype, S):
     R.check(gr._asdict(), ref, bound, (dtype, S))
 
 
+@pytest.mark.parametrize("S", [20, 150])
+@pytest.mark.parametrize("rate", [0.0, 2.0 ** -149, 2.0 ** -130, 2.0 ** -100, 1.0])
+def test_recur_of_the_largest_decays(rate, S):
+    """rate softplus(decay) of the largest decays: nothing is forgotten with a rate of zero, and what a small rate leaves of them counts."""
+    g = _gen(S + 3)
+    decay = [3.4e38, 2.4e38, 2.3e38, 1e38, 1.0]
+    x = _params(_recur_inputs(g, (2, S), 2, 5, FF), decay)
+    dout, ds = _rows(g, (2, S), 5, FF, False), torch.randn(2, 5, generator=g).cuda()
+    o, gr = m.mamba_recur_fwd(**x, rate=rate, return_state=True), m.mamba_recur_bwd(dout, **x, dstate=ds, rate=rate)
+    got = {**gr._asdict(), "out": o.out, "state": o.state}
+    for k, t in got.items():
+        assert torch.isfinite(t).all(), k
+    ref, bound = _reference(x, None, rate, dout, ds)
+    R.check(got, ref, bound, rate)
+    s = x["initial_state"].clone()
+    one = {k: x[k][:, 0].contiguous() for k in "xriz"}
+    y = m.mamba_recur_step(state=s, **one, decay=x["decay"], r_bias=x["r_bias"], i_bias=x["i_bias"], rate=rate)
+    assert torch.isfinite(y).all() and _same(y, o.out[:, 0])
+
+
 @pytest.mark.parametrize("size", [1e9, 1e12, 1e30, 3e38])
 @pytest.mark.parametrize("S", [8, 150])
 def test_recur_forgets_states_of_any_size(size, S):
