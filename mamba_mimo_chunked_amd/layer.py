@@ -671,12 +671,12 @@ def _check_stream(name, x, dtype):
     return dtype
 
 
-def _check_add_norm(x, weight, eps, dropout, seed, dev):
+def _check_add_norm(name, x, weight, eps, dropout, seed, dev):
     """Columns, the share dropped of 65536, its seed, the weight."""
     if weight is None:
         _required(weight=weight)
     if x.dim() < 1 or x.numel() == 0:
-        raise ValueError(f"x must have shape [..., D] and not be empty, got {list(x.shape)}")
+        raise ValueError(f"{name} must have shape [..., D] and not be empty, got {list(x.shape)}")
     D = x.shape[-1]
     if D > 16384:
         raise NotImplementedError(f"mamba_add_norm supports at most 16384 channels, got {D}")
@@ -715,7 +715,7 @@ def mamba_add_norm_fwd(x, weight, residual=None, *, eps: float = 1e-5, dropout: 
     magnitude / 448 or 127, rounded to nearest. A block with a value that is not finite has the scale NaN."""
     dev = _device("mamba_add_norm_fwd", "x", x)
     code = _data_dtype("x", x)
-    D, drop, seed, weight = _check_add_norm(x, weight, eps, dropout, seed, dev)
+    D, drop, seed, weight = _check_add_norm("x", x, weight, eps, dropout, seed, dev)
     dtype = x.dtype
     if residual is not None:
         stream = _check_stream("the dtype of residual", dtype, residual.dtype)
@@ -758,7 +758,7 @@ def mamba_add_norm_bwd(dout, sum, weight, dsum=None, *, eps: float = 1e-5, dropo
         _required(sum=sum)
     dev = _device("mamba_add_norm_bwd", "dout", dout)
     code = _data_dtype("dout", dout)
-    D, drop, seed, weight = _check_add_norm(dout, weight, eps, dropout, seed, dev)
+    D, drop, seed, weight = _check_add_norm("dout", dout, weight, eps, dropout, seed, dev)
     stream = _check_stream("the dtype of sum", dout.dtype, sum.dtype)
     _fits("sum", sum, dout.shape, stream, dev)
     gr, vr, sr = _row_view(dout, D), _row_view(sum, D), None
