@@ -237,7 +237,8 @@ mimo_status mamba_norm_bwd(const mamba_norm_bwd_args *args, void *stream);
  *   some 1e30. Token strides: 0 to MAMBA_RECUR_MAX_STRIDE elements (forward and backward;
  *   not used where S = 1).
  * Blocks of the forward pass wait for those in front of them, with a limit: where
- * cu_seqlens decreases, a call may take some tenths of a second and leave NaN.
+ * cu_seqlens decreases, a call may take some tenths of a second and leave NaN; its
+ * status, given before it runs, is MIMO_OK. Nothing else reaches the limit.
  * Workspace, in bytes, with chunks of C tokens: dense 128 forward and 64 backward, packed
  * 64 and 32, or 32 and 16 where S / n < 64; n ceil(S / C) chunks, packed S / C + n + 1.
  *   forward: 8 D for each chunk and for every C / 4 of them, none where S <= C
@@ -308,7 +309,8 @@ mimo_status mamba_recur_step(const mamba_recur_step_args *args, void *stream);
  *   v = dropout(x) + residual (or dropout(x));  y = v / sqrt(mean(v^2) + eps) * weight
  * The norm takes v before it is rounded to `sum`. The stream (residual, sum, and their
  * gradients) has the data dtype, or fp32 where wide is set. A square of v beyond fp32's
- * range (|v| > 1.8e19) makes the row's norm infinite.
+ * range (|v| > 1.8e19) makes the row's norm infinite; with eps = 0, a row of zeros, or of
+ * squares below that range, has the norm zero and gives NaN and infinities.
  *
  * Dropout: an element is dropped, whatever its value, where its 16 bits are below
  * `drop`, and multiplied by 65536 / (65536 - drop) elsewhere. The bits of the columns

@@ -30,12 +30,13 @@ __global__ __launch_bounds__(256) void k_recur_clear(RecurParams p) {
 // it joins its tokens' steps, tells the joined step (last state from zero, product of a; one word of 64 bits a channel) to the
 // chunks behind it, joins those of the chunks in front, and walks its tokens from there. The chunks of a sequence are joined in
 // groups of WAVES * EACH: a chunk looks at those of its group, and at the state that the last chunk of the group in front tells. The order in
-// which steps are joined is fixed, so equal inputs give equal bits.
+// which steps are joined is fixed, so equal inputs give equal bits. (Scans in one pass whose blocks look back: D. Merrill and M. Garland, "Single-pass
+// parallel prefix scan with decoupled look-back", 2016.)
 // Every wait ends: a block takes the next chunk of its tile from a counter, so that whatever it waits for belongs to a block that runs
 // already, and a chunk's step is told before its block waits, a group's state after waiting for lower chunks alone. cu_seqlens that
 // decrease may leave a word that nobody tells: POLLS ends the first such wait, its mark behind the counters all others, and outputs
-// are NaN. A word holds value and mark, so no fence is needed.
-// [8192, 2048] bf16: 42 us, 4.0 TB/s, vector units 45 % busy; in two passes over the inputs 82. What is left is that a block loads, joins,
+// are NaN (the host hears nothing of it: the call has returned). A word holds value and mark, so no fence is needed.
+// [8192, 2048] bf16: 42 us, 4.0 TB/s, vector units 46 % busy; in two passes over the inputs 82. What is left is that a block loads, joins,
 // waits and walks one after the other, with three blocks of 79 registers on a CU.
 // AUX: the policy of its accesses: past the last-level cache where the call is larger than it (bf16, D = 2048: [8 x 2048] 75 us, 79 through it,
 // [1 x 8192], which is smaller, 43 and 46, but what reads the outputs next finds them there).

@@ -66,8 +66,8 @@ __device__ __forceinline__ Place place_by_wave(const Seqs& q, int slot) {
 __device__ __forceinline__ long recur_row(const Seqs& q, const Place& pl) { return q.cu ? (long)pl.row0 : (long)pl.i * q.S; }
 
 // a = 2^l2 and 1 - a^2. Near a = 1 the difference would leave few bits (and e, of which tokens a slow channel takes in little,
-// with them): there the series of -expm1(y), y = 2 ln a, to y^6 (its next term is below 2^-25 of the sum for |y| < 1/4); elsewhere
-// one rounding, and a's error, which the difference enlarges five times at most.
+// with them): there the series of -expm1(y), y = 2 ln a, to y^6 (its next term is below 2^-24 of the sum for |y| < 1/4); elsewhere
+// one rounding, and a's error, which the difference enlarges 2 a^2 / (1 - a^2) times, some seven at most.
 __device__ __forceinline__ void keep_and_enter(float l2, float& a, float& e2) {
     a = exp2_hw(l2);
     const float y = l2 * (2.f * LN2);
@@ -191,6 +191,9 @@ template <int DT> bool passes_by(const Seqs& q, int D, int streams) {
 //   mean length     8               32              100             200             400             dense [1 x 8192]
 //   forward     555 312 203     192 131 110     120  97  97     104  91  97      94  88  96      47  47  61
 //   backward    877 547 418     372 283 257     260 225 227     234 217 222     215 206 219     102 109 118
+// The mean counts empty sequences too, which a batch that is padded to a fixed number of them has. The same tokens in 8 long sequences
+// (forward, backward; one long sequence): 8 in all 83, 201 (82, 208); 250, the last by 4 waves, 95, 222 (92, 273); 251, by 2, 99, 228 (110,
+// 280); 2000 153, 351 (164, 414): a chunk's place for each empty sequence costs more than the waves that its mean brings.
 inline int waves_of(bool packed, int64_t n, int64_t S, int TT) {
     if (packed) return S / n < 64 ? 2 : 4;
     return S <= 2 * TT ? 2 : S <= 4 * TT ? 4 : 8;

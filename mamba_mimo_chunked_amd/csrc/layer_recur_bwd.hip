@@ -94,7 +94,7 @@ template <int VC, int WAVES> struct Join {
     }
 };
 
-// One channel a lane, 52 registers: 32 waves a CU hide its loads ([4 x 4096, 2048] bf16 74 us, 4.6 TB/s, vector units 64 % busy). Its loads stay in the
+// One channel a lane, 52 registers: 32 waves a CU hide its loads ([4 x 4096, 2048] bf16 72 us, 4.7 TB/s, vector units 65 % busy). Its loads stay in the
 // last-level cache for k_recur_bwd.
 template <int DT, bool GATE, int WAVES> __global__ __launch_bounds__(64 * WAVES) void k_recur_agg(RecurParams p) {
     constexpr int CHUNK = WAVES * TT;
@@ -181,7 +181,7 @@ __global__ __launch_bounds__(64 * RSPAN_WAVES) void k_recur_carry(RecurParams p)
 }
 
 // AUX: the policy of its accesses, the last ones to the inputs. The chunks come from the last to the first: the inputs that the
-// aggregates read last are still in the last-level cache. [4 x 4096, 2048] bf16: 127 to 135 us for 604 MB, vector units 68 % busy; two channels a lane
+// aggregates read last are still in the last-level cache. [4 x 4096, 2048] bf16: 128 to 132 us for 604 MB, vector units 67 % busy; two channels a lane
 // where 4 bytes allow it ([16384, 1000] 147 us, with one 175).
 template <int DT, int VC, bool GATE, int AUX, int WAVES> __global__ __launch_bounds__(64 * WAVES, 4) void k_recur_bwd(RecurParams p) {
     typedef raw_t<DT> raw;
